@@ -16,3 +16,9 @@ from .gret import (  # noqa: F401
     gret_prefill_resume, gret_debug_inject_timeout, gret_set_gate_profile_events,
     gret_prefill_varlen_workspace_size, gret_prefill_varlen_launches,
 )
+from .block import (  # noqa: F401
+    Activation, gret_residual_norm, gret_selective_scan, gret_selective_scan_varlen,
+    gret_selective_scan_varlen_workspace_size, gret_selective_scan_workspace_size, gret_selective_step,
+    gret_short_conv, gret_short_conv_step, gret_short_conv_varlen, residual_norm, selective_scan,
+    selective_scan_varlen, selective_step, short_conv, short_conv_step, short_conv_varlen,
+)

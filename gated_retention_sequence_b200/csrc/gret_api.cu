@@ -10,6 +10,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "gret_block.cuh"
 #include "gret_common.cuh"
 
 namespace gret {
@@ -37,25 +38,6 @@ int take_injected_timeout() {
     while (n > 0 && !g_inject_timeouts.compare_exchange_weak(n, n - 1)) {
     }
     return n > 0 ? 1 : 0;
-}
-
-// Device status word and SM count of the current device (looked up once per
-// device, with that device current).
-bool device_info(unsigned int** status, int* num_sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
-    std::lock_guard<std::mutex> lock(g_mu);
-    if (!g_status_ptr[dev]) {
-        void* p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return false;
-        int sms = 0;
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
-        g_status_ptr[dev] = static_cast<unsigned int*>(p);
-        g_num_sms[dev] = sms;
-    }
-    if (status) *status = g_status_ptr[dev];
-    if (num_sms) *num_sms = g_num_sms[dev];
-    return true;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -102,6 +84,26 @@ gret_path select_path(int B, int H, int N, int dk, int dv, int chunk, gret_dtype
 }
 
 }  // namespace
+
+// Device status word and SM count of the current device (looked up once per
+// device, with that device current).
+bool device_info(unsigned int** status, int* num_sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!g_status_ptr[dev]) {
+        void* p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return false;
+        int sms = 0;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
+        g_status_ptr[dev] = static_cast<unsigned int*>(p);
+        g_num_sms[dev] = sms;
+    }
+    if (status) *status = g_status_ptr[dev];
+    if (num_sms) *num_sms = g_num_sms[dev];
+    return true;
+}
+
 }  // namespace gret
 
 using namespace gret;

@@ -1,0 +1,203 @@
+// Operators of the selective state space block (internal header): the short
+// causal convolution, the selective scan and the residual norm.
+//
+// Tokens come as rows.  A uniform batch has B sequences of N rows each; a
+// packed one has `total` rows, cut by cu_seqlens (device).  Either way the
+// kernels walk slots: a slot is one segment of at most `seg` consecutive tokens
+// of one sequence.  Sequence b's slots start at b * ceil(N / seg) in a uniform
+// batch and at floor(cu_seqlens[b] / seg) + b in a packed one: that leaves
+// every sequence room for ceil(len / seg) slots (at least one, so an empty
+// sequence has a slot that hands its state on), and total / seg + B slots hold
+// them all, without a plan and without a host copy of the offsets.
+#pragma once
+
+#include "gret_common.cuh"
+
+namespace gret {
+
+// Device status word and SM count of the current device.
+bool device_info(unsigned int** status, int* num_sms);
+
+struct Rows {
+    const int* cu;      // device offsets [B + 1], or null for a uniform batch
+    int B, N;           // sequences; tokens of each, or the longest
+    int total;          // rows of a packed batch
+    int seg;            // tokens of a slot
+};
+
+inline long long slots_of(const Rows& r) {
+    return r.cu ? (long long)r.total / r.seg + r.B : (long long)r.B * ((r.N + r.seg - 1) / r.seg);
+}
+
+struct Slot {
+    int b;              // sequence, or -1 for a slot that holds nothing
+    int s;              // segment of the sequence
+    int segs;           // segments the sequence has (0 when it is empty)
+    int first;          // first token of the segment within its sequence
+    int len;            // tokens of the segment
+    int seq_len;        // tokens of the sequence
+    long long row0;     // row of the sequence's first token
+};
+
+__device__ __forceinline__ long long slot_start(const Rows& r, int b) {
+    if (!r.cu) return (long long)b * ((r.N + r.seg - 1) / r.seg);
+    int c = r.cu[b];
+    c = c < 0 ? 0 : (c > r.total ? r.total : c);
+    return (long long)(c / r.seg) + b;
+}
+
+// The segment a slot holds.  All 32 lanes call it together: in a packed batch
+// they search the offsets 32 at a time.  Offsets that are not in order give
+// slots without tokens or rows that another slot has too, never a row outside
+// the tensors (packed_range clamps both ends).
+__device__ __forceinline__ Slot find_slot(const Rows& r, int slot) {
+    Slot f;
+    f.b = -1; f.s = 0; f.segs = 0; f.first = 0; f.len = 0; f.seq_len = 0; f.row0 = 0;
+    if (!r.cu) {
+        const int per = (r.N + r.seg - 1) / r.seg;
+        f.b = slot / per;
+        f.s = slot - f.b * per;
+        f.segs = per;
+        f.seq_len = r.N;
+        f.row0 = (long long)f.b * r.N;
+    } else {
+        const int lane = threadIdx.x & 31;
+        int lo = 0, n = r.B;
+        while (true) {
+            const int step = (n + 31) / 32;
+            const int at = lo + lane * step;
+            const bool before = at < lo + n && slot_start(r, at) <= slot;
+            const int hits = __popc(__ballot_sync(0xffffffffu, before));
+            if (hits == 0) return f;
+            lo += (hits - 1) * step;
+            n = min(step, n - (hits - 1) * step);
+            if (n <= 1 || step == 1) break;
+        }
+        int row0, len;
+        packed_range(r.cu, lo, r.total, row0, len);
+        len = min(len, r.N);
+        f.s = (int)(slot - slot_start(r, lo));
+        f.segs = (len + r.seg - 1) / r.seg;
+        if (f.s < 0 || f.s >= max(f.segs, 1)) return f;
+        f.b = lo;
+        f.seq_len = len;
+        f.row0 = row0;
+    }
+    f.first = f.s * r.seg;
+    f.len = min(r.seg, f.seq_len - f.first);
+    return f;
+}
+
+// Eight consecutive channels: 16 bytes of bf16 or 32 of fp32, 16-byte aligned.
+constexpr int kVec = 8;
+__device__ __forceinline__ void unpack8(const uint4& p, float* v) {
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+    unpack8(*reinterpret_cast<const uint4*>(p), v);
+}
+__device__ __forceinline__ void load8(const float* p, float* v) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+    *reinterpret_cast<uint4*>(p) = pack8(v);
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// d/dv of v sigmoid(v)
+__device__ __forceinline__ float swish_slope(float v, float sig) { return sig * (1.0f + v * (1.0f - sig)); }
+
+struct ConvArgs {
+    const void* x;
+    long long ldx;
+    const float *w, *bias;
+    const void* tail0;
+    void *y, *tail;
+    Rows rows;
+    int D, K;
+    int swish;
+    gret_dtype io;
+};
+cudaError_t launch_short_conv(ConvArgs a, cudaStream_t s);
+cudaError_t launch_short_conv_step(const ConvArgs& a, cudaStream_t s);   // tail0 -> tail, B rows
+
+struct ConvBackwardArgs {
+    ConvArgs f;          // x, w, bias, tail0 of the forward
+    const void *dy, *dtail;
+    void *dx, *dtail0;
+    float *dw, *dbias;
+    void* workspace;
+};
+size_t short_conv_backward_ws_bytes(int B, int N, int D, int K);
+cudaError_t launch_short_conv_backward(ConvBackwardArgs a, cudaStream_t s);
+
+struct ScanArgs {
+    const void *u, *dt, *Bm, *Cm, *z;
+    long long ldu, lddt, ldb, ldc, ldz;
+    const float *A, *skip, *dt_bias, *h0;
+    void* o;
+    float* h;
+    Rows rows;
+    int D, n;
+    gret_dtype io;
+    void* workspace;
+};
+bool selective_states_supported(int n);
+size_t selective_scan_ws_bytes(int B, int N, int total, int D, int n, bool packed, int num_sms);
+int selective_scan_launches(int B, int N, int total, int D, int n, bool packed, int num_sms);
+cudaError_t launch_selective_scan(ScanArgs a, int num_sms, cudaStream_t s);
+cudaError_t launch_selective_step(const ScanArgs& a, int num_sms, cudaStream_t s);   // h0 -> h, B rows
+
+struct ScanBackwardArgs {
+    ScanArgs f;          // inputs of the forward
+    const void* dout;
+    const float* dh_final;
+    void *du, *ddt, *dBm, *dCm, *dz;
+    float *dA, *dskip, *ddt_bias, *dh0;
+};
+size_t selective_backward_ws_bytes(int B, int N, int D, int n, gret_dtype io);
+cudaError_t launch_selective_backward(ScanBackwardArgs a, int num_sms, cudaStream_t s);
+
+struct NormArgs {
+    const void *x, *y, *gate;
+    long long ldx, ldy, ldg;
+    const float *scale, *w_post, *w_next;
+    void *r, *n;
+    long long T;
+    int D;
+    float eps;
+    gret_dtype stream_type, io;
+};
+cudaError_t launch_residual_norm(const NormArgs& a, int num_sms, cudaStream_t s);
+
+struct NormBackwardArgs {
+    NormArgs f;
+    const void *dr, *dn;
+    void *dx, *dy, *dgate;
+    float *dscale, *dw_post, *dw_next;
+    void* workspace;
+};
+constexpr int kNormMaxChannels = 8192;
+size_t residual_norm_backward_ws_bytes(long long T, int D, int num_sms);
+cudaError_t launch_residual_norm_backward(NormBackwardArgs a, int num_sms, cudaStream_t s);
+
+}  // namespace gret

@@ -1,0 +1,211 @@
+// C ABI of the selective state space block's operators: argument validation
+// and launch.  As in gret_api.cu nothing is allocated, copied or read here, and
+// a bad call returns before any launch.
+#include <math.h>
+#include <stdint.h>
+
+#include "gret_block.cuh"
+
+using namespace gret;
+
+namespace {
+
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <typename... P>
+bool all_set(P... p) {
+    return (... && (p != nullptr));
+}
+
+template <typename... P>
+bool all_aligned(P... p) {
+    return (... && aligned(p));
+}
+
+size_t size_of(gret_dtype t) { return t == GRET_BF16 ? 2 : 4; }
+bool type_ok(gret_dtype t) { return t == GRET_F32 || t == GRET_BF16; }
+
+// A row stride: at least the row, rows on 16-byte boundaries.
+bool stride_ok(long long ld, int width, gret_dtype t) {
+    return ld >= width && ld <= (1LL << 40) && ld * (long long)size_of(t) % 16 == 0;
+}
+
+bool overlap(const void* p, const void* q, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + bytes && b < a + bytes;
+}
+
+bool on_device_grid(const Rows& r) { return slots_of(r) <= 0x7fffffffLL; }
+
+constexpr long long kMaxRows = 1LL << 31;
+
+gret_status rows_ok(const Rows& r) {
+    if (r.B <= 0 || r.N <= 0 || (r.cu && r.total <= 0)) return GRET_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(r.cu) & 3u) != 0) return GRET_ERR_INVALID_ARG;
+    if (!r.cu && (long long)r.B * r.N >= kMaxRows) return GRET_ERR_UNSUPPORTED;
+    return GRET_OK;
+}
+
+gret_status done(cudaError_t e) { return e == cudaSuccess ? GRET_OK : GRET_ERR_CUDA; }
+
+cudaStream_t cu_stream(gret_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// ------------------------------------------------------------ short convolution
+gret_status conv_check(const ConvArgs& a) {
+    if (!all_set(a.x, a.w, a.y) || !type_ok(a.io)) return GRET_ERR_INVALID_ARG;
+    if (a.D <= 0 || a.K <= 0) return GRET_ERR_INVALID_ARG;
+    if (gret_status e = rows_ok(a.rows)) return e;
+    if (!all_aligned(a.x, a.w, a.bias, a.tail0, a.y, a.tail)) return GRET_ERR_INVALID_ARG;
+    if (a.D % kVec != 0 || a.K < 2 || a.K > 4) return GRET_ERR_UNSUPPORTED;
+    if (!stride_ok(a.ldx, a.D, a.io)) return GRET_ERR_INVALID_ARG;
+    return GRET_OK;
+}
+
+gret_status conv(const void* x, long long ldx, const float* w, const float* bias, const void* tail0, void* y,
+                 void* tail, Rows rows, int D, int K, gret_dtype io, gret_activation act, gret_stream_t stream) {
+    if (act != GRET_ACT_NONE && act != GRET_ACT_SWISH) return GRET_ERR_INVALID_ARG;
+    const ConvArgs a = {x, ldx, w, bias, tail0, y, tail, rows, D, K, act == GRET_ACT_SWISH, io};
+    if (gret_status e = conv_check(a)) return e;
+    const size_t tail_bytes = (size_t)rows.B * (K - 1) * D * size_of(io);
+    if (overlap(tail0, tail, tail_bytes)) return GRET_ERR_INVALID_ARG;
+    return done(launch_short_conv(a, cu_stream(stream)));
+}
+
+// --------------------------------------------------------------- selective scan
+gret_status scan_check(const ScanArgs& a) {
+    if (!all_set(a.u, a.dt, a.A, a.Bm, a.Cm, a.o) || !type_ok(a.io)) return GRET_ERR_INVALID_ARG;
+    if (a.D <= 0 || a.n <= 0) return GRET_ERR_INVALID_ARG;
+    if (gret_status e = rows_ok(a.rows)) return e;
+    if (!all_aligned(a.u, a.dt, a.A, a.Bm, a.Cm, a.skip, a.z, a.dt_bias, a.h0, a.o, a.h)) return GRET_ERR_INVALID_ARG;
+    if (a.D % kVec != 0 || !selective_states_supported(a.n)) return GRET_ERR_UNSUPPORTED;
+    if (!stride_ok(a.ldu, a.D, a.io) || !stride_ok(a.lddt, a.D, a.io) || !stride_ok(a.ldb, a.n, a.io) ||
+        !stride_ok(a.ldc, a.n, a.io) || (a.z && !stride_ok(a.ldz, a.D, a.io)))
+        return GRET_ERR_INVALID_ARG;
+    if ((long long)a.rows.B * a.D * a.n > (1LL << 40)) return GRET_ERR_UNSUPPORTED;
+    return GRET_OK;
+}
+
+bool workspace_ok(const void* ws, size_t have, size_t need) {
+    return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0);
+}
+
+gret_status scan(ScanArgs a, size_t workspace_bytes, gret_stream_t stream) {
+    if (gret_status e = scan_check(a)) return e;
+    if (overlap(a.h0, a.h, (size_t)a.rows.B * a.D * a.n * sizeof(float))) return GRET_ERR_INVALID_ARG;
+    int sms = 0;
+    if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
+    const size_t need = selective_scan_ws_bytes(a.rows.B, a.rows.N, a.rows.total, a.D, a.n, a.rows.cu != nullptr, sms);
+    if (!workspace_ok(a.workspace, workspace_bytes, need)) return GRET_ERR_INVALID_ARG;
+    return done(launch_selective_scan(a, sms, cu_stream(stream)));
+}
+
+size_t scan_workspace(int B, int N, int total, int D, int n, bool packed) {
+    if (B <= 0 || N <= 0 || (packed && total <= 0) || D <= 0 || D % kVec != 0 || !selective_states_supported(n)) return 0;
+    int sms = 148;
+    device_info(nullptr, &sms);
+    return selective_scan_ws_bytes(B, N, total, D, n, packed, sms);
+}
+
+// ---------------------------------------------------------------- residual norm
+gret_status norm_check(const NormArgs& a) {
+    if (!type_ok(a.io) || !type_ok(a.stream_type) || (a.io == GRET_F32 && a.stream_type != GRET_F32))
+        return GRET_ERR_INVALID_ARG;
+    if (!a.x || (!a.y && (a.gate || a.scale || a.w_post)) || (!a.y && !a.w_next)) return GRET_ERR_INVALID_ARG;
+    if (a.T <= 0 || a.D <= 0 || !(a.eps >= 0.f) || !isfinite(a.eps)) return GRET_ERR_INVALID_ARG;
+    if (!all_aligned(a.x, a.y, a.gate, a.scale, a.w_post, a.w_next, a.r, a.n)) return GRET_ERR_INVALID_ARG;
+    if (a.D % kVec != 0 || a.D > kNormMaxChannels || a.T > 0x7fffffffLL) return GRET_ERR_UNSUPPORTED;
+    if (!stride_ok(a.ldx, a.D, a.stream_type) || (a.y && !stride_ok(a.ldy, a.D, a.io)) ||
+        (a.gate && !stride_ok(a.ldg, a.D, a.io)))
+        return GRET_ERR_INVALID_ARG;
+    return GRET_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gret_status gret_short_conv(const void* x, long long ldx, const float* w, const float* bias, const void* tail0,
+                            void* y, void* tail, int B, int N, int D, int K, gret_dtype io_dtype, gret_activation act,
+                            gret_stream_t stream) {
+    return conv(x, ldx, w, bias, tail0, y, tail, Rows{nullptr, B, N, 0, 0}, D, K, io_dtype, act, stream);
+}
+
+gret_status gret_short_conv_varlen(const void* x, long long ldx, const float* w, const float* bias, const void* tail0,
+                                   const int* cu_seqlens, int num_seqs, int total_tokens, int max_seqlen, void* y,
+                                   void* tail, int D, int K, gret_dtype io_dtype, gret_activation act,
+                                   gret_stream_t stream) {
+    if (!cu_seqlens) return GRET_ERR_INVALID_ARG;
+    return conv(x, ldx, w, bias, tail0, y, tail, Rows{cu_seqlens, num_seqs, max_seqlen, total_tokens, 0}, D, K,
+                io_dtype, act, stream);
+}
+
+gret_status gret_short_conv_step(const void* x, long long ldx, const float* w, const float* bias, const void* tail_in,
+                                 void* tail_out, void* y, int num_seqs, int D, int K, gret_dtype io_dtype,
+                                 gret_activation act, gret_stream_t stream) {
+    if (!all_set(tail_in, tail_out) || (act != GRET_ACT_NONE && act != GRET_ACT_SWISH)) return GRET_ERR_INVALID_ARG;
+    const ConvArgs a = {x, ldx, w, bias, tail_in, y, tail_out, Rows{nullptr, num_seqs, 1, 0, 0}, D, K,
+                        act == GRET_ACT_SWISH, io_dtype};
+    if (gret_status e = conv_check(a)) return e;
+    if (tail_in != tail_out && overlap(tail_in, tail_out, (size_t)num_seqs * (K - 1) * D * size_of(io_dtype)))
+        return GRET_ERR_INVALID_ARG;
+    return done(launch_short_conv_step(a, cu_stream(stream)));
+}
+
+size_t gret_selective_scan_workspace_size(int B, int N, int D, int n, gret_dtype io_dtype) {
+    return type_ok(io_dtype) ? scan_workspace(B, N, 0, D, n, false) : 0;
+}
+
+gret_status gret_selective_scan(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
+                                const void* Bm, long long ldb, const void* Cm, long long ldc, const float* skip,
+                                const void* z, long long ldz, const float* dt_bias, const float* h0, void* o,
+                                float* h_final, int B, int N, int D, int n, gret_dtype io_dtype, void* workspace,
+                                size_t workspace_bytes, gret_stream_t stream) {
+    return scan(ScanArgs{u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h0, o, h_final,
+                         Rows{nullptr, B, N, 0, 0}, D, n, io_dtype, workspace},
+                workspace_bytes, stream);
+}
+
+size_t gret_selective_scan_varlen_workspace_size(int num_seqs, int total_tokens, int max_seqlen, int D, int n,
+                                                 gret_dtype io_dtype) {
+    return type_ok(io_dtype) ? scan_workspace(num_seqs, max_seqlen, total_tokens, D, n, true) : 0;
+}
+
+gret_status gret_selective_scan_varlen(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
+                                       const void* Bm, long long ldb, const void* Cm, long long ldc, const float* skip,
+                                       const void* z, long long ldz, const float* dt_bias, const float* h0,
+                                       const int* cu_seqlens, int num_seqs, int total_tokens, int max_seqlen, void* o,
+                                       float* h_final, int D, int n, gret_dtype io_dtype, void* workspace,
+                                       size_t workspace_bytes, gret_stream_t stream) {
+    if (!cu_seqlens) return GRET_ERR_INVALID_ARG;
+    return scan(ScanArgs{u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h0, o, h_final,
+                         Rows{cu_seqlens, num_seqs, max_seqlen, total_tokens, 0}, D, n, io_dtype, workspace},
+                workspace_bytes, stream);
+}
+
+gret_status gret_selective_step(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
+                                const void* Bm, long long ldb, const void* Cm, long long ldc, const float* skip,
+                                const void* z, long long ldz, const float* dt_bias, const float* h_in, float* h_out,
+                                void* o, int num_seqs, int D, int n, gret_dtype io_dtype, gret_stream_t stream) {
+    if (!all_set(h_in, h_out)) return GRET_ERR_INVALID_ARG;
+    const ScanArgs a = {u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h_in, o, h_out,
+                        Rows{nullptr, num_seqs, 1, 0, 0}, D, n, io_dtype, nullptr};
+    if (gret_status e = scan_check(a)) return e;
+    if (h_in != h_out && overlap(h_in, h_out, (size_t)num_seqs * D * n * sizeof(float))) return GRET_ERR_INVALID_ARG;
+    int sms = 0;
+    if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
+    return done(launch_selective_step(a, sms, cu_stream(stream)));
+}
+
+gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long long ldy, const void* gate,
+                               long long ldg, const float* scale, const float* w_post, const float* w_next, void* r,
+                               void* n, long long T, int D, float eps, gret_dtype stream_dtype, gret_dtype io_dtype,
+                               gret_stream_t stream) {
+    const NormArgs a = {x, y, gate, ldx, ldy, ldg, scale, w_post, w_next, r, n, T, D, eps, stream_dtype, io_dtype};
+    if (gret_status e = norm_check(a)) return e;
+    if ((y && !r) || (w_next && !n)) return GRET_ERR_INVALID_ARG;
+    int sms = 0;
+    if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
+    return done(launch_residual_norm(a, sms, cu_stream(stream)));
+}
+
+}  // extern "C"

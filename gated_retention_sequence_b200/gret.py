@@ -54,6 +54,9 @@ class GretError(RuntimeError):
 
 # Exported C symbols and their signatures.
 _VP, _FP, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_LL = ctypes.c_longlong
+# u, dt, A, B, C, skip, z, dt_bias of the selective scan, activations with their row strides
+_SCAN = [_VP, _LL, _VP, _LL, _FP, _VP, _LL, _VP, _LL, _FP, _VP, _LL, _FP]
 SIGNATURES = {
     "gret_prefill": (_I, [_VP, _VP, _VP, _FP, _VP, _F, _I, _VP, _FP, _I, _I, _I, _I, _I, _I, _F, _I,
                           _VP, _SZ, _VP]),
@@ -85,6 +88,15 @@ SIGNATURES = {
     "gret_prefill_projected": (_I, [_VP, _VP, _VP, _VP, _FP, _I, _VP, _F, _I, _VP, _FP, _I, _I, _I, _I, _I, _I,
                                     _F, _I, _VP, _SZ, _VP]),
     "gret_prefill_projected_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "gret_short_conv": (_I, [_VP, _LL, _FP, _FP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _VP]),
+    "gret_short_conv_varlen": (_I, [_VP, _LL, _FP, _FP, _VP, _VP, _I, _I, _I, _VP, _VP, _I, _I, _I, _I, _VP]),
+    "gret_short_conv_step": (_I, [_VP, _LL, _FP, _FP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP]),
+    "gret_selective_scan": (_I, _SCAN + [_FP, _VP, _FP, _I, _I, _I, _I, _I, _VP, _SZ, _VP]),
+    "gret_selective_scan_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "gret_selective_scan_varlen": (_I, _SCAN + [_FP, _VP, _I, _I, _I, _VP, _FP, _I, _I, _I, _VP, _SZ, _VP]),
+    "gret_selective_scan_varlen_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "gret_selective_step": (_I, _SCAN + [_FP, _FP, _VP, _I, _I, _I, _I, _VP]),
+    "gret_residual_norm": (_I, [_VP, _LL, _VP, _LL, _VP, _LL, _FP, _FP, _FP, _VP, _VP, _LL, _I, _F, _I, _I, _VP]),
     "gret_status_string": (ctypes.c_char_p, [_I]),
     "gret_version": (_I, []),
 }

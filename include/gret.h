@@ -347,6 +347,111 @@ gret_status gret_prefill_projected(const void* Q, const void* K, const void* V, 
 size_t gret_prefill_projected_workspace_size(int B, int H, int N, int dk, int dv, int chunk, int d_model,
                                              gret_dtype io_dtype);
 
+/* ------------------------------------------------------------------------
+ * The selective state space block: a second recurrent mixer, whose state
+ * decays per channel and per state number by a step that the token gives, with
+ * the short convolution in front of it, and the norm that joins a block (this
+ * one or gated retention) to the residual stream and to the next block.
+ *
+ * Tokens are rows.  An activation's rows lie `ld` elements apart (ld >= the
+ * row; ld times the element size a multiple of 16 bytes), so that columns of a
+ * wider projection are taken as they are; a uniform batch [B][N] has its rows
+ * at b * N + n.  Outputs, states and parameters are contiguous.  Parameters,
+ * states and sums are fp32.  Pointers must be 16-byte aligned; D is a multiple
+ * of 8.  An output must not alias an input except where it is said.  Every
+ * call may be captured into a CUDA graph.
+ * ------------------------------------------------------------------------ */
+typedef enum { GRET_ACT_NONE = 0, GRET_ACT_SWISH = 1 } gret_activation;
+
+/*
+ * gret_short_conv -- causal convolution along the tokens, one filter a channel:
+ *     y[n][d] = act(bias[d] + sum_k w[d][k] x[n - K + 1 + k][d])
+ *   x     [B][N][D] io dtype, row stride ldx;  y [B][N][D]
+ *   w     fp32 [D][K], K of 2, 3 or 4 (w[d][K-1] takes the token itself)
+ *   bias  fp32 [D] or NULL
+ *   tail0 [B][K-1][D] io dtype, the last K-1 inputs of the piece before,
+ *         oldest first, or NULL (zero: the sequence starts here)
+ *   tail  [B][K-1][D], the last K-1 inputs up to here, or NULL; must not
+ *         overlap tail0
+ * y holds what one call over all the pieces' tokens gives.
+ */
+gret_status gret_short_conv(const void* x, long long ldx, const float* w, const float* bias, const void* tail0,
+                            void* y, void* tail, int B, int N, int D, int K, gret_dtype io_dtype, gret_activation act,
+                            gret_stream_t stream);
+
+/* The same for a packed batch: x, y [total_tokens][D]; cu_seqlens, num_seqs,
+ * max_seqlen and rows outside the sequences as in gret_prefill_varlen; tail0
+ * and tail [num_seqs][K-1][D] (an empty sequence's tail is its tail0). */
+gret_status gret_short_conv_varlen(const void* x, long long ldx, const float* w, const float* bias, const void* tail0,
+                                   const int* cu_seqlens, int num_seqs, int total_tokens, int max_seqlen, void* y,
+                                   void* tail, int D, int K, gret_dtype io_dtype, gret_activation act,
+                                   gret_stream_t stream);
+
+/* One token per sequence: x, y [num_seqs][D]; tail_in -> tail_out
+ * [num_seqs][K-1][D], which may be the same buffer or disjoint ones. */
+gret_status gret_short_conv_step(const void* x, long long ldx, const float* w, const float* bias, const void* tail_in,
+                                 void* tail_out, void* y, int num_seqs, int D, int K, gret_dtype io_dtype,
+                                 gret_activation act, gret_stream_t stream);
+
+/*
+ * gret_selective_scan -- selective state space scan over prompts:
+ *     delta[t][d] = softplus(dt[t][d] + dt_bias[d])
+ *     h[t][d][i]  = exp(delta[t][d] A[d][i]) h[t-1][d][i] + delta[t][d] u[t][d] B[t][i]
+ *     o[t][d]     = (sum_i C[t][i] h[t][d][i] + skip[d] u[t][d]) swish(z[t][d])
+ *   u, dt, z  [B][N][D] io dtype with row strides ldu, lddt, ldz; z may be NULL
+ *             (no gate)
+ *   Bm, Cm    [B][N][n] io dtype with row strides ldb, ldc, shared by all channels
+ *   A         fp32 [D][n]; negative in a model that decays
+ *   skip, dt_bias  fp32 [D] or NULL (zero)
+ *   h0        fp32 [B][D][n], the state before the first token, or NULL (zero)
+ *   o         [B][N][D];  h_final fp32 [B][D][n] or NULL, must not overlap h0
+ *   n         8, 16, 32 or 64
+ *   workspace gret_selective_scan_workspace_size(...) bytes, 256-byte aligned
+ *             (may be NULL when that is 0); calls that share one must not overlap.
+ */
+gret_status gret_selective_scan(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
+                                const void* Bm, long long ldb, const void* Cm, long long ldc, const float* skip,
+                                const void* z, long long ldz, const float* dt_bias, const float* h0, void* o,
+                                float* h_final, int B, int N, int D, int n, gret_dtype io_dtype, void* workspace,
+                                size_t workspace_bytes, gret_stream_t stream);
+size_t gret_selective_scan_workspace_size(int B, int N, int D, int n, gret_dtype io_dtype);
+
+/* The same for a packed batch: rows [total_tokens], states [num_seqs][D][n];
+ * cu_seqlens, num_seqs, max_seqlen and rows outside the sequences as in
+ * gret_prefill_varlen (an empty sequence's h_final is its h0, or zero). */
+gret_status gret_selective_scan_varlen(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
+                                       const void* Bm, long long ldb, const void* Cm, long long ldc, const float* skip,
+                                       const void* z, long long ldz, const float* dt_bias, const float* h0,
+                                       const int* cu_seqlens, int num_seqs, int total_tokens, int max_seqlen, void* o,
+                                       float* h_final, int D, int n, gret_dtype io_dtype, void* workspace,
+                                       size_t workspace_bytes, gret_stream_t stream);
+size_t gret_selective_scan_varlen_workspace_size(int num_seqs, int total_tokens, int max_seqlen, int D, int n,
+                                                 gret_dtype io_dtype);
+
+/* One token per sequence: u, dt, z, o [num_seqs][D], Bm, Cm [num_seqs][n];
+ * h_in -> h_out fp32 [num_seqs][D][n], the same buffer or disjoint ones. */
+gret_status gret_selective_step(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
+                                const void* Bm, long long ldb, const void* Cm, long long ldc, const float* skip,
+                                const void* z, long long ldz, const float* dt_bias, const float* h_in, float* h_out,
+                                void* o, int num_seqs, int D, int n, gret_dtype io_dtype, gret_stream_t stream);
+
+/*
+ * gret_residual_norm -- a block's output into the residual stream, and the
+ * norm before the next block, with rms(v) = v / sqrt(mean(v^2) + eps):
+ *     r = x + scale (.) p,   p = rms(y) (.) w_post (.) swish(gate)
+ *     n = rms(r) (.) w_next
+ *   x, r      [T][D] stream dtype (io dtype, or fp32 beside a bf16 block)
+ *   y, gate   [T][D] io dtype;  n [T][D] io dtype
+ *   scale, w_post, w_next  fp32 [D]
+ * Each part may be left out with NULL: scale (1), gate (no gate), w_post (p
+ * starts from y itself), w_next (no n), y (n = rms(x) (.) w_next alone, r is not
+ * written).  n is formed from r before its rounding.  r may be x.  D <= 8192.
+ */
+gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long long ldy, const void* gate,
+                               long long ldg, const float* scale, const float* w_post, const float* w_next, void* r,
+                               void* n, long long T, int D, float eps, gret_dtype stream_dtype, gret_dtype io_dtype,
+                               gret_stream_t stream);
+
 /* Test aid for the give-up path of the bounded device waits.  The next `calls`
  * prefill calls that run the tensor-core kernels (any gret_prefill* entry
  * point on that path, from any host thread) make the fused kernel's TMA warp,

@@ -1,0 +1,100 @@
+"""Host-side checks of the selective state space block's entry points: bad arguments are refused before any launch
+(the pointers are never used, so this runs without a GPU)."""
+import pytest
+import torch
+
+import gated_retention_sequence_b200 as gret
+
+P = 0x100000                       # an aligned address; validation fails before it is used
+INVALID, UNSUPPORTED = gret.Status.ERR_INVALID_ARG, gret.Status.ERR_UNSUPPORTED
+BF = gret.Dtype.BF16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from gated_retention_sequence_b200 import build
+    build.build()
+    return gret.load()
+
+
+CONV = dict(x=P, ldx=64, w=P, bias=None, tail0=None, y=P, tail=None, B=2, N=5, D=64, K=4, io_dtype=BF,
+            act=gret.Activation.SWISH, stream=None)
+SCAN = dict(u=P, ldu=64, dt=P, lddt=64, A=P, Bm=P, ldb=16, Cm=P, ldc=16, skip=None, z=None, ldz=0, dt_bias=None, h0=None,
+            o=P, h_final=None, B=2, N=5, D=64, n=16, io_dtype=BF, workspace=None, workspace_bytes=0, stream=None)
+NORM = dict(x=P, ldx=64, y=P, ldy=64, gate=None, ldg=0, scale=None, w_post=None, w_next=P, r=P, n=P, T=3, D=64, eps=1e-5,
+            stream_dtype=BF, io_dtype=BF, stream=None)
+
+ROWS_BAD = [(dict(B=0), INVALID), (dict(N=0), INVALID), (dict(N=-1), INVALID), (dict(B=1 << 16, N=1 << 16), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(x=P + 2), INVALID),
+    (dict(tail0=P + 8), INVALID), (dict(D=0), INVALID), (dict(io_dtype=7), INVALID), (dict(act=9), INVALID),
+    (dict(ldx=63), INVALID), (dict(ldx=65), INVALID), (dict(ldx=-64), INVALID), (dict(D=60, ldx=64), UNSUPPORTED),
+    (dict(K=1), UNSUPPORTED), (dict(K=5), UNSUPPORTED), (dict(K=0), INVALID),
+    (dict(tail0=P, tail=P), INVALID), (dict(tail0=P, tail=P + 2 * 3 * 64 * 2 - 16), INVALID)] + ROWS_BAD)
+def test_conv_refuses(over, expect):
+    assert gret.gret_short_conv(**dict(CONV, **over)) == expect
+
+
+def test_conv_step_and_varlen_refuse():
+    step = dict(x=P, ldx=64, w=P, bias=None, tail_in=P, tail_out=P, y=P, num_seqs=2, D=64, K=4, io_dtype=BF, act=1,
+                stream=None)
+    for over in (dict(tail_in=None), dict(tail_out=None), dict(num_seqs=0), dict(tail_out=P + 16)):
+        assert gret.gret_short_conv_step(**dict(step, **over)) == INVALID, over
+    var = dict(x=P, ldx=64, w=P, bias=None, tail0=None, cu_seqlens=P, num_seqs=2, total_tokens=10, max_seqlen=6, y=P,
+               tail=None, D=64, K=4, io_dtype=BF, act=1, stream=None)
+    for over in (dict(cu_seqlens=None), dict(cu_seqlens=P + 2), dict(num_seqs=0), dict(total_tokens=0),
+                 dict(max_seqlen=0)):
+        assert gret.gret_short_conv_varlen(**dict(var, **over)) == INVALID, over
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(u=None), INVALID), (dict(dt=None), INVALID), (dict(A=None), INVALID), (dict(Bm=None), INVALID),
+    (dict(Cm=None), INVALID), (dict(o=None), INVALID), (dict(A=P + 4), INVALID), (dict(z=P + 2, ldz=64), INVALID),
+    (dict(z=P, ldz=0), INVALID), (dict(ldb=8), INVALID), (dict(ldc=17), INVALID), (dict(lddt=32), INVALID),
+    (dict(n=12), UNSUPPORTED), (dict(n=128), UNSUPPORTED), (dict(n=0), INVALID), (dict(D=60), UNSUPPORTED),
+    (dict(io_dtype=3), INVALID), (dict(h0=P, h_final=P), INVALID), (dict(h0=P, h_final=P + 2 * 64 * 16 * 4 - 16), INVALID),
+    ] + ROWS_BAD)
+def test_scan_refuses(over, expect):
+    assert gret.gret_selective_scan(**dict(SCAN, **over)) == expect
+
+
+def test_scan_step_and_varlen_refuse():
+    step = {k: v for k, v in SCAN.items() if k not in ("h0", "h_final", "B", "N", "workspace", "workspace_bytes")}
+    step.update(h_in=P, h_out=P, num_seqs=2)
+    for over in (dict(h_in=None), dict(h_out=None), dict(num_seqs=0), dict(h_out=P + 64), dict(u=None)):
+        assert gret.gret_selective_step(**dict(step, **over)) == INVALID, over
+    var = {k: v for k, v in SCAN.items() if k not in ("B", "N")}
+    var.update(cu_seqlens=P, num_seqs=2, total_tokens=9, max_seqlen=5)
+    for over in (dict(cu_seqlens=None), dict(cu_seqlens=P + 1), dict(total_tokens=0), dict(max_seqlen=-1)):
+        assert gret.gret_selective_scan_varlen(**dict(var, **over)) == INVALID, over
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(x=None), INVALID), (dict(r=None), INVALID), (dict(n=None), INVALID), (dict(y=None, w_next=None), INVALID),
+    (dict(y=None, gate=P, ldg=64), INVALID), (dict(y=None, scale=P), INVALID), (dict(eps=-1.0), INVALID),
+    (dict(eps=float("nan")), INVALID), (dict(T=0), INVALID), (dict(D=0), INVALID), (dict(ldx=60), INVALID),
+    (dict(gate=P, ldg=0), INVALID), (dict(y=P + 4), INVALID), (dict(io_dtype=gret.Dtype.F32), INVALID),
+    (dict(D=8200, ldx=8200, ldy=8200), UNSUPPORTED), (dict(D=60), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED)])
+def test_norm_refuses(over, expect):
+    assert gret.gret_residual_norm(**dict(NORM, **over)) == expect
+
+
+def test_workspace_sizes_of_refused_arguments():
+    assert gret.gret_selective_scan_workspace_size(0, 5, 64, 16, BF) == 0
+    assert gret.gret_selective_scan_workspace_size(1, 5, 64, 12, BF) == 0
+    assert gret.gret_selective_scan_varlen_workspace_size(2, 0, 5, 64, 16, BF) == 0
+
+
+def test_python_checks():
+    x = torch.zeros(2, 5, 64)
+    w = torch.zeros(64, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        gret.short_conv(x, w)
+    with pytest.raises(TypeError, match="unsupported io dtype"):
+        gret.short_conv(x.half(), w)
+    with pytest.raises(ValueError, match="go with y"):
+        gret.residual_norm(x, gate=x)
+    with pytest.raises(ValueError, match="y or w_next"):
+        gret.residual_norm(x)

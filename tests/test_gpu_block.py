@@ -1,0 +1,381 @@
+"""GPU parity of the selective state space block's operators with the 64-bit oracle, element by element within the
+error bound that the oracle carries (``oracle/block_oracle.py``)."""
+import numpy as np
+import pytest
+import torch
+
+import gated_retention_sequence_b200 as gret
+import gret_inputs as gi
+from oracle import block_oracle as bo
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gated_retention_sequence_b200 import build
+    build.build()
+    gret.load()
+
+
+def draw(tid, shape, io="f32", mean=0.0, std=1.0, seed=91):
+    """A seeded normal tensor on the GPU."""
+    n = int(np.prod(shape))
+    flat = gi.random_unit(seed, tid, (n,), mean, std * std, io) if n else torch.empty(0, dtype=TYPES[io])
+    return flat.view(shape).cuda()
+
+
+def columns(t, left=8, right=16):
+    """The same values as columns of a wider tensor, whose other columns are NaN."""
+    wide = torch.full(t.shape[:-1] + (left + t.shape[-1] + right,), float("nan"), dtype=t.dtype, device=t.device)
+    view = wide[..., left:left + t.shape[-1]]
+    view.copy_(t)
+    return view
+
+
+def offsets(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------ short convolution
+def conv_inputs(io, rows, D, K, seqs, seed=1):
+    return dict(x=draw(1, (rows, D), io, seed=seed), w=draw(2, (D, K), std=0.5, seed=seed), bias=draw(3, (D,), seed=seed),
+                tail0=draw(4, (seqs, K - 1, D), io, seed=seed))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("B,N,D", [(1, 1, 8), (3, 2, 72), (2, 33, 264), (1, 131, 1032)])
+def test_conv_prompts(io, K, B, N, D):
+    p = conv_inputs(io, B * N, D, K, B)
+    y, tail = gret.short_conv(p["x"].view(B, N, D), p["w"], p["bias"], tail0=p["tail0"])
+    for b in range(B):
+        ry, rt = bo.short_conv(p["x"][b * N:(b + 1) * N], p["w"], p["bias"], p["tail0"][b])
+        bo.check(y[b], ry, io, f"y of sequence {b}")
+        assert (tail[b].double().cpu().numpy() == rt.v).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_conv_from_zero_without_bias_or_activation(io):
+    B, N, D = 2, 40, 40
+    p = conv_inputs(io, B * N, D, 4, B)
+    x = columns(p["x"].view(B, N, D))
+    y, tail = gret.short_conv(x, p["w"], activation="none", want_tail=False)
+    assert tail is None
+    for b in range(B):
+        bo.check(y[b], bo.short_conv(x[b], p["w"], swish=False)[0], io)
+
+
+LENS = [[1], [5, 0, 1, 33, 64, 2], [0, 0, 3], [300, 1, 0, 31], [2] * 70]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", LENS)
+def test_conv_packed(io, lens):
+    D, K, T = 136, 4, sum(lens) + 3                 # three rows behind the last sequence
+    p = conv_inputs(io, T, D, K, len(lens))
+    y = torch.full((T, D), 7.0, dtype=TYPES[io], device="cuda")
+    _, tail = gret.short_conv_varlen(columns(p["x"]), p["w"], p["bias"], offsets(lens), max(lens), tail0=p["tail0"], y=y)
+    at = 0
+    for b, n in enumerate(lens):
+        ry, rt = bo.short_conv(p["x"][at:at + n], p["w"], p["bias"], p["tail0"][b])
+        bo.check(y[at:at + n], ry, io, f"y of sequence {b}")
+        assert (tail[b].double().cpu().numpy() == rt.v).all()
+        at += n
+    assert (y[at:] == 7).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("S,D", [(1, 8), (5, 264), (129, 72)])
+def test_conv_step(io, K, S, D):
+    p = conv_inputs(io, S, D, K, S)
+    apart = torch.empty_like(p["tail0"])
+    y, t = gret.short_conv_step(columns(p["x"]), p["w"], p["bias"], p["tail0"], tail_out=apart)
+    assert t is apart
+    for b in range(S):
+        ry, rt = bo.short_conv(p["x"][b:b + 1], p["w"], p["bias"], p["tail0"][b])
+        bo.check(y[b:b + 1], ry, io)
+        assert (t[b].double().cpu().numpy() == rt.v).all()
+    y2, t2 = gret.short_conv_step(p["x"], p["w"], p["bias"], p["tail0"])          # in place
+    assert t2 is p["tail0"] and torch.equal(t2, apart) and torch.equal(y, y2)
+
+
+# --------------------------------------------------------------- selective scan
+def scan_inputs(io, rows, D, n, seqs, seed=2):
+    return dict(u=draw(1, (rows, D), io, seed=seed), dt=draw(2, (rows, D), io, seed=seed),
+                A=-torch.exp(draw(3, (D, n), seed=seed)), B=draw(4, (rows, n), io, seed=seed),
+                C=draw(5, (rows, n), io, seed=seed), skip=draw(6, (D,), seed=seed), z=draw(7, (rows, D), io, seed=seed),
+                dt_bias=draw(8, (D,), mean=-3.0, seed=seed), h0=draw(9, (seqs, D, n), seed=seed))
+
+
+ROWS = ("u", "dt", "B", "C", "z")
+
+
+def scan_rows(p, a, b, s):
+    q = {k: v[a:b] if k in ROWS and v is not None else v for k, v in p.items()}
+    if q["h0"] is not None:
+        q["h0"] = q["h0"][s]
+    return q
+
+
+def scan_call(p, B, N, **kw):
+    q = {k: v.unflatten(0, (B, N)) if k in ROWS and v is not None else v for k, v in p.items()}
+    return gret.selective_scan(**q, **kw)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("B,N,D", [(1, 1, 8), (2, 17, 72), (1, 200, 40)])
+def test_scan_prompts(io, n, B, N, D):
+    p = scan_inputs(io, B * N, D, n, B)
+    o, h = scan_call(p, B, N)
+    for b in range(B):
+        ro, rh = bo.selective_scan(**scan_rows(p, b * N, (b + 1) * N, b))
+        bo.check(o[b], ro, io, f"o of sequence {b}")
+        bo.check(h[b], rh, "f32", f"h of sequence {b}")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("without", ["skip", "z", "dt_bias", "h0"])
+def test_scan_left_out_and_strided(io, without):
+    B, N, D, n = 3, 50, 264, 16
+    p = scan_inputs(io, B * N, D, n, B)
+    p[without] = None
+    q = {k: columns(v) if k in ROWS and v is not None else v for k, v in p.items()}
+    o, h = scan_call(q, B, N)
+    for b in range(B):
+        ro, rh = bo.selective_scan(**scan_rows(p, b * N, (b + 1) * N, b))
+        bo.check(o[b], ro, io)
+        bo.check(h[b], rh, "f32")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("n", [16, 64])
+def test_scan_packed(io, lens, n):
+    D, T = 72, sum(lens) + 5
+    p = scan_inputs(io, T, D, n, len(lens))
+    o = torch.full((T, D), 7.0, dtype=TYPES[io], device="cuda")
+    _, h = gret.selective_scan_varlen(**p, cu_seqlens=offsets(lens), max_seqlen=max(lens), o=o)
+    at = 0
+    for b, m in enumerate(lens):
+        if m:
+            ro, rh = bo.selective_scan(**scan_rows(p, at, at + m, b))
+            bo.check(o[at:at + m], ro, io, f"o of sequence {b}")
+            bo.check(h[b], rh, "f32", f"h of sequence {b}")
+        else:
+            assert torch.equal(h[b], p["h0"][b])
+        at += m
+    assert (o[at:] == 7).all()
+
+
+def test_scan_long_and_cut():
+    # long enough for the sequence to be cut into segments, which are joined again; few channels
+    N, D, n = 3000, 16, 16
+    p = scan_inputs("f32", N, D, n, 1)
+    o, h = scan_call(p, 1, N)
+    ro, rh = bo.selective_scan(**scan_rows(p, 0, N, 0))
+    bo.check(o[0], ro, "f32")
+    bo.check(h[0], rh, "f32")
+    # the same tokens as two sequences of one packed batch
+    cu = offsets([1700, 1300])
+    h0 = torch.cat([p["h0"], p["h0"]])
+    o2, h2 = gret.selective_scan_varlen(**dict(p, h0=h0), cu_seqlens=cu, max_seqlen=1700)
+    for b, (a, e) in enumerate([(0, 1700), (1700, 3000)]):
+        ro, rh = bo.selective_scan(**scan_rows(dict(p, h0=h0), a, e, b))
+        bo.check(o2[a:e], ro, "f32")
+        bo.check(h2[b], rh, "f32")
+
+
+def test_scan_extreme_steps():
+    # steps from nothing (softplus of -90) to all (a decay that underflows), and decays of zero and one
+    N, D, n = 64, 16, 16
+    p = scan_inputs("f32", N, D, n, 1)
+    p["dt_bias"][0::4] = -90.0
+    p["dt_bias"][1::4] = 60.0
+    p["A"][2] = 0.0
+    p["A"][5] = -1e30
+    p["B"][7] = 0.0
+    o, h = scan_call(p, 1, N)
+    ro, rh = bo.selective_scan(**scan_rows(p, 0, N, 0))
+    # a decay of exp(-1e30 delta) is zero in both: its bound must not count the argument
+    for r in (ro, rh):
+        r.e = np.where(np.isfinite(r.e), r.e, 0)
+    keep = [d for d in range(D) if d != 5]
+    bo.check(o[0][:, keep], ro[:, keep], "f32")
+    bo.check(h[0][keep], rh[keep], "f32")
+    b5 = torch.nn.functional.softplus(p["dt"][-1, 5] + p["dt_bias"][5]) * p["u"][-1, 5] * p["B"][-1]
+    torch.testing.assert_close(h[0, 5], b5, rtol=1e-5, atol=0)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("S,D", [(1, 8), (3, 72), (70, 264)])
+def test_scan_step(io, n, S, D):
+    p = scan_inputs(io, S, D, n, S)
+    h0 = p.pop("h0")
+    apart = torch.empty_like(h0)
+    q = {k: columns(v) if k in ROWS else v for k, v in p.items()}
+    o, h = gret.selective_step(**q, h=h0, h_out=apart)
+    assert h is apart
+    for b in range(S):
+        ro, rh = bo.selective_scan(**scan_rows(dict(p, h0=h0), b, b + 1, b))
+        bo.check(o[b:b + 1], ro, io)
+        bo.check(h[b], rh, "f32")
+    o2, h2 = gret.selective_step(**p, h=h0)                                       # in place
+    assert h2 is h0 and torch.equal(h0, apart) and torch.equal(o, o2)
+
+
+# ---------------------------------------------------------------- residual norm
+def norm_inputs(io, stream, T, D, seed=3):
+    p = dict(x=draw(1, (T, D), stream, std=2.0, seed=seed), y=draw(2, (T, D), io, seed=seed),
+             gate=draw(3, (T, D), io, seed=seed))
+    p.update({k: draw(4 + i, (D,), mean=1.0, std=0.2, seed=seed) for i, k in enumerate(("scale", "w_post", "w_next"))})
+    return p
+
+
+KINDS = [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")]
+
+
+@pytest.mark.parametrize("io,stream", KINDS)
+@pytest.mark.parametrize("T,D", [(1, 8), (3, 72), (5, 2048), (130, 264), (2, 4104), (3, 8192)])
+def test_norm(io, stream, T, D):
+    p = norm_inputs(io, stream, T, D)
+    r, n = gret.residual_norm(**p)
+    rr, rn = bo.residual_norm(**p)
+    bo.check(r, rr, stream, "r")
+    bo.check(n, rn, io, "n")
+
+
+@pytest.mark.parametrize("io,stream", KINDS)
+@pytest.mark.parametrize("without", [("gate",), ("scale",), ("w_post",), ("w_next",), ("gate", "scale", "w_post"),
+                                     ("gate", "scale", "w_post", "y")])
+def test_norm_left_out_and_strided(io, stream, without):
+    T, D = 7, 264
+    p = norm_inputs(io, stream, T, D)
+    for k in without:
+        p[k] = None
+    q = {k: columns(v) if k in ("x", "y", "gate") and v is not None else v for k, v in p.items()}
+    if p["y"] is None:
+        q["n"] = torch.empty(T, D, dtype=TYPES[io], device="cuda")
+    r, n = gret.residual_norm(**q)
+    rr, rn = bo.residual_norm(**p)
+    if p["y"] is None:
+        assert r is q["x"]
+    else:
+        bo.check(r, rr, stream, "r")
+    assert (n is None) == (p["w_next"] is None)
+    if n is not None:
+        bo.check(n, rn, io, "n")
+
+
+def test_norm_in_place_and_empty_rows():
+    # a row of zeros has rms sqrt(eps); the stream updated over itself gives what a copy gives
+    p = norm_inputs("bf16", "f32", 6, 520)
+    for k in ("x", "y"):
+        p[k][2] = 0
+    r, n = gret.residual_norm(**p)
+    rr, rn = bo.residual_norm(**p)
+    bo.check(r, rr, "f32")
+    bo.check(n, rn, "bf16")
+    x = p["x"].clone()
+    r2, n2 = gret.residual_norm(**dict(p, x=x), r=x)
+    assert r2 is x and torch.equal(x, r) and torch.equal(n, n2)
+
+
+# --------------------------------------------------------------------- together
+def block_weights(D, n, R, K=4):
+    g = lambda i, *s, std=1.0, mean=0.0: draw(20 + i, s, std=std, mean=mean)  # noqa: E731
+    return dict(w_in=g(0, D, 2 * D, std=D ** -0.5), conv_w=g(1, D, K, std=0.5), conv_b=g(2, D, std=0.1),
+                w_x=g(3, D, R + 2 * n, std=D ** -0.5), w_dt=g(4, R, D, std=R ** -0.5), dt_bias=g(5, D, mean=-3.0),
+                A=-torch.exp(g(6, D, n)), skip=g(7, D, mean=1.0, std=0.1), w_out=g(8, D, D, std=D ** -0.5),
+                w_post=g(9, D, mean=1.0, std=0.1), w_next=g(10, D, mean=1.0, std=0.1), scale=g(11, D, mean=0.5, std=0.1))
+
+
+def block_prompt(x, W, n, R, tail=None, h=None, gate=None):
+    _, v = gret.residual_norm(x, w_next=W["w_next"])
+    xz = v @ W["w_in"]
+    D = x.shape[-1]
+    c, tail = gret.short_conv(xz[..., :D], W["conv_w"], W["conv_b"], tail0=tail)
+    q = c @ W["w_x"]
+    o, h = gret.selective_scan(c, q[..., :R] @ W["w_dt"], W["A"], q[..., R:R + n], q[..., R + n:], skip=W["skip"],
+                               z=xz[..., D:], dt_bias=W["dt_bias"], h0=h)
+    r, v = gret.residual_norm(x, o @ W["w_out"], gate=xz[..., D:], scale=W["scale"], w_post=W["w_post"],
+                              w_next=W["w_next"])
+    return r, v, tail, h
+
+
+def block_step(x, W, n, R, tail, h):
+    _, v = gret.residual_norm(x, w_next=W["w_next"])
+    xz = v @ W["w_in"]
+    D = x.shape[-1]
+    c, _ = gret.short_conv_step(xz[:, :D], W["conv_w"], W["conv_b"], tail)
+    q = c @ W["w_x"]
+    o, _ = gret.selective_step(c, q[:, :R] @ W["w_dt"], W["A"], q[:, R:R + n], q[:, R + n:], h, skip=W["skip"],
+                               z=xz[:, D:], dt_bias=W["dt_bias"])
+    return gret.residual_norm(x, o @ W["w_out"], gate=xz[:, D:], scale=W["scale"], w_post=W["w_post"],
+                              w_next=W["w_next"])
+
+
+def test_block_prompt_then_steps_is_the_longer_prompt():
+    """A prompt, a second piece of it and single tokens give what one pass over all tokens gives."""
+    B, D, n, R, cuts = 2, 64, 16, 8, (37, 90, 96)
+    W = block_weights(D, n, R)
+    x = draw(40, (B, cuts[2], D))
+    r, v, tail, h = block_prompt(x, W, n, R)
+    r1, v1, t1, h1 = block_prompt(x[:, :cuts[0]].contiguous(), W, n, R)
+    r2, v2, t2, h2 = block_prompt(x[:, cuts[0]:cuts[1]].contiguous(), W, n, R, t1, h1)
+    rs, vs = [r1, r2], [v1, v2]
+    for t in range(cuts[1], cuts[2]):
+        a, b = block_step(x[:, t].contiguous(), W, n, R, t2, h2)
+        rs.append(a[:, None])
+        vs.append(b[:, None])
+    # the matrix products round differently for other row counts: fp32 with its default products, tens of units
+    for got, want in ((torch.cat(rs, 1), r), (torch.cat(vs, 1), v), (h2, h), (t2, tail)):
+        torch.testing.assert_close(got, want, rtol=2e-4, atol=2e-4)
+
+
+def test_block_step_in_a_graph_and_on_another_stream():
+    """Steps captured once and replayed, on a stream of their own, move the state as direct calls do."""
+    S, D, n, R = 3, 64, 16, 8
+    W = block_weights(D, n, R)
+    xs = draw(41, (4, S, D))
+    tail, h = draw(42, (S, 3, D)), draw(43, (S, D, n))
+    want_t, want_h = tail.clone(), h.clone()
+    want = [block_step(x, W, n, R, want_t, want_h)[0].clone() for x in xs]
+    x = torch.empty(S, D, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        keep_t, keep_h = tail.clone(), h.clone()
+        x.copy_(xs[0])
+        block_step(x, W, n, R, tail, h)              # warm up
+        tail.copy_(keep_t)
+        h.copy_(keep_h)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r, _ = block_step(x, W, n, R, tail, h)
+    for i in range(4):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.testing.assert_close(r, want[i], rtol=1e-4, atol=1e-4)
+    torch.testing.assert_close(h, want_h, rtol=1e-4, atol=1e-4)
+
+
+def test_calls_on_a_given_stream():
+    side = torch.cuda.Stream()
+    p = scan_inputs("bf16", 600, 264, 16, 1)
+    c = conv_inputs("bf16", 600, 264, 4, 1)
+    m = norm_inputs("bf16", "bf16", 600, 264)
+    want = [scan_call(p, 1, 600), gret.short_conv(c["x"][None], c["w"], c["bias"]), gret.residual_norm(**m)]
+    torch.cuda.synchronize()
+    got = [scan_call(p, 1, 600, stream=side), gret.short_conv(c["x"][None], c["w"], c["bias"], stream=side),
+           gret.residual_norm(**m, stream=side)]
+    side.synchronize()
+    for a, b in zip(want, got):
+        for s, t in zip(a, b):
+            assert torch.equal(s, t)
