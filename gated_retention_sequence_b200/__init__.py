@@ -17,8 +17,11 @@ from .gret import (  # noqa: F401
     gret_prefill_varlen_workspace_size, gret_prefill_varlen_launches,
 )
 from .block import (  # noqa: F401
-    Activation, gret_residual_norm, gret_selective_scan, gret_selective_scan_varlen,
-    gret_selective_scan_varlen_workspace_size, gret_selective_scan_workspace_size, gret_selective_step,
-    gret_short_conv, gret_short_conv_step, gret_short_conv_varlen, residual_norm, selective_scan,
-    selective_scan_varlen, selective_step, short_conv, short_conv_step, short_conv_varlen,
+    Activation, gret_residual_norm, gret_residual_norm_backward, gret_residual_norm_backward_workspace_size,
+    gret_selective_scan, gret_selective_scan_backward, gret_selective_scan_backward_workspace_size,
+    gret_selective_scan_varlen, gret_selective_scan_varlen_workspace_size, gret_selective_scan_workspace_size,
+    gret_selective_step, gret_short_conv, gret_short_conv_backward, gret_short_conv_backward_workspace_size,
+    gret_short_conv_step, gret_short_conv_varlen, residual_norm, residual_norm_backward, selective_scan,
+    selective_scan_backward, selective_scan_varlen, selective_step, short_conv, short_conv_backward, short_conv_step,
+    short_conv_varlen,
 )

@@ -1,7 +1,7 @@
 """The selective state space block's operators as calls on torch CUDA tensors.
 
 ``short_conv``, ``selective_scan`` and ``residual_norm`` (with their forms for
-packed batches and single tokens) check types and shapes, allocate
+packed batches and single tokens, and their gradients) check types and shapes, allocate
 outputs and scratch with torch's allocator and call the C ABI of
 ``include/gret.h``; all arithmetic runs in the CUDA library.
 
@@ -74,6 +74,39 @@ def gret_residual_norm(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, r, n, T
                        stream) -> int:
     return _g.load().gret_residual_norm(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, r, n, T, D, eps,
                                         int(stream_dtype), int(io_dtype), stream)
+
+
+def gret_short_conv_backward_workspace_size(B, N, D, K, io_dtype) -> int:
+    return _g.load().gret_short_conv_backward_workspace_size(B, N, D, K, int(io_dtype))
+
+
+def gret_short_conv_backward(x, ldx, w, bias, tail0, dy, dtail, dx, dw, dbias, dtail0, B, N, D, K, io_dtype, act,
+                             workspace, workspace_bytes, stream) -> int:
+    return _g.load().gret_short_conv_backward(x, ldx, w, bias, tail0, dy, dtail, dx, dw, dbias, dtail0, B, N, D, K,
+                                              int(io_dtype), int(act), workspace, workspace_bytes, stream)
+
+
+def gret_selective_scan_backward_workspace_size(B, N, D, n, io_dtype) -> int:
+    return _g.load().gret_selective_scan_backward_workspace_size(B, N, D, n, int(io_dtype))
+
+
+def gret_selective_scan_backward(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, dout, dh_final, du,
+                                 ddt, dA, dBm, dCm, dskip, dz, ddt_bias, dh0, B, N, D, n, io_dtype, workspace,
+                                 workspace_bytes, stream) -> int:
+    return _g.load().gret_selective_scan_backward(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0,
+                                                  dout, dh_final, du, ddt, dA, dBm, dCm, dskip, dz, ddt_bias, dh0, B,
+                                                  N, D, n, int(io_dtype), workspace, workspace_bytes, stream)
+
+
+def gret_residual_norm_backward_workspace_size(T, D) -> int:
+    return _g.load().gret_residual_norm_backward_workspace_size(T, D)
+
+
+def gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, dr, dn, dx, dy, dgate, dscale, dw_post,
+                                dw_next, T, D, eps, stream_dtype, io_dtype, workspace, workspace_bytes, stream) -> int:
+    return _g.load().gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, dr, dn, dx, dy,
+                                                 dgate, dscale, dw_post, dw_next, T, D, eps, int(stream_dtype),
+                                                 int(io_dtype), workspace, workspace_bytes, stream)
 
 
 # ---------------------------------------------------------------- helpers
@@ -242,6 +275,33 @@ def short_conv_step(x, w, bias, tail, activation: Optional[str] = "swish", y=Non
     return y, tail_out
 
 
+def short_conv_backward(x, w, bias, dy, tail0=None, dtail=None, activation: Optional[str] = "swish", workspace=None,
+                        stream=None):
+    """Gradients of <y, dy> + <tail, dtail> (gret_short_conv_backward).
+
+    Shapes as for ``short_conv``.  Returns a dict: dx (x's dtype), dw [D,K] fp32, dbias [D] fp32 (None without a bias),
+    dtail0 (x's dtype; None without a tail0)."""
+    torch = _g._torch()
+    B, N, D = x.shape
+    dev, io = x.device, _io_of(x)
+    ldx = _rows(x, "x", x.dtype, x.shape, dev)
+    K = _conv_weights(w, bias, D, dev)
+    _check(dy, "dy", x.dtype, (B, N, D), dev)
+    _opt(tail0, "tail0", x.dtype, (B, K - 1, D), dev)
+    _opt(dtail, "dtail", x.dtype, (B, K - 1, D), dev)
+    act = _act(activation)
+    with _on(dev, stream) as st:
+        g = {"dx": torch.empty((B, N, D), dtype=x.dtype, device=dev), "dw": torch.empty_like(w),
+             "dbias": None if bias is None else torch.empty_like(bias),
+             "dtail0": None if tail0 is None else torch.empty_like(tail0)}
+        need = gret_short_conv_backward_workspace_size(B, N, D, K, io)
+        workspace = _workspace(workspace, need, dev)
+        _raise_if(gret_short_conv_backward(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(dy), _ptr(dtail),
+                                           _ptr(g["dx"]), _ptr(g["dw"]), _ptr(g["dbias"]), _ptr(g["dtail0"]), B, N, D,
+                                           K, io, act, _ptr(workspace), need, st), "gret_short_conv_backward")
+    return g
+
+
 # ---------------------------------------------------------------- selective scan
 def _scan_inputs(u, dt, A, B, C, skip, z, dt_bias):
     """Check the scan's inputs; returns (device, io dtype, D, n, row strides)."""
@@ -334,6 +394,35 @@ def selective_step(u, dt, A, B, C, h, skip=None, z=None, dt_bias=None, h_out=Non
     return o, h_out
 
 
+def selective_scan_backward(u, dt, A, B, C, do, skip=None, z=None, dt_bias=None, h0=None, dh_final=None,
+                            want_dh0: bool = False, workspace=None, stream=None):
+    """Gradients of <o, do> + <h_final, dh_final> (gret_selective_scan_backward).
+
+    Shapes as for ``selective_scan``.  Returns a dict: du, ddt, dB, dC, dz (u's dtype) and dA, dskip, ddt_bias, dh0
+    (fp32); dz, dskip and ddt_bias are None where their input is, dh0 without h0 unless ``want_dh0``."""
+    torch = _g._torch()
+    b, N, D = u.shape
+    dev, io, D, n, ld = _scan_inputs(u, dt, A, B, C, skip, z, dt_bias)
+    _check(do, "do", u.dtype, (b, N, D), dev)
+    _opt(h0, "h0", torch.float32, (b, D, n), dev)
+    _opt(dh_final, "dh_final", torch.float32, (b, D, n), dev)
+    with _on(dev, stream) as st:
+        row = lambda w: torch.empty((b, N, w), dtype=u.dtype, device=dev)  # noqa: E731
+        g = {"du": row(D), "ddt": row(D), "dA": torch.empty_like(A), "dB": row(n), "dC": row(n),
+             "dz": None if z is None else row(D), "dskip": None if skip is None else torch.empty_like(skip),
+             "ddt_bias": None if dt_bias is None else torch.empty_like(dt_bias),
+             "dh0": torch.empty((b, D, n), dtype=torch.float32, device=dev) if h0 is not None or want_dh0 else None}
+        need = gret_selective_scan_backward_workspace_size(b, N, D, n, io)
+        workspace = _workspace(workspace, need, dev)
+        _raise_if(gret_selective_scan_backward(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
+                                               _ptr(skip), _ptr(z), ld[4], _ptr(dt_bias), _ptr(h0), _ptr(do),
+                                               _ptr(dh_final), _ptr(g["du"]), _ptr(g["ddt"]), _ptr(g["dA"]),
+                                               _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dskip"]), _ptr(g["dz"]),
+                                               _ptr(g["ddt_bias"]), _ptr(g["dh0"]), b, N, D, n, io, _ptr(workspace),
+                                               need, st), "gret_selective_scan_backward")
+    return g
+
+
 # ---------------------------------------------------------------- residual norm
 def _norm_inputs(x, y, gate, scale, w_post, w_next, n=None):
     """Check the norm's inputs; returns (device, stream dtype, io dtype, T, D, row strides).  Without y an fp32 stream's n
@@ -381,3 +470,33 @@ def residual_norm(x, y=None, gate=None, scale=None, w_post=None, w_next=None, ep
                                      _ptr(w_next), _ptr(r) if y is not None else None, _ptr(n), T, D, float(eps), sd,
                                      io, st), "gret_residual_norm")
     return r, n
+
+
+def residual_norm_backward(x, y=None, dr=None, dn=None, gate=None, scale=None, w_post=None, w_next=None,
+                           eps: float = 1e-5, workspace=None, stream=None):
+    """Gradients of <r, dr> + <n, dn> (gret_residual_norm_backward).
+
+    Shapes as for ``residual_norm``; dr has x's dtype and may be None, dn goes with w_next.  Returns a dict: dx (x's
+    dtype), dy, dgate (y's dtype), dscale, dw_post, dw_next (fp32), None where the input is None."""
+    torch = _g._torch()
+    if (dn is None) != (w_next is None):
+        raise ValueError("dn goes with w_next")
+    if dr is None and dn is None:
+        raise ValueError("dr or dn is required")
+    dev, sd, io, T, D, ld = _norm_inputs(x, y, gate, scale, w_post, w_next, dn)
+    io_torch = torch.float32 if io == Dtype.F32 else torch.bfloat16
+    _opt(dr, "dr", x.dtype, x.shape, dev)
+    _opt(dn, "dn", io_torch, x.shape, dev)
+    with _on(dev, stream) as st:
+        row = lambda t, dtype: None if t is None else torch.empty(x.shape, dtype=dtype, device=dev)  # noqa: E731
+        par = lambda w: None if w is None else torch.empty_like(w)  # noqa: E731
+        g = {"dx": row(x, x.dtype), "dy": row(y, io_torch), "dgate": row(gate, io_torch), "dscale": par(scale),
+             "dw_post": par(w_post), "dw_next": par(w_next)}
+        need = gret_residual_norm_backward_workspace_size(T, D)
+        workspace = _workspace(workspace, need, dev)
+        _raise_if(gret_residual_norm_backward(_ptr(x), ld[0], _ptr(y), ld[1], _ptr(gate), ld[2], _ptr(scale),
+                                              _ptr(w_post), _ptr(w_next), _ptr(dr), _ptr(dn), _ptr(g["dx"]),
+                                              _ptr(g["dy"]), _ptr(g["dgate"]), _ptr(g["dscale"]), _ptr(g["dw_post"]),
+                                              _ptr(g["dw_next"]), T, D, float(eps), sd, io, _ptr(workspace), need, st),
+                  "gret_residual_norm_backward")
+    return g

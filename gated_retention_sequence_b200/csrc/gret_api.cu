@@ -167,8 +167,6 @@ static size_t projected_extra_bytes(gret_path path, int B, int H, int N, int d_m
     return ((size_t)B * N * H * 4 + 255) & ~size_t(255);
 }
 
-static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 static gret_status prefill_impl(const void* Q, const void* K, const void* V, const float* gate_logits,
                                 const void* G, const float* S0, const int* cu_seqlens, int total, float tau,
                                 int chunk, void* O, float* S_final, int B, int H, int N, int dk, int dv,

@@ -126,6 +126,18 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
 // d/dv of v sigmoid(v)
 __device__ __forceinline__ float swish_slope(float v, float sig) { return sig * (1.0f + v * (1.0f - sig)); }
 
+// partial [groups][offset[count]] summed over the groups; columns offset[j] ..
+// offset[j + 1] - 1 go to dst[j], stride[j] floats apart (null: not wanted).
+struct ColumnOutputs {
+    int count;
+    long long offset[6];
+    float* dst[5];
+    int stride[5];
+};
+cudaError_t launch_column_sums(const float* partial, int groups, const ColumnOutputs& out, cudaStream_t s);
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
 struct ConvArgs {
     const void* x;
     long long ldx;
@@ -173,6 +185,7 @@ struct ScanBackwardArgs {
     const float* dh_final;
     void *du, *ddt, *dBm, *dCm, *dz;
     float *dA, *dskip, *ddt_bias, *dh0;
+    void* workspace;
 };
 size_t selective_backward_ws_bytes(int B, int N, int D, int n, gret_dtype io);
 cudaError_t launch_selective_backward(ScanBackwardArgs a, int num_sms, cudaStream_t s);

@@ -92,10 +92,11 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 gret_status scan(ScanArgs a, size_t workspace_bytes, gret_stream_t stream) {
     if (gret_status e = scan_check(a)) return e;
     if (overlap(a.h0, a.h, (size_t)a.rows.B * a.D * a.n * sizeof(float))) return GRET_ERR_INVALID_ARG;
-    int sms = 0;
-    if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
+    int sms = 148;
+    const bool device = device_info(nullptr, &sms);
     const size_t need = selective_scan_ws_bytes(a.rows.B, a.rows.N, a.rows.total, a.D, a.n, a.rows.cu != nullptr, sms);
     if (!workspace_ok(a.workspace, workspace_bytes, need)) return GRET_ERR_INVALID_ARG;
+    if (!device) return GRET_ERR_CUDA;
     return done(launch_selective_scan(a, sms, cu_stream(stream)));
 }
 
@@ -206,6 +207,83 @@ gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long
     int sms = 0;
     if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
     return done(launch_residual_norm(a, sms, cu_stream(stream)));
+}
+
+size_t gret_short_conv_backward_workspace_size(int B, int N, int D, int K, gret_dtype io_dtype) {
+    if (rows_ok(Rows{nullptr, B, N, 0, 0}) || D <= 0 || D % kVec != 0 || K < 2 || K > 4 || !type_ok(io_dtype)) return 0;
+    return short_conv_backward_ws_bytes(B, N, D, K);
+}
+
+gret_status gret_short_conv_backward(const void* x, long long ldx, const float* w, const float* bias,
+                                     const void* tail0, const void* dy, const void* dtail, void* dx, float* dw,
+                                     float* dbias, void* dtail0, int B, int N, int D, int K, gret_dtype io_dtype,
+                                     gret_activation act, void* workspace, size_t workspace_bytes,
+                                     gret_stream_t stream) {
+    if (act != GRET_ACT_NONE && act != GRET_ACT_SWISH) return GRET_ERR_INVALID_ARG;
+    if (!all_set(dy, dx) || !all_aligned(dy, dtail, dx, dw, dbias, dtail0)) return GRET_ERR_INVALID_ARG;
+    ConvBackwardArgs g = {};
+    g.f = ConvArgs{x, ldx, w, bias, tail0, dx, nullptr, Rows{nullptr, B, N, 0, 0}, D, K, act == GRET_ACT_SWISH, io_dtype};
+    if (gret_status e = conv_check(g.f)) return e;
+    if (!workspace_ok(workspace, workspace_bytes, short_conv_backward_ws_bytes(B, N, D, K))) return GRET_ERR_INVALID_ARG;
+    g.dy = dy; g.dtail = dtail; g.dx = dx; g.dtail0 = dtail0; g.dw = dw; g.dbias = dbias; g.workspace = workspace;
+    return done(launch_short_conv_backward(g, cu_stream(stream)));
+}
+
+size_t gret_selective_scan_backward_workspace_size(int B, int N, int D, int n, gret_dtype io_dtype) {
+    if (rows_ok(Rows{nullptr, B, N, 0, 0}) || D <= 0 || D % kVec != 0 || !selective_states_supported(n) ||
+        !type_ok(io_dtype))
+        return 0;
+    return selective_backward_ws_bytes(B, N, D, n, io_dtype);
+}
+
+gret_status gret_selective_scan_backward(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
+                                         const void* Bm, long long ldb, const void* Cm, long long ldc,
+                                         const float* skip, const void* z, long long ldz, const float* dt_bias,
+                                         const float* h0, const void* dout, const float* dh_final, void* du, void* ddt,
+                                         float* dA, void* dBm, void* dCm, float* dskip, void* dz, float* ddt_bias,
+                                         float* dh0, int B, int N, int D, int n, gret_dtype io_dtype, void* workspace,
+                                         size_t workspace_bytes, gret_stream_t stream) {
+    if (!all_set(dout, du, ddt, dA, dBm, dCm) || (z && !dz)) return GRET_ERR_INVALID_ARG;
+    if (!all_aligned(dout, dh_final, du, ddt, dA, dBm, dCm, dskip, dz, ddt_bias, dh0)) return GRET_ERR_INVALID_ARG;
+    ScanBackwardArgs g = {};
+    g.f = ScanArgs{u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h0, du, nullptr,
+                   Rows{nullptr, B, N, 0, 0}, D, n, io_dtype, nullptr};
+    if (gret_status e = scan_check(g.f)) return e;
+    if (!workspace_ok(workspace, workspace_bytes, selective_backward_ws_bytes(B, N, D, n, io_dtype)))
+        return GRET_ERR_INVALID_ARG;
+    int sms = 0;
+    if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
+    g.dout = dout; g.dh_final = dh_final; g.du = du; g.ddt = ddt; g.dBm = dBm; g.dCm = dCm; g.dz = dz;
+    g.dA = dA; g.dskip = dskip; g.ddt_bias = ddt_bias; g.dh0 = dh0; g.workspace = workspace;
+    return done(launch_selective_backward(g, sms, cu_stream(stream)));
+}
+
+size_t gret_residual_norm_backward_workspace_size(long long T, int D) {
+    if (T <= 0 || D <= 0 || D % kVec != 0 || D > kNormMaxChannels) return 0;
+    int sms = 148;
+    device_info(nullptr, &sms);
+    return residual_norm_backward_ws_bytes(T, D, sms);
+}
+
+gret_status gret_residual_norm_backward(const void* x, long long ldx, const void* y, long long ldy, const void* gate,
+                                        long long ldg, const float* scale, const float* w_post, const float* w_next,
+                                        const void* dr, const void* dn, void* dx, void* dy, void* dgate, float* dscale,
+                                        float* dw_post, float* dw_next, long long T, int D, float eps,
+                                        gret_dtype stream_dtype, gret_dtype io_dtype, void* workspace,
+                                        size_t workspace_bytes, gret_stream_t stream) {
+    NormBackwardArgs g = {};
+    g.f = NormArgs{x, y, gate, ldx, ldy, ldg, scale, w_post, w_next, nullptr, nullptr, T, D, eps, stream_dtype, io_dtype};
+    if (gret_status e = norm_check(g.f)) return e;
+    if (!dx || (y && !dy) || (gate && !dgate) || (w_next != nullptr) != (dn != nullptr) || (!dr && !dn))
+        return GRET_ERR_INVALID_ARG;
+    if (!all_aligned(dr, dn, dx, dy, dgate, dscale, dw_post, dw_next)) return GRET_ERR_INVALID_ARG;
+    int sms = 148;
+    const bool device = device_info(nullptr, &sms);
+    if (!workspace_ok(workspace, workspace_bytes, residual_norm_backward_ws_bytes(T, D, sms))) return GRET_ERR_INVALID_ARG;
+    if (!device) return GRET_ERR_CUDA;
+    g.dr = dr; g.dn = dn; g.dx = dx; g.dy = dy; g.dgate = dgate;
+    g.dscale = dscale; g.dw_post = dw_post; g.dw_next = dw_next; g.workspace = workspace;
+    return done(launch_residual_norm_backward(g, sms, cu_stream(stream)));
 }
 
 }  // extern "C"

@@ -96,6 +96,15 @@ SIGNATURES = {
     "gret_selective_scan_varlen": (_I, _SCAN + [_FP, _VP, _I, _I, _I, _VP, _FP, _I, _I, _I, _VP, _SZ, _VP]),
     "gret_selective_scan_varlen_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "gret_selective_step": (_I, _SCAN + [_FP, _FP, _VP, _I, _I, _I, _I, _VP]),
+    "gret_short_conv_backward_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "gret_short_conv_backward": (_I, [_VP, _LL, _FP, _FP, _VP, _VP, _VP, _VP, _FP, _FP, _VP, _I, _I, _I, _I, _I, _I,
+                                      _VP, _SZ, _VP]),
+    "gret_selective_scan_backward_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "gret_selective_scan_backward": (_I, _SCAN + [_FP, _VP, _FP, _VP, _VP, _FP, _VP, _VP, _FP, _VP, _FP, _FP, _I, _I,
+                                                  _I, _I, _I, _VP, _SZ, _VP]),
+    "gret_residual_norm_backward_workspace_size": (_SZ, [_LL, _I]),
+    "gret_residual_norm_backward": (_I, [_VP, _LL, _VP, _LL, _VP, _LL, _FP, _FP, _FP, _VP, _VP, _VP, _VP, _VP, _FP,
+                                         _FP, _FP, _LL, _I, _F, _I, _I, _VP, _SZ, _VP]),
     "gret_residual_norm": (_I, [_VP, _LL, _VP, _LL, _VP, _LL, _FP, _FP, _FP, _VP, _VP, _LL, _I, _F, _I, _I, _VP]),
     "gret_status_string": (ctypes.c_char_p, [_I]),
     "gret_version": (_I, []),

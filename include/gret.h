@@ -452,6 +452,50 @@ gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long
                                void* n, long long T, int D, float eps, gret_dtype stream_dtype, gret_dtype io_dtype,
                                gret_stream_t stream);
 
+/*
+ * Gradients.  Each call takes the forward's inputs (what the forward computed is
+ * formed again) and the gradients of its outputs, and returns those of its
+ * inputs: activations in the io dtype, contiguous; parameters and states in
+ * fp32, summed over all rows in a fixed order, so that a call gives the same
+ * bits every time.  Workspaces are 256-byte aligned, of the size that the
+ * function next to the call gives (0 for refused arguments); calls that share
+ * one must not overlap.  Uniform batches only.
+ *
+ * gret_short_conv_backward -- of <y, dy> + <tail, dtail>: dx, and where wanted
+ * (not NULL) dw [D][K], dbias [D], dtail0 [B][K-1][D].  dy [B][N][D]; dtail
+ * [B][K-1][D] or NULL.
+ */
+size_t gret_short_conv_backward_workspace_size(int B, int N, int D, int K, gret_dtype io_dtype);
+gret_status gret_short_conv_backward(const void* x, long long ldx, const float* w, const float* bias,
+                                     const void* tail0, const void* dy, const void* dtail, void* dx, float* dw,
+                                     float* dbias, void* dtail0, int B, int N, int D, int K, gret_dtype io_dtype,
+                                     gret_activation act, void* workspace, size_t workspace_bytes,
+                                     gret_stream_t stream);
+
+/* gret_selective_scan_backward -- of <o, dout> + <h_final, dh_final>: du, ddt,
+ * dz [B][N][D] (dz where z is given), dBm, dCm [B][N][n], dA [D][n], and where
+ * wanted dskip, ddt_bias [D] and dh0 [B][D][n].  dh_final may be NULL (zero). */
+size_t gret_selective_scan_backward_workspace_size(int B, int N, int D, int n, gret_dtype io_dtype);
+gret_status gret_selective_scan_backward(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
+                                         const void* Bm, long long ldb, const void* Cm, long long ldc,
+                                         const float* skip, const void* z, long long ldz, const float* dt_bias,
+                                         const float* h0, const void* dout, const float* dh_final, void* du, void* ddt,
+                                         float* dA, void* dBm, void* dCm, float* dskip, void* dz, float* ddt_bias,
+                                         float* dh0, int B, int N, int D, int n, gret_dtype io_dtype, void* workspace,
+                                         size_t workspace_bytes, gret_stream_t stream);
+
+/* gret_residual_norm_backward -- of <r, dr> + <n, dn>: dx in the stream dtype,
+ * dy where y is given, dgate where gate is given, and where wanted dscale,
+ * dw_post, dw_next [D].  dr (stream dtype) may be NULL (zero); dn goes with
+ * w_next. */
+size_t gret_residual_norm_backward_workspace_size(long long T, int D);
+gret_status gret_residual_norm_backward(const void* x, long long ldx, const void* y, long long ldy, const void* gate,
+                                        long long ldg, const float* scale, const float* w_post, const float* w_next,
+                                        const void* dr, const void* dn, void* dx, void* dy, void* dgate, float* dscale,
+                                        float* dw_post, float* dw_next, long long T, int D, float eps,
+                                        gret_dtype stream_dtype, gret_dtype io_dtype, void* workspace,
+                                        size_t workspace_bytes, gret_stream_t stream);
+
 /* Test aid for the give-up path of the bounded device waits.  The next `calls`
  * prefill calls that run the tensor-core kernels (any gret_prefill* entry
  * point on that path, from any host thread) make the fused kernel's TMA warp,

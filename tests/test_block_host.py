@@ -81,10 +81,35 @@ def test_norm_refuses(over, expect):
     assert gret.gret_residual_norm(**dict(NORM, **over)) == expect
 
 
+def test_backwards_refuse():
+    ws = dict(workspace=P, workspace_bytes=1 << 40)
+    conv = dict({k: v for k, v in CONV.items() if k not in ("y", "tail")}, dy=P, dtail=None, dx=P, dw=P, dbias=None,
+                dtail0=None, **ws)
+    for over in (dict(dy=None), dict(dx=None), dict(dw=P + 4), dict(dtail=P + 8), dict(workspace=None),
+                 dict(workspace=P + 128), dict(workspace_bytes=0), dict(act=4), dict(N=0)):
+        assert gret.gret_short_conv_backward(**dict(conv, **over)) == INVALID, over
+    assert gret.gret_short_conv_backward(**dict(conv, K=7)) == UNSUPPORTED
+    scan = dict({k: v for k, v in SCAN.items() if k not in ("o", "h_final")}, dout=P, dh_final=None, du=P, ddt=P, dA=P,
+                dBm=P, dCm=P, dskip=None, dz=None, ddt_bias=None, dh0=None, **ws)
+    for over in (dict(dout=None), dict(du=None), dict(ddt=None), dict(dA=None), dict(dBm=None), dict(dCm=None),
+                 dict(z=P, ldz=64), dict(dh0=P + 4), dict(workspace=None), dict(workspace_bytes=0), dict(B=0)):
+        assert gret.gret_selective_scan_backward(**dict(scan, **over)) == INVALID, over
+    assert gret.gret_selective_scan_backward(**dict(scan, n=24)) == UNSUPPORTED
+    norm = dict({k: v for k, v in NORM.items() if k not in ("r", "n")}, dr=P, dn=P, dx=P, dy=P, dgate=None, dscale=None,
+                dw_post=None, dw_next=None, **ws)
+    for over in (dict(dx=None), dict(dy=None), dict(dn=None), dict(w_next=None), dict(gate=P, ldg=64),
+                 dict(dr=P + 2), dict(workspace_bytes=0), dict(T=0), dict(eps=float("inf"))):
+        assert gret.gret_residual_norm_backward(**dict(norm, **over)) == INVALID, over
+    assert gret.gret_residual_norm_backward(**dict(norm, D=8200, ldx=8200, ldy=8200)) == UNSUPPORTED
+
+
 def test_workspace_sizes_of_refused_arguments():
     assert gret.gret_selective_scan_workspace_size(0, 5, 64, 16, BF) == 0
     assert gret.gret_selective_scan_workspace_size(1, 5, 64, 12, BF) == 0
     assert gret.gret_selective_scan_varlen_workspace_size(2, 0, 5, 64, 16, BF) == 0
+    assert gret.gret_selective_scan_backward_workspace_size(1, 0, 64, 16, BF) == 0
+    assert gret.gret_short_conv_backward_workspace_size(1, 5, 64, 5, BF) == 0
+    assert gret.gret_residual_norm_backward_workspace_size(5, 60) == 0
 
 
 def test_python_checks():

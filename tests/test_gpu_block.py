@@ -103,6 +103,35 @@ def test_conv_step(io, K, S, D):
     assert t2 is p["tail0"] and torch.equal(t2, apart) and torch.equal(y, y2)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("B,N,D", [(1, 1, 8), (3, 2, 72), (2, 65, 264), (1, 300, 136), (20, 7, 8)])
+def test_conv_backward(io, K, B, N, D):
+    p = conv_inputs(io, B * N, D, K, B)
+    dy, dtail = draw(5, (B, N, D), io), draw(6, (B, K - 1, D), io)
+    g = gret.short_conv_backward(columns(p["x"].view(B, N, D)), p["w"], p["bias"], dy, tail0=p["tail0"], dtail=dtail)
+    total = None
+    for b in range(B):
+        want = bo.short_conv(p["x"][b * N:(b + 1) * N], p["w"], p["bias"], p["tail0"][b], dy=dy[b], dtail=dtail[b])
+        bo.check(g["dx"][b], want["dx"], io, f"dx of sequence {b}")
+        bo.check(g["dtail0"][b], want["dtail0"], io, f"dtail0 of sequence {b}")
+        part = {k: want[k] for k in ("dw", "dbias")}
+        total = part if total is None else {k: total[k] + part[k] for k in part}
+    for k, v in total.items():
+        bo.check(g[k], v, "f32", k)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_conv_backward_left_out(io):
+    p = conv_inputs(io, 90, 40, 4, 1)
+    dy = draw(5, (1, 90, 40), io)
+    g = gret.short_conv_backward(p["x"][None], p["w"], None, dy, activation="none")
+    want = bo.short_conv(p["x"], p["w"], swish=False, dy=dy[0])
+    assert g["dbias"] is None and g["dtail0"] is None
+    bo.check(g["dx"][0], want["dx"], io, "dx")
+    bo.check(g["dw"], want["dw"], "f32", "dw")
+
+
 # --------------------------------------------------------------- selective scan
 def scan_inputs(io, rows, D, n, seqs, seed=2):
     return dict(u=draw(1, (rows, D), io, seed=seed), dt=draw(2, (rows, D), io, seed=seed),
@@ -229,6 +258,61 @@ def test_scan_step(io, n, S, D):
     assert h2 is h0 and torch.equal(h0, apart) and torch.equal(o, o2)
 
 
+SUMS = ("dA", "dskip", "ddt_bias")
+
+
+def check_scan_backward(io, p, do, dh, g, B, N):
+    total = None
+    for b in range(B):
+        want = bo.selective_scan(**scan_rows(p, b * N, (b + 1) * N, b), do=do[b], dh_final=None if dh is None else dh[b])
+        for k in ("du", "ddt", "dB", "dC", "dz"):
+            if g[k] is not None:
+                bo.check(g[k][b], want[k], io, f"{k} of sequence {b}")
+        if g["dh0"] is not None:
+            bo.check(g["dh0"][b], want["dh0"], "f32", f"dh0 of sequence {b}")
+        total = {k: want[k] if total is None else total[k] + want[k] for k in SUMS}
+    for k in SUMS:
+        if g[k] is not None:
+            bo.check(g[k], total[k], "f32", k)
+
+
+def scan_backward_call(p, do, B, N, **kw):
+    q = {k: v.unflatten(0, (B, N)) if k in ROWS and v is not None else v for k, v in p.items()}
+    return gret.selective_scan_backward(**q, do=do, **kw)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("B,N,D", [(1, 1, 8), (2, 33, 72), (1, 150, 40), (3, 16, 136)])
+def test_scan_backward(io, n, B, N, D):
+    p = scan_inputs(io, B * N, D, n, B)
+    do, dh = draw(10, (B, N, D), io), draw(11, (B, D, n))
+    g = scan_backward_call(p, do, B, N, dh_final=dh)
+    check_scan_backward(io, p, do, dh, g, B, N)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("without", ["skip", "z", "dt_bias", "h0"])
+def test_scan_backward_left_out_and_strided(io, without):
+    B, N, D, n = 2, 70, 136, 16
+    p = scan_inputs(io, B * N, D, n, B)
+    p[without] = None
+    do = draw(10, (B, N, D), io)
+    q = {k: columns(v) if k in ROWS and v is not None else v for k, v in p.items()}
+    g = scan_backward_call(q, do, B, N)
+    assert (g["dh0"] is None) == (without == "h0") and (g["dz"] is None) == (without == "z")
+    check_scan_backward(io, p, do, None, g, B, N)
+    again = scan_backward_call(q, do, B, N)
+    for k, v in g.items():
+        assert v is None or torch.equal(v, again[k]), k          # the same bits every time
+
+
+def test_scan_backward_long():
+    p = scan_inputs("f32", 1500, 16, 16, 1)
+    do, dh = draw(10, (1, 1500, 16)), draw(11, (1, 16, 16))
+    check_scan_backward("f32", p, do, dh, scan_backward_call(p, do, 1, 1500, dh_final=dh), 1, 1500)
+
+
 # ---------------------------------------------------------------- residual norm
 def norm_inputs(io, stream, T, D, seed=3):
     p = dict(x=draw(1, (T, D), stream, std=2.0, seed=seed), y=draw(2, (T, D), io, seed=seed),
@@ -284,6 +368,35 @@ def test_norm_in_place_and_empty_rows():
     x = p["x"].clone()
     r2, n2 = gret.residual_norm(**dict(p, x=x), r=x)
     assert r2 is x and torch.equal(x, r) and torch.equal(n, n2)
+
+
+@pytest.mark.parametrize("io,stream", KINDS)
+@pytest.mark.parametrize("T,D", [(1, 8), (3, 72), (700, 264), (5, 2048), (2, 4104), (3, 8192)])
+def test_norm_backward(io, stream, T, D):
+    p = norm_inputs(io, stream, T, D)
+    dr, dn = draw(8, (T, D), stream), draw(9, (T, D), io)
+    g = gret.residual_norm_backward(**p, dr=dr, dn=dn)
+    want = bo.residual_norm(**p, dr=dr, dn=dn)
+    for k, v in want.items():
+        bo.check(g[k], v, stream if k == "dx" else io if k in ("dy", "dgate") else "f32", k)
+
+
+@pytest.mark.parametrize("io,stream", KINDS)
+@pytest.mark.parametrize("without", [("gate",), ("scale",), ("w_post",), ("w_next", "dn"), ("dr",),
+                                     ("gate", "scale", "w_post"), ("gate", "scale", "w_post", "y")])
+def test_norm_backward_left_out_and_strided(io, stream, without):
+    T, D = 37, 264
+    p = dict(norm_inputs(io, stream, T, D), dr=draw(8, (T, D), stream), dn=draw(9, (T, D), io))
+    for k in without:
+        p[k] = None
+    q = {k: columns(v) if k in ("x", "y", "gate") and v is not None else v for k, v in p.items()}
+    g = gret.residual_norm_backward(**q)
+    want = bo.residual_norm(**p)
+    for k, v in want.items():
+        if p[k[1:]] is None:
+            assert g[k] is None
+        else:
+            bo.check(g[k], v, stream if k == "dx" else io if k in ("dy", "dgate") else "f32", k)
 
 
 # --------------------------------------------------------------------- together
