@@ -35,9 +35,8 @@ bool overlap(const void* p, const void* q, size_t bytes) {
     return p && q && a < b + bytes && b < a + bytes;
 }
 
-bool on_device_grid(const Rows& r) { return slots_of(r) <= 0x7fffffffLL; }
-
 constexpr long long kMaxRows = 1LL << 31;
+constexpr int kMaxChannels = 1 << 16;       // channel blocks are a grid's second dimension
 
 gret_status rows_ok(const Rows& r) {
     if (r.B <= 0 || r.N <= 0 || (r.cu && r.total <= 0)) return GRET_ERR_INVALID_ARG;
@@ -56,7 +55,7 @@ gret_status conv_check(const ConvArgs& a) {
     if (a.D <= 0 || a.K <= 0) return GRET_ERR_INVALID_ARG;
     if (gret_status e = rows_ok(a.rows)) return e;
     if (!all_aligned(a.x, a.w, a.bias, a.tail0, a.y, a.tail)) return GRET_ERR_INVALID_ARG;
-    if (a.D % kVec != 0 || a.K < 2 || a.K > 4) return GRET_ERR_UNSUPPORTED;
+    if (a.D % kVec != 0 || a.D > kMaxChannels || a.K < 2 || a.K > 4) return GRET_ERR_UNSUPPORTED;
     if (!stride_ok(a.ldx, a.D, a.io)) return GRET_ERR_INVALID_ARG;
     return GRET_OK;
 }
@@ -77,7 +76,7 @@ gret_status scan_check(const ScanArgs& a) {
     if (a.D <= 0 || a.n <= 0) return GRET_ERR_INVALID_ARG;
     if (gret_status e = rows_ok(a.rows)) return e;
     if (!all_aligned(a.u, a.dt, a.A, a.Bm, a.Cm, a.skip, a.z, a.dt_bias, a.h0, a.o, a.h)) return GRET_ERR_INVALID_ARG;
-    if (a.D % kVec != 0 || !selective_states_supported(a.n)) return GRET_ERR_UNSUPPORTED;
+    if (a.D % kVec != 0 || a.D > kMaxChannels || !selective_states_supported(a.n)) return GRET_ERR_UNSUPPORTED;
     if (!stride_ok(a.ldu, a.D, a.io) || !stride_ok(a.lddt, a.D, a.io) || !stride_ok(a.ldb, a.n, a.io) ||
         !stride_ok(a.ldc, a.n, a.io) || (a.z && !stride_ok(a.ldz, a.D, a.io)))
         return GRET_ERR_INVALID_ARG;
