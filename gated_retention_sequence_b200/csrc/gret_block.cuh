@@ -123,6 +123,65 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// One special function each: 2^x (2 units in the last place) and 1/x.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sigmoid with two special functions: 1 / (1 + 2^(-x log2 e)).  An overflow of
+// the power gives 0, as it should.
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_approx(1.0f + exp2_approx(-kLog2e * x)); }
+
+// softplus of two numbers, max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].
+// log1p(e) = e P(e) with P of degree 9, the minimax fit of log1p(e) / e on
+// [0, 1] in relative error by Remez exchange (0.1 units; 2.5 units with P in
+// fp32, measured over the interval), so that small steps keep their relative
+// precision; one special function each instead of two.
+__device__ __forceinline__ float2 softplus2(float2 x) {
+    const float2 e = make_float2(exp2_approx(-kLog2e * fabsf(x.x)), exp2_approx(-kLog2e * fabsf(x.y)));
+    float2 p = both(-0.0032440251670777798f);
+    p = fma2(p, e, both(0.01985146291553974f));
+    p = fma2(p, e, both(-0.05695953592658043f));
+    p = fma2(p, e, both(0.10603655129671097f));
+    p = fma2(p, e, both(-0.15305592119693756f));
+    p = fma2(p, e, both(0.1967593878507614f));
+    p = fma2(p, e, both(-0.24954134225845337f));
+    p = fma2(p, e, both(0.3332996368408203f));
+    p = fma2(p, e, both(-0.4999990165233612f));
+    p = fma2(p, e, both(1.0f));
+    return fma2(p, e, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
+
 // d/dv of v sigmoid(v)
 __device__ __forceinline__ float swish_slope(float v, float sig) { return sig * (1.0f + v * (1.0f - sig)); }
 

@@ -6,6 +6,8 @@
 //   o[t,d]     = (sum_i C[t,i] h[t,d,i] + skip[d] u[t,d]) swish(z[t,d])
 //
 // B and C are shared by all channels of a token.
+#include <math.h>
+
 #include "gret_block.cuh"
 
 namespace gret {
@@ -13,22 +15,20 @@ namespace {
 
 constexpr int kStepThreads = 128;
 
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-
-// How a warp lays out its channels and states: a lane holds kLane states of CPL
-// channels, n / kLane lanes share a channel, and the warp's kWidth channels are
-// walked kTile tokens at a time.
-constexpr int kLane = 4, kTile = 16, kWarps = 4;
+// How a warp lays out its channels and states: a lane holds SPL states of two
+// channels, n / SPL lanes share a channel, and the warp's W channels are walked
+// kTile tokens at a time, kGroup of them between two rounds of shuffles.
+constexpr int kTile = 16, kWarps = 4, kGroup = 4, kPair = 2;
 template <int NS>
 struct Layout {
-    static constexpr int CPL = NS == 8 ? 2 : 4;            // channels of a lane
-    static constexpr int LPC = NS / kLane;                 // lanes of a channel
-    static constexpr int W = 32 / LPC * CPL;               // channels of a warp: 32, 32, 16, 8
-    static constexpr int LD = W + 4;                       // shared row: 16-byte steps over the banks
-    static constexpr int VR = W / kVec;                    // 16-byte vectors of a row
-    static constexpr int V = (kTile * VR + 31) / 32;       // and of a lane
-    static constexpr int BV = (kTile * NS / kVec + 31) / 32;   // vectors of B (of C) a lane stages
-    static constexpr int FLOATS = 3 * kTile * LD + 2 * kTile * NS;   // shared floats of a warp
+    static constexpr int SPL = NS >= 32 ? 8 : 4;            // states of a lane
+    static constexpr int LPC = NS / SPL;                    // lanes of a channel
+    static constexpr int W = 32 / LPC * kPair;              // channels of a warp: 32, 16, 16, 8
+    static constexpr int LD = 2 * W + 4, LY = W + 4;        // shared rows: 16-byte steps over the banks
+    static constexpr int VR = W / kVec;                     // 16-byte vectors of a row
+    static constexpr int V = (kTile * VR + 31) / 32;        // and of a lane
+    static constexpr int BV = (kTile * NS / kVec + 31) / 32;    // vectors of B (of C) a lane stages
+    static constexpr int FLOATS = kTile * (LD + 2 * NS + LY);   // shared floats of a warp
 };
 
 // Eight values as they lie in memory.
@@ -52,68 +52,39 @@ template <> struct Raw<float> {
     }
 };
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(r))
-        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long&>(r))
-        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
-          "l"(reinterpret_cast<unsigned long long&>(c)));
-    return r;
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-
 // A warp walks one slot's tokens for its channels.  Each tile of tokens is
 // staged first (delta and delta u of the warp's channels, B and C), then
-// scanned token by token from shared memory, then gated and stored; the next
-// tile's inputs are in flight meanwhile.  kFinal: the outputs, from the state
-// before the slot (the folded one of a cut sequence).  Otherwise the state that
-// the slot alone leaves, from zero, and the sum of its steps.
+// scanned from shared memory, then gated and stored; the next tile's inputs are
+// in flight meanwhile.  kFinal: the outputs, from the state before the slot.
+// Otherwise the state that the slot alone leaves, from zero, and the sum of its
+// steps.  `leave`: where the state after the slot goes as well.
 template <typename T, int NS, bool kFinal>
-__global__ void __launch_bounds__(kWarps * 32, 3) selective_scan_kernel(const ScanArgs a, float* local, float* steps) {
+__device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* shared, const float* before, float* leave,
+                                     float* steps) {
     using L = Layout<NS>;
-    constexpr int CPL = L::CPL, LPC = L::LPC, W = L::W, LD = L::LD, V = L::V, BV = L::BV, P = CPL / 2;
-    __shared__ __align__(16) float smem[kWarps][L::FLOATS];
-    const Slot f = find_slot(a.rows, blockIdx.x);
+    constexpr int SPL = L::SPL, LPC = L::LPC, W = L::W, LD = L::LD, LY = L::LY, V = L::V, BV = L::BV, H = SPL / 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.D;
     const int d0 = (blockIdx.y * kWarps + warp) * W;
-    if (f.b < 0 || d0 >= D) return;
-    if (!kFinal && f.s + 1 >= f.segs) return;               // nothing comes after it
-    float *sd = smem[warp], *su = sd + kTile * LD, *sy = su + kTile * LD, *sb = sy + kTile * LD, *sc = sb + kTile * NS;
+    if (d0 >= D) return;
+    // per token: (delta, delta, delta u, delta u) of each two channels; B; C; the sums over the states
+    float *sd = shared + warp * L::FLOATS, *sb = sd + kTile * LD, *sc = sb + kTile * NS, *sy = sc + kTile * NS;
 
-    const int q = lane % LPC, g = lane / LPC;               // states 4 q .., channels d0 + g CPL ..
-    float2 A[P][kLane], h[P][kLane];
-    const float* h0 = nullptr;
-    if (kFinal) {
-        if (f.segs > 1 && f.s > 0)
-            h0 = local + (size_t)(blockIdx.x - 1) * D * NS;
-        else if (a.h0)
-            h0 = a.h0 + (size_t)f.b * D * NS;
-    }
+    const int q = lane % LPC, g = lane / LPC;               // states q SPL .., channels d0 + 2 g ..
+    float2 A[kPair][H], h[kPair][H];                        // two states each
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-        const int d = d0 + g * CPL + c;
-        float4 av = make_float4(0.f, 0.f, 0.f, 0.f), hv = av;
-        if (d < D) {
-            av = *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q * kLane);
-            if (h0) hv = *reinterpret_cast<const float4*>(h0 + (size_t)d * NS + q * kLane);
-        }
-        const float as[4] = {av.x, av.y, av.z, av.w}, hs[4] = {hv.x, hv.y, hv.z, hv.w};
+    for (int c = 0; c < kPair; ++c) {
+        const int d = d0 + g * kPair + c;
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) {
-            (c & 1 ? A[c / 2][i].y : A[c / 2][i].x) = as[i] * kLog2e;
-            (c & 1 ? h[c / 2][i].y : h[c / 2][i].x) = hs[i];
+        for (int i = 0; i < H; i += 2) {
+            float4 av = make_float4(0.f, 0.f, 0.f, 0.f), hv = av;
+            if (d < D) {
+                av = *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q * SPL + 2 * i);
+                if (before) hv = *reinterpret_cast<const float4*>(before + (size_t)d * NS + q * SPL + 2 * i);
+            }
+            A[c][i] = make_float2(av.x * kLog2e, av.y * kLog2e);
+            A[c][i + 1] = make_float2(av.z * kLog2e, av.w * kLog2e);
+            h[c][i] = make_float2(hv.x, hv.y);
+            h[c][i + 1] = make_float2(hv.z, hv.w);
         }
     }
 
@@ -147,6 +118,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) selective_scan_kernel(const Sc
             if (br + j * BSTEP < kTile && t < f.len) {
                 nb[j].load(B + t * a.ldb);
                 if (kFinal) nc[j].load(C + t * a.ldc);
+            } else {
+                nb[j].zero();
+                nc[j].zero();
             }
         }
     };
@@ -166,20 +140,32 @@ __global__ void __launch_bounds__(kWarps * 32, 3) selective_scan_kernel(const Sc
             nu[j].get(x);
             nd[j].get(s);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                s[e] = softplus(s[e] + bias[e]);
-                x[e] *= s[e];
-                if (!kFinal && von && r < len) total[e] += s[e];
+            for (int e = 0; e < kVec; e += 2) {
+                const float2 d = softplus2(make_float2(s[e] + bias[e], s[e + 1] + bias[e + 1]));
+                s[e] = d.x;
+                s[e + 1] = d.y;
+                x[e] *= d.x;
+                x[e + 1] *= d.y;
+                if (!kFinal && von && r < len) {
+                    total[e] += d.x;
+                    total[e + 1] += d.y;
+                }
+            }
+            if (r >= len) {                                 // past the end: a step of nothing
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) s[e] = x[e] = 0.f;
             }
             if (V > 1 || lane < kTile * L::VR) {
-                store8(sd + r * LD + (vc - d0), s);
-                store8(su + r * LD + (vc - d0), x);
+                float* to = sd + r * LD + 2 * (vc - d0);
+#pragma unroll
+                for (int e = 0; e < kVec; e += 2)
+                    *reinterpret_cast<float4*>(to + 2 * e) = make_float4(s[e], s[e + 1], x[e], x[e + 1]);
             }
         }
 #pragma unroll
         for (int j = 0; j < BV; ++j) {
             const int r = br + j * BSTEP;
-            if (r < len) {
+            if (r < kTile) {
                 float x[kVec];
                 nb[j].get(x);
                 store8(sb + r * NS + bc, x);
@@ -191,61 +177,53 @@ __global__ void __launch_bounds__(kWarps * 32, 3) selective_scan_kernel(const Sc
         }
         __syncwarp();
         if (t0 + kTile < f.len) fetch(t0 + kTile);
-#pragma unroll 4
-        for (int t = 0; t < len; ++t) {
-            float dv[CPL], uv[CPL];
-            if (CPL == 4) {
-                *reinterpret_cast<float4*>(dv) = *reinterpret_cast<const float4*>(sd + t * LD + g * CPL);
-                *reinterpret_cast<float4*>(uv) = *reinterpret_cast<const float4*>(su + t * LD + g * CPL);
-            } else {
-                *reinterpret_cast<float2*>(dv) = *reinterpret_cast<const float2*>(sd + t * LD + g * CPL);
-                *reinterpret_cast<float2*>(uv) = *reinterpret_cast<const float2*>(su + t * LD + g * CPL);
-            }
-            const float4 bv = *reinterpret_cast<const float4*>(sb + t * NS + q * kLane);
-            const float bs[4] = {bv.x, bv.y, bv.z, bv.w};
-            float4 cv = bv;
-            if (kFinal) cv = *reinterpret_cast<const float4*>(sc + t * NS + q * kLane);
-            const float cs[4] = {cv.x, cv.y, cv.z, cv.w};
-            float2 y[P];
+        for (int t1 = 0; t1 < len; t1 += kGroup) {
+            float v[kGroup * kPair];
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const float2 dd = make_float2(dv[2 * p], dv[2 * p + 1]), uu = make_float2(uv[2 * p], uv[2 * p + 1]);
-                y[p] = make_float2(0.f, 0.f);
+            for (int k = 0; k < kGroup; ++k) {
+                const int t = t1 + k;
+                const float4 du = *reinterpret_cast<const float4*>(sd + t * LD + g * 4);
+                const float dv[2] = {du.x, du.y}, uv[2] = {du.z, du.w};
+                float2 bs[H], cs[H], y[kPair];
 #pragma unroll
-                for (int i = 0; i < kLane; ++i) {
-                    const float2 x = mul2(dd, A[p][i]);
-                    const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-                    h[p][i] = fma2(e, h[p][i], mul2(uu, make_float2(bs[i], bs[i])));
-                    if (kFinal) y[p] = fma2(make_float2(cs[i], cs[i]), h[p][i], y[p]);
+                for (int i = 0; i < H; i += 2) {
+                    const float4 bv = *reinterpret_cast<const float4*>(sb + t * NS + q * SPL + 2 * i);
+                    bs[i] = make_float2(bv.x, bv.y);
+                    bs[i + 1] = make_float2(bv.z, bv.w);
+                    if (kFinal) {
+                        const float4 cv = *reinterpret_cast<const float4*>(sc + t * NS + q * SPL + 2 * i);
+                        cs[i] = make_float2(cv.x, cv.y);
+                        cs[i + 1] = make_float2(cv.z, cv.w);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < kPair; ++c) {
+                    const float2 dd = both(dv[c]), uu = both(uv[c]);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float2 x = mul2(dd, A[c][i]);
+                        const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                        h[c][i] = fma2(e, h[c][i], mul2(uu, bs[i]));
+                        if (kFinal) y[c] = i == 0 ? mul2(cs[i], h[c][i]) : fma2(cs[i], h[c][i], y[c]);
+                    }
+                    if (kFinal) v[k * kPair + c] = y[c].x + y[c].y;
                 }
             }
             if (kFinal) {
-                // the lanes of a channel add up their states; lane q keeps channel q mod CPL
-                float v[CPL];
+                // the lanes of a channel add up their states; lane q keeps the group's values q R ..
+                constexpr int R = kGroup * kPair / LPC;
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    v[2 * p] = y[p].x;
-                    v[2 * p + 1] = y[p].y;
-                }
-                int m = LPC / 2;
-#pragma unroll
-                for (int half = CPL / 2; half > 0; half /= 2) {
-                    if (m == 0) break;
+                for (int m = LPC / 2, half = kGroup * kPair / 2; m > 0; m /= 2, half /= 2) {
                     const bool up = (q & m) != 0;
 #pragma unroll
                     for (int c = 0; c < half; ++c) {
                         const float keep = up ? v[c + half] : v[c], send = up ? v[c] : v[c + half];
                         v[c] = keep + __shfl_xor_sync(0xffffffffu, send, m);
                     }
-                    m /= 2;
                 }
-                for (; m > 0; m /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
-                if (LPC >= CPL) {
-                    // the channel's bits are the highest of q
-                    if (q % (LPC / CPL) == 0) sy[t * LD + g * CPL + q / (LPC / CPL)] = v[0];
-                } else {
-                    sy[t * LD + g * CPL + q] = v[0];
-                }
+#pragma unroll
+                for (int k = 0; k < R; ++k)
+                    sy[(t1 + (q * R + k) / kPair) * LY + g * kPair + (q * R + k) % kPair] = v[k];
             }
         }
         __syncwarp();
@@ -257,30 +235,29 @@ __global__ void __launch_bounds__(kWarps * 32, 3) selective_scan_kernel(const Sc
                 const int r = vr + j * VSTEP;
                 if (!von || r >= len) continue;
                 float y[kVec], x[kVec];
-                load8(sy + r * LD + (vc - d0), y);
+                load8(sy + r * LY + (vc - d0), y);
                 cu[j].get(x);
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) y[e] = fmaf(skip[e], x[e], y[e]);
                 if (a.z) {
                     cz[j].get(x);
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) y[e] *= x[e] * sigmoidf_(x[e]);
+                    for (int e = 0; e < kVec; ++e) y[e] *= x[e] * sigmoid_fast(x[e]);
                 }
                 store8(static_cast<T*>(a.o) + (row0 + t0 + r) * D + vc, y);
             }
             __syncwarp();
         }
     }
-    float* to = kFinal ? (a.h && f.s == max(f.segs, 1) - 1 ? a.h + (size_t)f.b * D * NS : nullptr)
-                       : local + (size_t)blockIdx.x * D * NS;
-    if (to) {
+    if (leave) {
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-            const int d = d0 + g * CPL + c;
-            float o[4];
+        for (int c = 0; c < kPair; ++c) {
+            const int d = d0 + g * kPair + c;
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) o[i] = c & 1 ? h[c / 2][i].y : h[c / 2][i].x;
-            if (d < D) *reinterpret_cast<float4*>(to + (size_t)d * NS + q * kLane) = make_float4(o[0], o[1], o[2], o[3]);
+            for (int i = 0; i < H; i += 2)
+                if (d < D)
+                    *reinterpret_cast<float4*>(leave + (size_t)d * NS + q * SPL + 2 * i) =
+                        make_float4(h[c][i].x, h[c][i].y, h[c][i + 1].x, h[c][i + 1].y);
         }
     }
     if (!kFinal) {
@@ -289,12 +266,34 @@ __global__ void __launch_bounds__(kWarps * 32, 3) selective_scan_kernel(const Sc
         for (int m = L::VR; m < 32; m *= 2)
 #pragma unroll
             for (int e = 0; e < kVec; ++e) total[e] += __shfl_xor_sync(0xffffffffu, total[e], m);
-        if (lane < L::VR && vc < D) store8(steps + (size_t)blockIdx.x * D + vc, total);
+        if (lane < L::VR && vc < D) store8(steps + vc, total);
     }
 }
 
-// The state before every segment but the first, from the local ones:
-// h <- exp(A sum of the segment's steps) h + local, over local in place.
+// A sequence that is cut is walked in two launches.  The first gives the first
+// segment's outputs, whose state before is known, and the local states of the
+// segments between the first and the last; the second, after the fold, the
+// other segments' outputs.  So two segments cost no token twice.
+template <typename T, int NS, bool kFirst>
+__global__ void __launch_bounds__(kWarps * 32, NS >= 32 ? 3 : 4) selective_scan_kernel(const ScanArgs a, float* local,
+                                                                                       float* steps) {
+    __shared__ __align__(16) float shared[kWarps * Layout<NS>::FLOATS];
+    const Slot f = find_slot(a.rows, blockIdx.x);
+    const bool last = f.s + 1 >= f.segs;
+    if (f.b < 0 || (kFirst ? f.s > 0 && last : f.s == 0)) return;
+    const size_t state = (size_t)a.D * NS;
+    float* leave = !last ? local + blockIdx.x * state : a.h ? a.h + f.b * state : nullptr;
+    if (!kFirst)
+        walk<T, NS, true>(a, f, shared, local + (blockIdx.x - 1) * state, last ? leave : nullptr, nullptr);
+    else if (f.s == 0)
+        walk<T, NS, true>(a, f, shared, a.h0 ? a.h0 + f.b * state : nullptr, leave, nullptr);
+    else
+        walk<T, NS, false>(a, f, shared, nullptr, leave, steps + (size_t)blockIdx.x * a.D);
+}
+
+// The state after every segment but the last, from the first one's and the
+// local ones of the others: h <- exp(A sum of the segment's steps) h + local,
+// over local in place.
 template <int NS>
 __global__ void __launch_bounds__(128) fold_kernel(const ScanArgs a, float* local, const float* steps) {
     const int i = blockIdx.y * 128 + threadIdx.x, b = blockIdx.x;
@@ -307,16 +306,15 @@ __global__ void __launch_bounds__(128) fold_kernel(const ScanArgs a, float* loca
         len = min(len, a.rows.N);
     }
     const int cuts = (len + a.rows.seg - 1) / a.rows.seg - 1;
-    if (cuts <= 0) return;
+    if (cuts <= 1) return;
     const long long slot = slot_start(a.rows, b);
     float4 A = *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q);
     A = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
-    float4 h = a.h0 ? *reinterpret_cast<const float4*>(a.h0 + ((size_t)b * a.D + d) * NS + q)
-                    : make_float4(0.f, 0.f, 0.f, 0.f);
     float* l = local + ((size_t)slot * a.D + d) * NS + q;
     const float* s = steps + (size_t)slot * a.D + d;
+    float4 h = *reinterpret_cast<const float4*>(l);
     constexpr int U = 8;
-    for (int k = 0; k < cuts; k += U) {
+    for (int k = 1; k < cuts; k += U) {
         float4 v[U];
         float w[U];
 #pragma unroll
@@ -337,20 +335,26 @@ __global__ void __launch_bounds__(128) fold_kernel(const ScanArgs a, float* loca
     }
 }
 
-// Tokens of a segment: the whole sequence where the channels of all sequences
-// give the GPU enough warps, else as many cuts as fill it (each cut token is
-// scanned twice).
+// Tokens of a segment: N leaves the sequences whole.  Measured with 16 states,
+// a token costs a warp 88 ns when it has its scheduler to itself and 62 ns a
+// warp when two share it; many warps bring that to 53 ns.  A whole sequence
+// therefore costs its length times the former, and cut ones the latter over all
+// tokens, most of them twice.  For example, in us whole / cut: 1 x 4096 tokens
+// x 4096 channels 358 / 189, 2 x 1024 x 4096 94 / 100, 4 x 4096 x 4096 514 /
+// 594, 38 packed sequences of 16384 tokens x 4096 channels 620 / 560.  The
+// segment gives some 8192 warps, about four times what the GPU holds: fewer
+// leave it idle at the end, more cost staging.
 int segment(int B, int N, int total, int D, int n, bool packed, int num_sms) {
-    const int width = n <= 16 ? 32 : n == 32 ? 16 : 8;
-    const long long tokens = packed ? total : (long long)B * N;
-    const long long per_seq = ((long long)D + width - 1) / width;
-    const long long want = 12LL * num_sms;
-    const long long have = per_seq * B;
-    if (!packed && have >= want / 2) return N;
-    long long seg = (tokens * per_seq + want - 1) / want;
-    seg = (seg + kTile - 1) / kTile * kTile;
+    const int width = n == 8 ? 32 : n == 64 ? 8 : 16;
+    const double warps = (D + width - 1) / width, tokens = packed ? (double)total : (double)B * N;
+    const double schedulers = 4.0 * num_sms, filled = 53e-3 * tokens * warps / schedulers;
+    const double shared = B * warps / schedulers;
+    const double whole = packed ? filled + 88e-3 * N : N * (shared <= 1 ? 88e-3 : 62e-3 * ceil(shared));
+    long long seg = (long long)ceil(tokens * warps / 8192 / kTile) * kTile;
     if (seg < 4 * kTile) seg = 4 * kTile;
-    return seg >= N ? N : (int)seg;
+    if (seg >= N) return N;
+    const double again = packed ? 1.4 : 2.0 - (double)seg / N;
+    return whole <= 1.1 * again * filled + 10 ? N : (int)seg;
 }
 
 // One token per sequence: the states are read and written once, 16 bytes at a
@@ -365,7 +369,7 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Scan
     const float4 A = *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q);
     float4 h = on ? *reinterpret_cast<const float4*>(a.h0 + unit * NS + q) : make_float4(0.f, 0.f, 0.f, 0.f);
     const float u = to_f32(static_cast<const T*>(a.u)[b * a.ldu + d]);
-    const float delta = softplus(to_f32(static_cast<const T*>(a.dt)[b * a.lddt + d]) + (a.dt_bias ? a.dt_bias[d] : 0.f));
+    const float delta = softplus2(both(to_f32(static_cast<const T*>(a.dt)[b * a.lddt + d]) + (a.dt_bias ? a.dt_bias[d] : 0.f))).x;
     const T* B = static_cast<const T*>(a.Bm) + b * a.ldb + q;
     const T* C = static_cast<const T*>(a.Cm) + b * a.ldc + q;
     const float du = delta * u;
@@ -389,17 +393,18 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Scan
 }
 
 template <typename T, int NS>
-cudaError_t scan(ScanArgs a, int num_sms, cudaStream_t s) {
-    a.rows.seg = segment(a.rows.B, a.rows.N, a.rows.total, a.D, NS, a.rows.cu != nullptr, num_sms);
+cudaError_t scan(const ScanArgs& a, cudaStream_t s) {
+    constexpr int W = Layout<NS>::W;
     const long long slots = slots_of(a.rows);
-    const dim3 grid((unsigned)slots, (a.D + kWarps * Layout<NS>::W - 1) / (kWarps * Layout<NS>::W));
+    const dim3 grid((unsigned)slots, (a.D + kWarps * W - 1) / (kWarps * W));
     float* local = static_cast<float*>(a.workspace);
     float* steps = local + (size_t)slots * a.D * NS;
-    if (a.rows.seg < a.rows.N) {
-        selective_scan_kernel<T, NS, false><<<grid, kWarps * 32, 0, s>>>(a, local, steps);
-        fold_kernel<NS><<<dim3(a.rows.B, (a.D * (NS / 4) + 127) / 128), 128, 0, s>>>(a, local, steps);
-    }
     selective_scan_kernel<T, NS, true><<<grid, kWarps * 32, 0, s>>>(a, local, steps);
+    if (a.rows.seg < a.rows.N) {
+        if (2LL * a.rows.seg < a.rows.N)
+            fold_kernel<NS><<<dim3(a.rows.B, (a.D * (NS / 4) + 127) / 128), 128, 0, s>>>(a, local, steps);
+        selective_scan_kernel<T, NS, false><<<grid, kWarps * 32, 0, s>>>(a, local, steps);
+    }
     return cudaGetLastError();
 }
 
@@ -415,19 +420,20 @@ cudaError_t step(const ScanArgs& a, cudaStream_t s) {
 bool selective_states_supported(int n) { return n == 8 || n == 16 || n == 32 || n == 64; }
 
 size_t selective_scan_ws_bytes(int B, int N, int total, int D, int n, bool packed, int num_sms) {
-    Rows r = {nullptr, B, N, total, segment(B, N, total, D, n, packed, num_sms)};
-    if (r.seg >= N) return 0;
-    const long long slots = packed ? (long long)total / r.seg + B : slots_of(r);
+    const int seg = segment(B, N, total, D, n, packed, num_sms);
+    if (seg >= N) return 0;
+    const long long slots = packed ? (long long)total / seg + B : (long long)B * ((N + seg - 1) / seg);
     return align256((size_t)slots * D * (n + 1) * sizeof(float));
 }
 
 cudaError_t launch_selective_scan(ScanArgs a, int num_sms, cudaStream_t s) {
+    a.rows.seg = segment(a.rows.B, a.rows.N, a.rows.total, a.D, a.n, a.rows.cu != nullptr, num_sms);
     const bool bf = a.io == GRET_BF16;
     switch (a.n) {
-        case 8: return bf ? scan<__nv_bfloat16, 8>(a, num_sms, s) : scan<float, 8>(a, num_sms, s);
-        case 16: return bf ? scan<__nv_bfloat16, 16>(a, num_sms, s) : scan<float, 16>(a, num_sms, s);
-        case 32: return bf ? scan<__nv_bfloat16, 32>(a, num_sms, s) : scan<float, 32>(a, num_sms, s);
-        default: return bf ? scan<__nv_bfloat16, 64>(a, num_sms, s) : scan<float, 64>(a, num_sms, s);
+        case 8: return bf ? scan<__nv_bfloat16, 8>(a, s) : scan<float, 8>(a, s);
+        case 16: return bf ? scan<__nv_bfloat16, 16>(a, s) : scan<float, 16>(a, s);
+        case 32: return bf ? scan<__nv_bfloat16, 32>(a, s) : scan<float, 32>(a, s);
+        default: return bf ? scan<__nv_bfloat16, 64>(a, s) : scan<float, 64>(a, s);
     }
 }
 
