@@ -6,181 +6,527 @@
 //   du = skip dy + delta s,  ddelta = sum_i A g a h[t-1] + u s,  ddt = ddelta sigmoid(dt + dt_bias)
 //   dA = sum_t delta g a h[t-1],  dskip = sum_t dy u,  ddt_bias = sum_t ddt,  dh0 = a[0] g[0]
 //
-// One pass forward leaves the state before every segment of kSeg tokens; one
-// pass backward forms a segment's states again and walks it in reverse.
-#include "gret_block.cuh"
+// Both recurrences are linear, so the sequence is cut into short segments that
+// are independent but for two states each:
+//
+//   ends     per segment, walked once: the state it leaves from zero, what it
+//            hands back from a zero gradient past its end (sum of P C dy, P the
+//            product of the decays up to t), and the sum of its steps
+//   fold     per channel and state, forwards and backwards over the segments:
+//            the state before each and the gradient carried into each
+//   walk     per segment: a sweep keeps the state before every group of
+//            kGroup tokens in shared memory; then group by group from the last,
+//            the group's states and decays are formed again in registers and
+//            the group is walked in reverse
+//   join     dB, dC: the channel blocks' shares; column sums for the parameters
+//
+// Three exponentials per state and token, all of them parallel over the tokens.
+#include "gret_selective.cuh"
 
 namespace gret {
 namespace {
 
-constexpr int kSeg = 16;
-constexpr int kThreads = 32;
+template <int NS>
+struct Layout {
+    static constexpr int SPL = NS == 64 ? 8 : 4;            // states of a lane
+    static constexpr int LPC = NS / SPL;                    // lanes of a channel
+    static constexpr int W = 32 / LPC * kPair;              // channels of a warp: 32, 16, 8, 8
+    static constexpr int GROUP = NS == 64 ? 2 : 4;          // tokens walked in registers
+    static constexpr int SEG = NS == 64 ? 16 : 32;          // tokens of a segment
+    static constexpr int LD = 2 * W + 4, LY = W + 4;        // shared rows: 16-byte steps over the banks
+    static constexpr int VR = W / kVec;                     // 16-byte vectors of a row
+    static constexpr int V = (SEG * VR + 31) / 32;          // and of a lane
+    static constexpr int START = 32 * kPair * SPL;          // floats of a group's start
+    static constexpr int ROWS = SEG * (LD + LY);            // floats a warp stages
+    static constexpr int WARP = ROWS + SEG / GROUP * START;
+    static constexpr int BC = 2 * SEG * NS;                 // B and C of the segment
+    static constexpr int W4 = kScanWarps * W;               // channels of a block
+    static_assert(GROUP * 2 * NS <= START, "a group's dB and dC go where its start was");
+};
 
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+struct Work {
+    float *h, *g, *steps;   // [slots][D][n], [slots][D][n], [slots][D]
+    float *bc;              // [channel blocks][rows][2 n]
+    float *partial;         // [slots][D (n + 2)]
+};
 
+// Stage the segment: (delta, delta, delta u, delta u) of each two channels and
+// dy, of this warp's channels; B and C for the block.  Rows past the end are
+// steps of nothing.  Adds the steps to `total`.
 template <typename T, int NS>
-__global__ void __launch_bounds__(kThreads) states_kernel(const ScanArgs a, float* states) {
-    const int d = blockIdx.x * kThreads + threadIdx.x, b = blockIdx.y, N = a.rows.N, segs = (N + kSeg - 1) / kSeg;
-    if (d >= a.D) return;
-    float h[NS], A[NS];
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        A[i] = a.A[(size_t)d * NS + i];
-        h[i] = a.h0 ? a.h0[((size_t)b * a.D + d) * NS + i] : 0.f;
+__device__ __forceinline__ void stage(const ScanBackwardArgs& g, const Slot& f, int d0, float* sd, float* sy, float* sbc,
+                                      float* total) {
+    using L = Layout<NS>;
+    const ScanArgs& a = g.f;
+    const int lane = threadIdx.x & 31;
+    const long long row0 = f.row0 + f.first;
+    for (int i = threadIdx.x; i < 2 * L::SEG * NS / kVec; i += kScanWarps * 32) {
+        const int which = i / (L::SEG * NS / kVec), j = i % (L::SEG * NS / kVec), r = j / (NS / kVec),
+                  c = j % (NS / kVec) * kVec;
+        float x[kVec] = {};
+        if (r < f.len)
+            load8(which ? static_cast<const T*>(a.Cm) + (row0 + r) * a.ldc + c
+                        : static_cast<const T*>(a.Bm) + (row0 + r) * a.ldb + c, x);
+        store8(sbc + which * L::SEG * NS + r * NS + c, x);
     }
-    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-    for (int t = 0; t < N; ++t) {
-        if (t % kSeg == 0) {
-            float* to = states + (((size_t)b * segs + t / kSeg) * a.D + d) * NS;
+    const int vc = d0 + lane % L::VR * kVec;
+    if (d0 < a.D) {
+        float bias[kVec] = {};
+        if (vc < a.D && a.dt_bias) load8(a.dt_bias + vc, bias);
 #pragma unroll
-            for (int i = 0; i < NS; ++i) to[i] = h[i];
+        for (int j = 0; j < L::V; ++j) {
+            const int r = lane / L::VR + j * (32 / L::VR);
+            if (r >= L::SEG) continue;
+            float u[kVec] = {}, s[kVec] = {}, dy[kVec] = {};
+            if (vc < a.D && r < f.len) {
+                const long long row = row0 + r;
+                load8(static_cast<const T*>(a.dt) + row * a.lddt + vc, s);
+                load8(static_cast<const T*>(a.u) + row * a.ldu + vc, u);
+                load8(static_cast<const T*>(g.dout) + row * a.D + vc, dy);
+                if (a.z) {
+                    float z[kVec];
+                    load8(static_cast<const T*>(a.z) + row * a.ldz + vc, z);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) dy[e] *= z[e] * sigmoid_fast(z[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < kVec; e += 2) {
+                    const float2 d = softplus2(make_float2(s[e] + bias[e], s[e + 1] + bias[e + 1]));
+                    s[e] = d.x;
+                    s[e + 1] = d.y;
+                    u[e] *= d.x;
+                    u[e + 1] *= d.y;
+                    total[e] += d.x;
+                    total[e + 1] += d.y;
+                }
+            }
+            float* to = sd + r * L::LD + 2 * (vc - d0);
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2)
+                *reinterpret_cast<float4*>(to + 2 * e) = make_float4(s[e], s[e + 1], u[e], u[e + 1]);
+            store8(sy + r * L::LY + (vc - d0), dy);
         }
-        const long long row = (long long)b * N + t;
-        const float delta = softplus(to_f32(static_cast<const T*>(a.dt)[row * a.lddt + d]) + bias);
-        const float du = delta * to_f32(static_cast<const T*>(a.u)[row * a.ldu + d]);
-        const T* B = static_cast<const T*>(a.Bm) + row * a.ldb;
+    }
+    __syncthreads();
+}
+
+// Eight channels' sums over the lanes that hold other rows of them.
+template <int VR>
+__device__ __forceinline__ void sum_rows(float* v) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) h[i] = fmaf(expf(delta * A[i]), h[i], du * to_f32(B[i]));
+    for (int m = VR; m < 32; m *= 2)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], m);
+}
+
+template <int H>
+__device__ __forceinline__ void read_states(float2* v, const float* row) {
+#pragma unroll
+    for (int i = 0; i < H; i += 2) {
+        const float4 x = *reinterpret_cast<const float4*>(row + 2 * i);
+        v[i] = make_float2(x.x, x.y);
+        v[i + 1] = make_float2(x.z, x.w);
     }
 }
 
-// One warp: 32 channels of one sequence, its segments from the last to the
-// first.  bc [D / 32][rows][2 NS]: this warp's share of dB and dC.
+__device__ __forceinline__ float2 exp2_pair(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
+
 template <typename T, int NS>
-__global__ void __launch_bounds__(kThreads) selective_backward_kernel(const ScanBackwardArgs g, const float* states,
-                                                                      float* bc, float* partial) {
+__global__ void __launch_bounds__(kScanWarps * 32, 4) ends_kernel(const ScanBackwardArgs g, const Work w) {
+    using L = Layout<NS>;
+    constexpr int SPL = L::SPL, H = SPL / 2;
+    extern __shared__ __align__(16) float shared[];
     const ScanArgs& a = g.f;
-    const int lane = threadIdx.x, D = a.D, b = blockIdx.y, N = a.rows.N, segs = (N + kSeg - 1) / kSeg;
-    const bool on = blockIdx.x * kThreads + lane < (unsigned)D;
-    const int d = on ? blockIdx.x * kThreads + lane : D - 1;
-    const long long rows = (long long)a.rows.B * N;
-    float A[NS], dA[NS], gh[NS];
+    const Slot f = find_slot(a.rows, blockIdx.x);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.D;
+    const int d0 = blockIdx.y * L::W4 + warp * L::W;
+    float *sbc = shared, *sd = shared + L::BC + warp * L::ROWS, *sy = sd + L::SEG * L::LD;
+    float total[kVec] = {};
+    stage<T, NS>(g, f, d0, sd, sy, sbc, total);
+    if (d0 >= D) return;
+    sum_rows<L::VR>(total);
+    if (lane < L::VR && d0 + lane * kVec < D) store8(w.steps + (size_t)blockIdx.x * D + d0 + lane * kVec, total);
+
+    const int q = lane % L::LPC, cg = lane / L::LPC, d = d0 + cg * kPair;
+    float2 A[kPair][H], h[kPair][H], back[kPair][H], P[kPair][H];
+    load_states<SPL>(A, a.A, NS, q, d, D);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        A[i] = a.A[(size_t)d * NS + i];
-        dA[i] = 0.f;
-        gh[i] = g.dh_final ? g.dh_final[((size_t)b * D + d) * NS + i] : 0.f;
-    }
-    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
-    float dskip = 0.f, dbias = 0.f;
-    for (int s = segs - 1; s >= 0; --s) {
-        const int len = min(kSeg, N - s * kSeg);
-        float hs[kSeg + 1][NS];
-        const float* from = states + (((size_t)b * segs + s) * D + d) * NS;
+    for (int c = 0; c < kPair; ++c)
 #pragma unroll
-        for (int i = 0; i < NS; ++i) hs[0][i] = from[i];
-        for (int t = 0; t < len; ++t) {
-            const long long row = (long long)b * N + s * kSeg + t;
-            const float delta = softplus(to_f32(static_cast<const T*>(a.dt)[row * a.lddt + d]) + bias);
-            const float du = delta * to_f32(static_cast<const T*>(a.u)[row * a.ldu + d]);
-            const T* B = static_cast<const T*>(a.Bm) + row * a.ldb;
-#pragma unroll
-            for (int i = 0; i < NS; ++i) hs[t + 1][i] = fmaf(expf(delta * A[i]), hs[t][i], du * to_f32(B[i]));
+        for (int i = 0; i < H; ++i) {
+            A[c][i] = mul2(A[c][i], both(kLog2e));
+            h[c][i] = back[c][i] = both(0.f);
+            P[c][i] = both(1.f);
         }
-        for (int t = len - 1; t >= 0; --t) {
-            const long long row = (long long)b * N + s * kSeg + t;
-            const T* B = static_cast<const T*>(a.Bm) + row * a.ldb;
-            const T* C = static_cast<const T*>(a.Cm) + row * a.ldc;
-            const float raw = to_f32(static_cast<const T*>(a.dt)[row * a.lddt + d]) + bias;
-            const float delta = softplus(raw), u = to_f32(static_cast<const T*>(a.u)[row * a.ldu + d]);
-            const float up = on ? to_f32(static_cast<const T*>(g.dout)[row * D + d]) : 0.f;
-            float dy = up;
-            if (a.z) {
-                const float z = to_f32(static_cast<const T*>(a.z)[row * a.ldz + d]), sig = sigmoidf_(z);
-                float y = skip * u;
+    const float *B = sbc + q * SPL, *C = B + L::SEG * NS;
+#pragma unroll 4
+    for (int t = 0; t < L::SEG; ++t) {
+        const float4 du = *reinterpret_cast<const float4*>(sd + t * L::LD + cg * 4);
+        const float2 dy = *reinterpret_cast<const float2*>(sy + t * L::LY + cg * 2);
+        float2 b[H], cs[H];
+        read_states<H>(b, B + t * NS);
+        read_states<H>(cs, C + t * NS);
 #pragma unroll
-                for (int i = 0; i < NS; ++i) y = fmaf(to_f32(C[i]), hs[t + 1][i], y);
-                dy = up * z * sig;
-                if (on) static_cast<T*>(g.dz)[row * D + d] = from_f32<T>(up * y * swish_slope(z, sig));
+        for (int c = 0; c < kPair; ++c) {
+            const float2 dd = both(c ? du.y : du.x), uu = both(c ? du.w : du.z), yy = both(c ? dy.y : dy.x);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float2 e = exp2_pair(mul2(dd, A[c][i]));
+                h[c][i] = fma2(e, h[c][i], mul2(uu, b[i]));
+                P[c][i] = mul2(P[c][i], e);
+                back[c][i] = fma2(P[c][i], mul2(yy, cs[i]), back[c][i]);
             }
-            float sB = 0.f, sA = 0.f;
-            float* to = bc + ((size_t)blockIdx.x * rows + row) * 2 * NS;
+        }
+    }
+    const size_t state = (size_t)blockIdx.x * D * NS;
+    store_states<SPL>(w.h + state, h, NS, q, d, D);
+    store_states<SPL>(w.g + state, back, NS, q, d, D);
+}
+
+// h: the state before each segment; g: the gradient carried into its last token
+// from behind; both over the segments' own, in place.
+template <int NS>
+__global__ void __launch_bounds__(64) fold_kernel(const ScanBackwardArgs g, const Work w, int segs) {
+    const ScanArgs& a = g.f;
+    const int i = blockIdx.y * 64 + threadIdx.x, b = blockIdx.x;
+    if (i >= a.D * (NS / 4)) return;
+    const int d = i / (NS / 4), q = i % (NS / 4) * 4;
+    const size_t stride = (size_t)a.D * NS, own = ((size_t)b * a.D + d) * NS + q;
+    float4 A = *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q);
+    A = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 8;
 #pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                const float Bi = to_f32(B[i]);
-                gh[i] = fmaf(to_f32(C[i]), dy, gh[i]);
-                const float dB = warp_sum(on ? gh[i] * delta * u : 0.f), dC = warp_sum(hs[t + 1][i] * dy);
-                if (lane == 0) {
-                    to[i] = dB;
-                    to[NS + i] = dC;
+    for (int side = 0; side < 2; ++side) {
+        const float* start = side ? g.dh_final : a.h0;
+        float4 x = start ? *reinterpret_cast<const float4*>(start + own) : zero;
+        const long long first = (long long)b * segs + (side ? segs - 1 : 0);
+        const long long step = side ? -1 : 1;
+        float* v = (side ? w.g : w.h) + first * stride + (size_t)d * NS + q;
+        const float* s = w.steps + first * a.D + d;
+        for (int k = 0; k < segs; k += U) {
+            float4 local[U];
+            float sum[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (k + j < segs) {
+                    local[j] = *reinterpret_cast<const float4*>(v + (k + j) * step * (long long)stride);
+                    sum[j] = s[(k + j) * step * a.D];
                 }
-                sB = fmaf(gh[i], Bi, sB);
-                gh[i] *= expf(delta * A[i]);
-                const float through = gh[i] * hs[t][i];
-                sA = fmaf(through, A[i], sA);
-                dA[i] = fmaf(through, delta, dA[i]);
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (k + j < segs) {
+                    *reinterpret_cast<float4*>(v + (k + j) * step * (long long)stride) = x;
+                    x.x = fmaf(exp2_approx(sum[j] * A.x), x.x, local[j].x);
+                    x.y = fmaf(exp2_approx(sum[j] * A.y), x.y, local[j].y);
+                    x.z = fmaf(exp2_approx(sum[j] * A.z), x.z, local[j].z);
+                    x.w = fmaf(exp2_approx(sum[j] * A.w), x.w, local[j].w);
+                }
+        }
+        if (side && g.dh0) *reinterpret_cast<float4*>(g.dh0 + own) = x;
+    }
+}
+
+template <typename T, int NS>
+__global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel(const ScanBackwardArgs g, const Work w) {
+    using L = Layout<NS>;
+    constexpr int SPL = L::SPL, H = SPL / 2, G = L::GROUP, LPC = L::LPC, W = L::W;
+    extern __shared__ __align__(16) float shared[];
+    const ScanArgs& a = g.f;
+    const Slot f = find_slot(a.rows, blockIdx.x);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.D;
+    const int d0 = blockIdx.y * L::W4 + warp * W;
+    float *sbc = shared, *sd = shared + L::BC + warp * L::WARP, *sy = sd + L::SEG * L::LD, *starts = sd + L::ROWS;
+    const long long row0 = f.row0 + f.first;
+    {
+        float total[kVec] = {};
+        stage<T, NS>(g, f, d0, sd, sy, sbc, total);
+    }
+    if (d0 < D) {
+        const int q = lane % LPC, cg = lane / LPC, d = d0 + cg * kPair;
+        const size_t state = (size_t)blockIdx.x * D * NS;
+        const float *B = sbc + q * SPL, *C = B + L::SEG * NS;
+        float2 A[kPair][H], dA[kPair][H], carry[kPair][H];
+        load_states<SPL>(A, a.A, NS, q, d, D);
+        load_states<SPL>(carry, w.g + state, NS, q, d, D);
+#pragma unroll
+        for (int c = 0; c < kPair; ++c)
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                A[c][i] = mul2(A[c][i], both(kLog2e));
+                dA[c][i] = both(0.f);
             }
-            const float ddt = fmaf(u, sB, sA) * sigmoidf_(raw);
-            dskip = fmaf(dy, u, dskip);
-            dbias += ddt;
-            if (on) {
-                static_cast<T*>(g.du)[row * D + d] = from_f32<T>(fmaf(delta, sB, skip * dy));
-                static_cast<T*>(g.ddt)[row * D + d] = from_f32<T>(ddt);
+        // the state before every group
+        {
+            float2 h[kPair][H];
+            load_states<SPL>(h, w.h + state, NS, q, d, D);
+#pragma unroll 2
+            for (int k = 0; k < L::SEG / G; ++k) {
+                float4* to = reinterpret_cast<float4*>(starts + k * L::START) + lane;
+#pragma unroll
+                for (int c = 0; c < kPair; ++c)
+#pragma unroll
+                    for (int i = 0; i < H; i += 2)
+                        to[(c * H + i) / 2 * 32] = make_float4(h[c][i].x, h[c][i].y, h[c][i + 1].x, h[c][i + 1].y);
+                if (k + 1 == L::SEG / G) break;
+#pragma unroll
+                for (int t = k * G; t < (k + 1) * G; ++t) {
+                    const float4 du = *reinterpret_cast<const float4*>(sd + t * L::LD + cg * 4);
+                    float2 b[H];
+                    read_states<H>(b, B + t * NS);
+#pragma unroll
+                    for (int c = 0; c < kPair; ++c) {
+                        const float2 dd = both(c ? du.y : du.x), uu = both(c ? du.w : du.z);
+#pragma unroll
+                        for (int i = 0; i < H; ++i)
+                            h[c][i] = fma2(exp2_pair(mul2(dd, A[c][i])), h[c][i], mul2(uu, b[i]));
+                    }
+                }
             }
         }
-    }
-    if (!on) return;
-    float* to = partial + (size_t)b * D * (NS + 2);
+        for (int k = L::SEG / G - 1; k >= 0; --k) {
+            // the group's states and decays
+            float2 h[G + 1][kPair][H], e[G][kPair][H];
+            const float4* from = reinterpret_cast<const float4*>(starts + k * L::START) + lane;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        to[(size_t)d * NS + i] = dA[i];
-        if (g.dh0) g.dh0[((size_t)b * D + d) * NS + i] = gh[i];
+            for (int c = 0; c < kPair; ++c)
+#pragma unroll
+                for (int i = 0; i < H; i += 2) {
+                    const float4 x = from[(c * H + i) / 2 * 32];
+                    h[0][c][i] = make_float2(x.x, x.y);
+                    h[0][c][i + 1] = make_float2(x.z, x.w);
+                }
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const int t = k * G + j;
+                const float4 du = *reinterpret_cast<const float4*>(sd + t * L::LD + cg * 4);
+                float2 b[H];
+                read_states<H>(b, B + t * NS);
+#pragma unroll
+                for (int c = 0; c < kPair; ++c) {
+                    const float2 dd = both(c ? du.y : du.x), uu = both(c ? du.w : du.z);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        e[j][c][i] = exp2_pair(mul2(dd, A[c][i]));
+                        h[j + 1][c][i] = fma2(e[j][c][i], h[j][c][i], mul2(uu, b[i]));
+                    }
+                }
+            }
+            // and the way back; sums[token][channel]: y, sum of A g a h[t-1] (in log2 units), sum of g B
+            float sums[G * kPair * 3];
+#pragma unroll
+            for (int j = G - 1; j >= 0; --j) {
+                const int t = k * G + j;
+                const float4 du = *reinterpret_cast<const float4*>(sd + t * L::LD + cg * 4);
+                const float2 dy = *reinterpret_cast<const float2*>(sy + t * L::LY + cg * 2);
+                float2 b[H], cs[H], bc[2 * H];
+                read_states<H>(b, B + t * NS);
+                read_states<H>(cs, C + t * NS);
+#pragma unroll
+                for (int c = 0; c < kPair; ++c) {
+                    const float2 dd = both(c ? du.y : du.x), uu = both(c ? du.w : du.z), yy = both(c ? dy.y : dy.x);
+                    float2 y, sa, sb;
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float2 gr = fma2(cs[i], yy, carry[c][i]);
+                        y = i ? fma2(cs[i], h[j + 1][c][i], y) : mul2(cs[i], h[j + 1][c][i]);
+                        sb = i ? fma2(gr, b[i], sb) : mul2(gr, b[i]);
+                        bc[i] = c ? fma2(gr, uu, bc[i]) : mul2(gr, uu);
+                        bc[H + i] = c ? fma2(h[j + 1][c][i], yy, bc[H + i]) : mul2(h[j + 1][c][i], yy);
+                        carry[c][i] = mul2(gr, e[j][c][i]);
+                        const float2 through = mul2(carry[c][i], h[j][c][i]);
+                        sa = i ? fma2(through, A[c][i], sa) : mul2(through, A[c][i]);
+                        dA[c][i] = fma2(through, dd, dA[c][i]);
+                    }
+                    float* s = sums + (j * kPair + c) * 3;
+                    s[0] = y.x + y.y;
+                    s[1] = sa.x + sa.y;
+                    s[2] = sb.x + sb.y;
+                }
+                // dB, dC of the warp's channels: over the lanes of other channels
+                float v[2 * SPL];
+#pragma unroll
+                for (int i = 0; i < 2 * H; ++i) {
+                    v[2 * i] = bc[i].x;
+                    v[2 * i + 1] = bc[i].y;
+                }
+                add_parts<2 * SPL, 16, LPC>(v, lane);
+                constexpr int R = parts_left<2 * SPL, 16, LPC>();
+                constexpr int HOLDERS = 32 / LPC, TWINS = HOLDERS * R / (2 * SPL);
+                __syncwarp();
+                if (cg % TWINS == 0) {
+                    const int first = cg / TWINS * R;                  // of the lane's dB and dC values
+                    float* to = starts + k * L::START + j * 2 * NS + (first / SPL) * NS + q * SPL + first % SPL;
+#pragma unroll
+                    for (int i = 0; i < R; ++i) to[i] = v[i];
+                }
+            }
+            add_parts<G * kPair * 3, LPC / 2, 1>(sums, lane);
+            constexpr int R = parts_left<G * kPair * 3, LPC / 2, 1>();
+            constexpr int TWINS = LPC * R / (G * kPair * 3);
+            static_assert(R % 3 == 0, "whole channels");
+            __syncwarp();
+            if (q % TWINS == 0) {
+                // where the tokens' delta u and dy were: A g a h[t-1], g B, y
+#pragma unroll
+                for (int i = 0; i < R / 3; ++i) {
+                    const int item = q / TWINS * (R / 3) + i, t = k * G + item / kPair, c = item % kPair;
+                    sd[t * L::LD + cg * 4 + c] = sums[3 * i + 1];
+                    sd[t * L::LD + cg * 4 + 2 + c] = sums[3 * i + 2];
+                    sy[t * L::LY + cg * 2 + c] = sums[3 * i];
+                }
+            }
+        }
+        __syncwarp();
+        float* partial = w.partial + (size_t)blockIdx.x * D * (NS + 2);
+        store_states<SPL>(partial, dA, NS, q, d, D);
+
+        const int vc = d0 + lane % L::VR * kVec;
+        float bias[kVec] = {}, skip[kVec] = {}, dskip[kVec] = {}, dbias[kVec] = {};
+        if (vc < D && a.dt_bias) load8(a.dt_bias + vc, bias);
+        if (vc < D && a.skip) load8(a.skip + vc, skip);
+#pragma unroll
+        for (int j = 0; j < L::V; ++j) {
+            const int r = lane / L::VR + j * (32 / L::VR);
+            if (vc >= D || r >= f.len) continue;
+            const long long row = row0 + r;
+            float u[kVec], raw[kVec], up[kVec], z[kVec], y[kVec], du[kVec], ddt[kVec], dz[kVec];
+            load8(static_cast<const T*>(a.u) + row * a.ldu + vc, u);
+            load8(static_cast<const T*>(a.dt) + row * a.lddt + vc, raw);
+            load8(static_cast<const T*>(g.dout) + row * D + vc, up);
+            if (a.z) load8(static_cast<const T*>(a.z) + row * a.ldz + vc, z);
+            load8(sy + r * L::LY + (vc - d0), y);
+            const float* s = sd + r * L::LD + 2 * (vc - d0);
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2) {
+                const float4 ab = *reinterpret_cast<const float4*>(s + 2 * e);
+                const float sa[2] = {ab.x, ab.y}, sb[2] = {ab.z, ab.w};
+                raw[e] += bias[e];
+                raw[e + 1] += bias[e + 1];
+                const float2 dl = softplus2(make_float2(raw[e], raw[e + 1]));
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const int i = e + o;
+                    float dy = up[i];
+                    if (a.z) {
+                        const float sig = sigmoid_fast(z[i]);
+                        dz[i] = up[i] * fmaf(skip[i], u[i], y[i]) * swish_slope(z[i], sig);
+                        dy *= z[i] * sig;
+                    }
+                    ddt[i] = fmaf(u[i], sb[o], sa[o] * 0.6931471805599453f) * sigmoid_fast(raw[i]);
+                    du[i] = fmaf(o ? dl.y : dl.x, sb[o], skip[i] * dy);
+                    dskip[i] = fmaf(dy, u[i], dskip[i]);
+                    dbias[i] += ddt[i];
+                }
+            }
+            store8(static_cast<T*>(g.du) + row * D + vc, du);
+            store8(static_cast<T*>(g.ddt) + row * D + vc, ddt);
+            if (a.z) store8(static_cast<T*>(g.dz) + row * D + vc, dz);
+        }
+        sum_rows<L::VR>(dskip);
+        sum_rows<L::VR>(dbias);
+        if (lane < L::VR && vc < D) {
+            store8(partial + (size_t)D * NS + vc, dskip);
+            store8(partial + (size_t)D * (NS + 1) + vc, dbias);
+        }
     }
-    to[(size_t)D * NS + d] = dskip;
-    to[(size_t)D * (NS + 1) + d] = dbias;
+    __syncthreads();
+    // the block's share of dB and dC
+    const int warps = min(kScanWarps, (D - (int)blockIdx.y * L::W4 + W - 1) / W);
+    float* bc = w.bc + ((size_t)blockIdx.y * a.rows.B * a.rows.N + row0) * 2 * NS;
+    for (int i = threadIdx.x; i < f.len * 2 * NS; i += kScanWarps * 32) {
+        const int t = i / (2 * NS);
+        const float* from = shared + L::BC + L::ROWS + t / G * L::START + t % G * 2 * NS + i % (2 * NS);
+        float s = 0.f;
+        for (int k = 0; k < warps; ++k) s += from[k * L::WARP];
+        bc[i] = s;
+    }
 }
 
 // dB, dC: the channel blocks' shares, added in order.
 template <typename T>
 __global__ void __launch_bounds__(256) join_kernel(const float* bc, int blocks, long long rows, int n, T* dB, T* dC) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows * 2 * n) return;
-    float s = 0.f;
-    for (int k = 0; k < blocks; ++k) s += bc[(size_t)k * rows * 2 * n + i];
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4, all = rows * 2 * n;
+    if (i >= all) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < blocks; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(bc + k * all + i);
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+    }
     const long long row = i / (2 * n);
     const int j = (int)(i - row * 2 * n);
-    (j < n ? dB[row * n + j] : dC[row * n + j - n]) = from_f32<T>(s);
+    T* to = j < n ? dB + row * n + j : dC + row * n + j - n;
+    to[0] = from_f32<T>(s.x);
+    to[1] = from_f32<T>(s.y);
+    to[2] = from_f32<T>(s.z);
+    to[3] = from_f32<T>(s.w);
 }
 
-struct Sizes {
-    size_t states, bc, partial;
+// Tokens of a segment and channels of a block for n states.
+struct Cut {
+    int seg, channels;
 };
-Sizes sizes(int B, int N, int D, int n) {
-    const size_t segs = (N + kSeg - 1) / kSeg, blocks = (D + kThreads - 1) / kThreads;
-    return {align256((size_t)B * segs * D * n * 4), align256(blocks * B * N * 2 * n * 4),
-            align256((size_t)B * D * (n + 2) * 4)};
+Cut cut_of(int n) {
+    switch (n) {
+        case 8: return {Layout<8>::SEG, Layout<8>::W4};
+        case 16: return {Layout<16>::SEG, Layout<16>::W4};
+        case 32: return {Layout<32>::SEG, Layout<32>::W4};
+        default: return {Layout<64>::SEG, Layout<64>::W4};
+    }
+}
+
+// Offsets of the workspace's parts, in bytes, and its size.
+struct Parts {
+    size_t g, steps, bc, partial, all;
+};
+Parts parts_of(int B, int N, int D, int n) {
+    const Cut c = cut_of(n);
+    const size_t slots = (size_t)B * ((N + c.seg - 1) / c.seg), blocks = (D + c.channels - 1) / c.channels;
+    Parts p;
+    p.g = align256(slots * D * n * 4);
+    p.steps = 2 * p.g;
+    p.bc = p.steps + align256(slots * D * 4);
+    p.partial = p.bc + align256(blocks * B * N * 2 * n * 4);
+    p.all = p.partial + align256(slots * D * (n + 2) * 4);
+    return p;
 }
 
 template <typename T, int NS>
-cudaError_t backward(const ScanBackwardArgs& g, cudaStream_t s) {
-    const ScanArgs& a = g.f;
-    const Sizes z = sizes(a.rows.B, a.rows.N, a.D, NS);
+cudaError_t backward(ScanBackwardArgs g, cudaStream_t s) {
+    using L = Layout<NS>;
+    ScanArgs& a = g.f;
+    a.rows.seg = L::SEG;
+    const Parts p = parts_of(a.rows.B, a.rows.N, a.D, NS);
     char* ws = static_cast<char*>(g.workspace);
-    float* states = reinterpret_cast<float*>(ws);
-    float* bc = reinterpret_cast<float*>(ws + z.states);
-    float* partial = reinterpret_cast<float*>(ws + z.states + z.bc);
-    const dim3 grid((a.D + kThreads - 1) / kThreads, a.rows.B);
-    states_kernel<T, NS><<<grid, kThreads, 0, s>>>(a, states);
-    selective_backward_kernel<T, NS><<<grid, kThreads, 0, s>>>(g, states, bc, partial);
-    const long long rows = (long long)a.rows.B * a.rows.N;
-    join_kernel<T><<<(unsigned)((rows * 2 * NS + 255) / 256), 256, 0, s>>>(bc, grid.x, rows, NS, static_cast<T*>(g.dBm),
-                                                                          static_cast<T*>(g.dCm));
-    cudaError_t err = cudaGetLastError();
+    const Work w = {reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + p.g), reinterpret_cast<float*>(ws + p.steps),
+                    reinterpret_cast<float*>(ws + p.bc), reinterpret_cast<float*>(ws + p.partial)};
+    const long long slots = slots_of(a.rows), D = a.D, rows = (long long)a.rows.B * a.rows.N;
+    const dim3 grid((unsigned)slots, (a.D + L::W4 - 1) / L::W4);
+    const int ends_bytes = (L::BC + kScanWarps * L::ROWS) * 4, walk_bytes = (L::BC + kScanWarps * L::WARP) * 4;
+    cudaError_t err = cudaFuncSetAttribute(ends_kernel<T, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, ends_bytes);
+    if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(walk_kernel<T, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk_bytes);
     if (err != cudaSuccess) return err;
-    const long long D = a.D;
+    ends_kernel<T, NS><<<grid, kScanWarps * 32, ends_bytes, s>>>(g, w);
+    fold_kernel<NS><<<dim3(a.rows.B, (a.D * (NS / 4) + 63) / 64), 64, 0, s>>>(g, w, (int)(slots / a.rows.B));
+    walk_kernel<T, NS><<<grid, kScanWarps * 32, walk_bytes, s>>>(g, w);
+    join_kernel<T><<<(unsigned)((rows * 2 * NS / 4 + 255) / 256), 256, 0, s>>>(w.bc, grid.y, rows, NS,
+                                                                              static_cast<T*>(g.dBm), static_cast<T*>(g.dCm));
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
     const ColumnOutputs out = {3, {0, D * NS, D * (NS + 1), D * (NS + 2)}, {g.dA, g.dskip, g.ddt_bias}, {1, 1, 1}};
-    return launch_column_sums(partial, a.rows.B, out, s);
+    return launch_column_sums(w.partial, (int)slots, out, s);
 }
 
 }  // namespace
 
-size_t selective_backward_ws_bytes(int B, int N, int D, int n, gret_dtype) {
-    const Sizes z = sizes(B, N, D, n);
-    return z.states + z.bc + z.partial;
-}
+size_t selective_backward_ws_bytes(int B, int N, int D, int n, gret_dtype) { return parts_of(B, N, D, n).all; }
 
-cudaError_t launch_selective_backward(ScanBackwardArgs g, int num_sms, cudaStream_t s) {
-    (void)num_sms;
+cudaError_t launch_selective_backward(ScanBackwardArgs g, int, cudaStream_t s) {
     const bool bf = g.f.io == GRET_BF16;
     switch (g.f.n) {
         case 8: return bf ? backward<__nv_bfloat16, 8>(g, s) : backward<float, 8>(g, s);

@@ -8,7 +8,7 @@
 // B and C are shared by all channels of a token.
 #include <math.h>
 
-#include "gret_block.cuh"
+#include "gret_selective.cuh"
 
 namespace gret {
 namespace {
@@ -18,7 +18,7 @@ constexpr int kStepThreads = 128;
 // How a warp lays out its channels and states: a lane holds SPL states of two
 // channels, n / SPL lanes share a channel, and the warp's W channels are walked
 // kTile tokens at a time, kGroup of them between two rounds of shuffles.
-constexpr int kTile = 16, kWarps = 4, kGroup = 4, kPair = 2;
+constexpr int kTile = 16, kWarps = kScanWarps, kGroup = 4;
 template <int NS>
 struct Layout {
     static constexpr int SPL = NS >= 32 ? 8 : 4;            // states of a lane
@@ -29,27 +29,6 @@ struct Layout {
     static constexpr int V = (kTile * VR + 31) / 32;        // and of a lane
     static constexpr int BV = (kTile * NS / kVec + 31) / 32;    // vectors of B (of C) a lane stages
     static constexpr int FLOATS = kTile * (LD + 2 * NS + LY);   // shared floats of a warp
-};
-
-// Eight values as they lie in memory.
-template <typename T> struct Raw;
-template <> struct Raw<__nv_bfloat16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float* v) const { unpack8(a, v); }
-};
-template <> struct Raw<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float* v) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
 };
 
 // A warp walks one slot's tokens for its channels.  Each tile of tokens is
@@ -71,22 +50,12 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* sh
 
     const int q = lane % LPC, g = lane / LPC;               // states q SPL .., channels d0 + 2 g ..
     float2 A[kPair][H], h[kPair][H];                        // two states each
+    load_states<SPL>(A, a.A, NS, q, d0 + g * kPair, D);
+    load_states<SPL>(h, before, NS, q, d0 + g * kPair, D);
 #pragma unroll
-    for (int c = 0; c < kPair; ++c) {
-        const int d = d0 + g * kPair + c;
+    for (int c = 0; c < kPair; ++c)
 #pragma unroll
-        for (int i = 0; i < H; i += 2) {
-            float4 av = make_float4(0.f, 0.f, 0.f, 0.f), hv = av;
-            if (d < D) {
-                av = *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q * SPL + 2 * i);
-                if (before) hv = *reinterpret_cast<const float4*>(before + (size_t)d * NS + q * SPL + 2 * i);
-            }
-            A[c][i] = make_float2(av.x * kLog2e, av.y * kLog2e);
-            A[c][i + 1] = make_float2(av.z * kLog2e, av.w * kLog2e);
-            h[c][i] = make_float2(hv.x, hv.y);
-            h[c][i + 1] = make_float2(hv.z, hv.w);
-        }
-    }
+        for (int i = 0; i < H; ++i) A[c][i] = mul2(A[c][i], both(kLog2e));
 
     // staging: vector lane + 32 j of the tile is row / L::VR, always the same channels
     const int vc = d0 + (lane % L::VR) * kVec, vr = lane / L::VR;
@@ -212,15 +181,7 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* sh
             if (kFinal) {
                 // the lanes of a channel add up their states; lane q keeps the group's values q R ..
                 constexpr int R = kGroup * kPair / LPC;
-#pragma unroll
-                for (int m = LPC / 2, half = kGroup * kPair / 2; m > 0; m /= 2, half /= 2) {
-                    const bool up = (q & m) != 0;
-#pragma unroll
-                    for (int c = 0; c < half; ++c) {
-                        const float keep = up ? v[c + half] : v[c], send = up ? v[c] : v[c + half];
-                        v[c] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-                    }
-                }
+                add_parts<kGroup * kPair, LPC / 2, 1>(v, q);
 #pragma unroll
                 for (int k = 0; k < R; ++k)
                     sy[(t1 + (q * R + k) / kPair) * LY + g * kPair + (q * R + k) % kPair] = v[k];
@@ -249,17 +210,7 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* sh
             __syncwarp();
         }
     }
-    if (leave) {
-#pragma unroll
-        for (int c = 0; c < kPair; ++c) {
-            const int d = d0 + g * kPair + c;
-#pragma unroll
-            for (int i = 0; i < H; i += 2)
-                if (d < D)
-                    *reinterpret_cast<float4*>(leave + (size_t)d * NS + q * SPL + 2 * i) =
-                        make_float4(h[c][i].x, h[c][i].y, h[c][i + 1].x, h[c][i + 1].y);
-        }
-    }
+    if (leave) store_states<SPL>(leave, h, NS, q, d0 + g * kPair, D);
     if (!kFinal) {
         // a channel's vectors lie in the lanes VR apart
 #pragma unroll
