@@ -73,19 +73,29 @@ __device__ __forceinline__ void stage(const ScanBackwardArgs& g, const Slot& f, 
     if (d0 < a.D) {
         float bias[kVec] = {};
         if (vc < a.D && a.dt_bias) load8(a.dt_bias + vc, bias);
+        Raw<T> ru[L::V], rt[L::V], rg[L::V], rz[L::V];
+#pragma unroll
+        for (int j = 0; j < L::V; ++j) {
+            const int r = lane / L::VR + j * (32 / L::VR);
+            if (vc >= a.D || r >= f.len) continue;
+            const long long row = row0 + r;
+            rt[j].load(static_cast<const T*>(a.dt) + row * a.lddt + vc);
+            ru[j].load(static_cast<const T*>(a.u) + row * a.ldu + vc);
+            rg[j].load(static_cast<const T*>(g.dout) + row * a.D + vc);
+            if (a.z) rz[j].load(static_cast<const T*>(a.z) + row * a.ldz + vc);
+        }
 #pragma unroll
         for (int j = 0; j < L::V; ++j) {
             const int r = lane / L::VR + j * (32 / L::VR);
             if (r >= L::SEG) continue;
             float u[kVec] = {}, s[kVec] = {}, dy[kVec] = {};
             if (vc < a.D && r < f.len) {
-                const long long row = row0 + r;
-                load8(static_cast<const T*>(a.dt) + row * a.lddt + vc, s);
-                load8(static_cast<const T*>(a.u) + row * a.ldu + vc, u);
-                load8(static_cast<const T*>(g.dout) + row * a.D + vc, dy);
+                rt[j].get(s);
+                ru[j].get(u);
+                rg[j].get(dy);
                 if (a.z) {
                     float z[kVec];
-                    load8(static_cast<const T*>(a.z) + row * a.ldz + vc, z);
+                    rz[j].get(z);
 #pragma unroll
                     for (int e = 0; e < kVec; ++e) dy[e] *= z[e] * sigmoid_fast(z[e]);
                 }
@@ -238,17 +248,18 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
     const int d0 = blockIdx.y * L::W4 + warp * W;
     float *sbc = shared, *sd = shared + L::BC + warp * L::WARP, *sy = sd + L::SEG * L::LD, *starts = sd + L::ROWS;
     const long long row0 = f.row0 + f.first;
+    const int q = lane % LPC, cg = lane / LPC, d = d0 + cg * kPair;
+    const size_t state = (size_t)blockIdx.x * D * NS;
+    float2 A[kPair][H], dA[kPair][H], carry[kPair][H], first[kPair][H];
+    load_states<SPL>(A, a.A, NS, q, d, D);
+    load_states<SPL>(first, w.h + state, NS, q, d, D);
+    load_states<SPL>(carry, w.g + state, NS, q, d, D);
     {
         float total[kVec] = {};
         stage<T, NS>(g, f, d0, sd, sy, sbc, total);
     }
     if (d0 < D) {
-        const int q = lane % LPC, cg = lane / LPC, d = d0 + cg * kPair;
-        const size_t state = (size_t)blockIdx.x * D * NS;
         const float *B = sbc + q * SPL, *C = B + L::SEG * NS;
-        float2 A[kPair][H], dA[kPair][H], carry[kPair][H];
-        load_states<SPL>(A, a.A, NS, q, d, D);
-        load_states<SPL>(carry, w.g + state, NS, q, d, D);
 #pragma unroll
         for (int c = 0; c < kPair; ++c)
 #pragma unroll
@@ -258,8 +269,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
             }
         // the state before every group
         {
-            float2 h[kPair][H];
-            load_states<SPL>(h, w.h + state, NS, q, d, D);
+            float2 (&h)[kPair][H] = first;
 #pragma unroll 2
             for (int k = 0; k < L::SEG / G; ++k) {
                 float4* to = reinterpret_cast<float4*>(starts + k * L::START) + lane;
@@ -355,8 +365,8 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
                 constexpr int HOLDERS = 32 / LPC, TWINS = HOLDERS * R / (2 * SPL);
                 __syncwarp();
                 if (cg % TWINS == 0) {
-                    const int first = cg / TWINS * R;                  // of the lane's dB and dC values
-                    float* to = starts + k * L::START + j * 2 * NS + (first / SPL) * NS + q * SPL + first % SPL;
+                    const int at = cg / TWINS * R;                     // of the lane's dB and dC values
+                    float* to = starts + k * L::START + j * 2 * NS + (at / SPL) * NS + q * SPL + at % SPL;
 #pragma unroll
                     for (int i = 0; i < R; ++i) to[i] = v[i];
                 }
@@ -385,16 +395,27 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
         float bias[kVec] = {}, skip[kVec] = {}, dskip[kVec] = {}, dbias[kVec] = {};
         if (vc < D && a.dt_bias) load8(a.dt_bias + vc, bias);
         if (vc < D && a.skip) load8(a.skip + vc, skip);
+        Raw<T> ru[L::V], rt[L::V], rg[L::V], rz[L::V];
+#pragma unroll
+        for (int j = 0; j < L::V; ++j) {
+            const int r = lane / L::VR + j * (32 / L::VR);
+            if (vc >= D || r >= f.len) continue;
+            const long long row = row0 + r;
+            ru[j].load(static_cast<const T*>(a.u) + row * a.ldu + vc);
+            rt[j].load(static_cast<const T*>(a.dt) + row * a.lddt + vc);
+            rg[j].load(static_cast<const T*>(g.dout) + row * D + vc);
+            if (a.z) rz[j].load(static_cast<const T*>(a.z) + row * a.ldz + vc);
+        }
 #pragma unroll
         for (int j = 0; j < L::V; ++j) {
             const int r = lane / L::VR + j * (32 / L::VR);
             if (vc >= D || r >= f.len) continue;
             const long long row = row0 + r;
             float u[kVec], raw[kVec], up[kVec], z[kVec], y[kVec], du[kVec], ddt[kVec], dz[kVec];
-            load8(static_cast<const T*>(a.u) + row * a.ldu + vc, u);
-            load8(static_cast<const T*>(a.dt) + row * a.lddt + vc, raw);
-            load8(static_cast<const T*>(g.dout) + row * D + vc, up);
-            if (a.z) load8(static_cast<const T*>(a.z) + row * a.ldz + vc, z);
+            ru[j].get(u);
+            rt[j].get(raw);
+            rg[j].get(up);
+            if (a.z) rz[j].get(z);
             load8(sy + r * L::LY + (vc - d0), y);
             const float* s = sd + r * L::LD + 2 * (vc - d0);
 #pragma unroll
