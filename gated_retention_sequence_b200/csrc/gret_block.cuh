@@ -123,6 +123,34 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// Eight values as they lie in memory.
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float* v) const { unpack8(a, v); }
+};
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float* v) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
+template <typename T>
+__device__ __forceinline__ void pairs_of(const Raw<T>& r, float2* v) {
+    float x[kVec];
+    r.get(x);
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;
@@ -162,6 +190,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // the power gives 0, as it should.
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_approx(1.0f + exp2_approx(-kLog2e * x)); }
 
+__device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid_fast(x.x), sigmoid_fast(x.y)); }
+
 // softplus of two numbers, max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].
 // log1p(e) = e P(e) with P of degree 9, the minimax fit of log1p(e) / e on
 // [0, 1] in relative error by Remez exchange (0.1 units; 2.5 units with P in
@@ -184,6 +214,15 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
 
 // d/dv of v sigmoid(v)
 __device__ __forceinline__ float swish_slope(float v, float sig) { return sig * (1.0f + v * (1.0f - sig)); }
+__device__ __forceinline__ float2 swish_slope2(float2 v, float2 sig) {
+    return mul2(sig, fma2(v, fma2(sig, both(-1.f), both(1.f)), both(1.f)));
+}
+
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* p, const float2* v) {
+    const float x[kVec] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+    store8(p, x);
+}
 
 // partial [groups][offset[count]] summed over the groups; columns offset[j] ..
 // offset[j + 1] - 1 go to dst[j], stride[j] floats apart (null: not wanted).

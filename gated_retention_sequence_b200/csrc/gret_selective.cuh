@@ -1,5 +1,5 @@
 // What the selective scan and its gradients share: the way a warp holds
-// channels and states, and its inputs as they lie in memory.
+// channels and states.
 #pragma once
 
 #include "gret_block.cuh"
@@ -8,27 +8,6 @@ namespace gret {
 
 constexpr int kScanWarps = 4;       // warps of a block: neighbouring channels, the same tokens
 constexpr int kPair = 2;            // channels of a lane
-
-// Eight values as they lie in memory.
-template <typename T> struct Raw;
-template <> struct Raw<__nv_bfloat16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float* v) const { unpack8(a, v); }
-};
-template <> struct Raw<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float* v) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-};
 
 // The values of a lane's two channels x SPL states, as pairs of states, from
 // or to rows of n per channel; a channel from `end` on reads as zero.

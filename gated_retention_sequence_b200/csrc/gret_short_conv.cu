@@ -3,86 +3,146 @@
 //   s[t,d] = bias[d] + sum_k w[d,k] x[t-K+1+k,d],   y = act(s)
 //
 // Rows from before a sequence's first token come from its tail (the last K-1
-// inputs of the piece before, or zero).  A thread owns eight channels of one
+// inputs of the piece before, or zero).  A thread owns four channels of one
 // slot (a segment of tokens) and keeps the last K-1 inputs in registers, so
-// that each input is read once, 16 bytes at a time, and K-1 more rows per slot.
+// that each input is read once, and K-1 more rows per slot.  Rows are loaded
+// kBatch at a time, a batch ahead: stores between the loads would otherwise
+// hold them up.
 #include "gret_block.cuh"
 
 namespace gret {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kSeg = 32;
+constexpr int kSeg = 64, kBatch = 4, kC = 4, kP = kC / 2;
 
-template <typename T, int K>
+// Four channels as they lie in memory.
+template <typename T> struct Four;
+template <> struct Four<__nv_bfloat16> {
+    uint2 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void zero() { a = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float2* v) const {
+        v[0] = make_float2(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u));
+        v[1] = make_float2(__uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
+    }
+};
+template <> struct Four<float> {
+    float4 a;
+    __device__ __forceinline__ void load(const float* p) { a = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float2* v) const {
+        v[0] = make_float2(a.x, a.y);
+        v[1] = make_float2(a.z, a.w);
+    }
+};
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float2* v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0].x, v[0].y), b = __floats2bfloat162_rn(v[1].x, v[1].y);
+    *reinterpret_cast<uint2*>(p) = make_uint2(reinterpret_cast<const uint32_t&>(a), reinterpret_cast<const uint32_t&>(b));
+}
+__device__ __forceinline__ void store4(float* p, const float2* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+}
+
+// Tokens of a slot: `most`, or fewer where that leaves the GPU without threads
+// (some 1024 per SM), down to 16.
+int slot_tokens(int most, long long tokens, int D) {
+    int seg = most;
+    while (seg > 16 && tokens / seg * (D / kC) < 148 * 1024) seg /= 2;
+    return seg;
+}
+
+template <int K>
 struct Taps {
-    float w[K][kVec], b[kVec];
+    float2 w[K][kP], b[kP];
     __device__ __forceinline__ void load(const float* wp, const float* bp, int c) {
-        float flat[K * kVec];
+        float flat[K * kC];
 #pragma unroll
-        for (int i = 0; i < K * kVec / 4; ++i) {
+        for (int i = 0; i < K; ++i) {
             const float4 q = reinterpret_cast<const float4*>(wp + (size_t)c * K)[i];
             flat[4 * i] = q.x; flat[4 * i + 1] = q.y; flat[4 * i + 2] = q.z; flat[4 * i + 3] = q.w;
         }
+        const float4 q = bp ? *reinterpret_cast<const float4*>(bp + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float bias[kC] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int e = 0; e < kVec; ++e)
+        for (int p = 0; p < kP; ++p) {
+            b[p] = make_float2(bias[2 * p], bias[2 * p + 1]);
 #pragma unroll
-            for (int k = 0; k < K; ++k) w[k][e] = flat[e * K + k];
-        if (bp) {
-            load8(bp + c, b);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) b[e] = 0.f;
+            for (int k = 0; k < K; ++k) w[k][p] = make_float2(flat[2 * p * K + k], flat[(2 * p + 1) * K + k]);
         }
+    }
+    // The sum before the activation of pair p, from the K-1 rows before and the row itself.
+    __device__ __forceinline__ float2 sum(const float2 (*past)[kP], float2 now, int p) const {
+        float2 s = b[p];
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) s = fma2(w[k][p], past[k][p], s);
+        return fma2(w[K - 1][p], now, s);
     }
 };
 
-// Row t (within its sequence) of the inputs; t in [-(K-1), seq_len).
-template <typename T, int K>
-__device__ __forceinline__ void input_row(const ConvArgs& a, const Slot& f, int t, int c, float* v) {
-    if (t >= 0) {
-        load8(static_cast<const T*>(a.x) + (f.row0 + t) * a.ldx + c, v);
-    } else if (a.tail0) {
-        load8(static_cast<const T*>(a.tail0) + ((size_t)f.b * (K - 1) + (K - 1 + t)) * a.D + c, v);
-    } else {
+template <int K>
+__device__ __forceinline__ void shift_in(float2 (*past)[kP], const float2* now) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] = 0.f;
+    for (int p = 0; p < kP; ++p) {
+#pragma unroll
+        for (int k = 0; k + 1 < K - 1; ++k) past[k][p] = past[k + 1][p];
+        past[K - 2][p] = now[p];
     }
 }
 
+// Row t (within its sequence) of the inputs; t in [-(K-1), seq_len).
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) short_conv_kernel(const ConvArgs a) {
+__device__ __forceinline__ void input_row(const ConvArgs& a, const Slot& f, int t, int c, float2* v) {
+    Four<T> r;
+    r.zero();
+    if (t >= 0)
+        r.load(static_cast<const T*>(a.x) + (f.row0 + t) * a.ldx + c);
+    else if (a.tail0)
+        r.load(static_cast<const T*>(a.tail0) + ((size_t)f.b * (K - 1) + (K - 1 + t)) * a.D + c);
+    r.get(v);
+}
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads, 5) short_conv_kernel(const ConvArgs a) {
     const Slot f = find_slot(a.rows, blockIdx.x);
-    const int c = (blockIdx.y * kThreads + threadIdx.x) * kVec;
+    const int c = (blockIdx.y * kThreads + threadIdx.x) * kC;
     if (f.b < 0 || c >= a.D) return;
-    Taps<T, K> taps;
+    Taps<K> taps;
     taps.load(a.w, a.bias, c);
-    float past[K - 1][kVec];
+    float2 past[K - 1][kP];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) input_row<T, K>(a, f, f.first - (K - 1) + j, c, past[j]);
     const T* x = static_cast<const T*>(a.x) + (f.row0 + f.first) * a.ldx + c;
     T* y = static_cast<T*>(a.y) + (f.row0 + f.first) * (long long)a.D + c;
-#pragma unroll 4
-    for (int t = 0; t < f.len; ++t) {
-        float now[kVec], out[kVec];
-        load8(x + t * a.ldx, now);
+    Four<T> next[kBatch];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            float s = taps.b[e];
+    for (int k = 0; k < kBatch; ++k)
+        if (k < f.len) next[k].load(x + k * a.ldx);
+    for (int t0 = 0; t0 < f.len; t0 += kBatch) {
+        Four<T> in[kBatch];
 #pragma unroll
-            for (int k = 0; k < K - 1; ++k) s = fmaf(taps.w[k][e], past[k][e], s);
-            s = fmaf(taps.w[K - 1][e], now[e], s);
-            out[e] = a.swish ? s * sigmoidf_(s) : s;
-#pragma unroll
-            for (int k = 0; k + 1 < K - 1; ++k) past[k][e] = past[k + 1][e];
-            past[K - 2][e] = now[e];
+        for (int k = 0; k < kBatch; ++k) {
+            in[k] = next[k];
+            if (t0 + kBatch + k < f.len) next[k].load(x + (t0 + kBatch + k) * a.ldx);
         }
-        store8(y + (size_t)t * a.D, out);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (t0 + k >= f.len) break;
+            float2 now[kP], out[kP];
+            in[k].get(now);
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                const float2 s = taps.sum(past, now[p], p);
+                out[p] = a.swish ? mul2(s, sigmoid2(s)) : s;
+            }
+            shift_in<K>(past, now);
+            store4(y + (size_t)(t0 + k) * a.D, out);
+        }
     }
     if (a.tail && f.s == max(f.segs, 1) - 1) {
 #pragma unroll
         for (int j = 0; j < K - 1; ++j)
-            store8(static_cast<T*>(a.tail) + ((size_t)f.b * (K - 1) + j) * a.D + c, past[j]);
+            store4(static_cast<T*>(a.tail) + ((size_t)f.b * (K - 1) + j) * a.D + c, past[j]);
     }
 }
 
@@ -91,27 +151,28 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const ConvArgs a) 
 template <typename T, int K>
 __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const ConvArgs a) {
     const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int groups = a.D / kVec;
+    const int groups = a.D / kC;
     if (i >= (long long)a.rows.B * groups) return;
-    const int b = (int)(i / groups), c = (int)(i - (long long)b * groups) * kVec;
-    Taps<T, K> taps;
-    taps.load(a.w, a.bias, c);
+    const int b = (int)(i / groups), c = (int)(i - (long long)b * groups) * kC;
     const T* old = static_cast<const T*>(a.tail0) + (size_t)b * (K - 1) * a.D + c;
     T* next = static_cast<T*>(a.tail) + (size_t)b * (K - 1) * a.D + c;
-    float v[K][kVec], out[kVec];
+    Four<T> r[K];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) load8(old + (size_t)j * a.D, v[j]);
-    load8(static_cast<const T*>(a.x) + b * a.ldx + c, v[K - 1]);
+    for (int j = 0; j < K - 1; ++j) r[j].load(old + (size_t)j * a.D);
+    r[K - 1].load(static_cast<const T*>(a.x) + b * a.ldx + c);
+    Taps<K> taps;
+    taps.load(a.w, a.bias, c);
+    float2 v[K][kP], out[kP];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-        float s = taps.b[e];
+    for (int j = 0; j < K; ++j) r[j].get(v[j]);
 #pragma unroll
-        for (int k = 0; k < K; ++k) s = fmaf(taps.w[k][e], v[k][e], s);
-        out[e] = a.swish ? s * sigmoidf_(s) : s;
+    for (int p = 0; p < kP; ++p) {
+        const float2 s = taps.sum(v, v[K - 1][p], p);
+        out[p] = a.swish ? mul2(s, sigmoid2(s)) : s;
     }
-    store8(static_cast<T*>(a.y) + (size_t)b * a.D + c, out);
+    store4(static_cast<T*>(a.y) + (size_t)b * a.D + c, out);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) store8(next + (size_t)j * a.D, v[j + 1]);
+    for (int j = 0; j < K - 1; ++j) store4(next + (size_t)j * a.D, v[j + 1]);
 }
 
 // Gradients.  With ds[t] = dy[t] act'(s[t]) (s formed again from the inputs):
@@ -119,82 +180,111 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const ConvArg
 //   dw[k]   = sum_t ds[t] x[t-K+1+k],  dbias = sum_t ds[t]
 // and dtail adds to the last K-1 rows.  A thread walks one slot and K-1 tokens
 // past its end; the slots of a block add up their dw and dbias in shared memory.
-constexpr int kBackGroups = 16, kBackSlots = 8, kBackSeg = 64;
+constexpr int kBackGroups = 32, kBackSlots = 4, kBackSeg = 128, kBackBatch = 2;
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kBackGroups* kBackSlots) short_conv_backward_kernel(const ConvBackwardArgs g,
+__global__ void __launch_bounds__(kBackGroups* kBackSlots, 4) short_conv_backward_kernel(const ConvBackwardArgs g,
                                                                                      float* partial, int slots) {
-    __shared__ float red[kBackSlots][kBackGroups * kVec + 1];
+    __shared__ float red[kBackSlots][kBackGroups * kC + 1];
     const ConvArgs& a = g.f;
     const int slot = blockIdx.x * kBackSlots + threadIdx.y;
-    const int c = (blockIdx.y * kBackGroups + threadIdx.x) * kVec;
-    const bool on = slot < slots && c < a.D;
-    float dw[K + 1][kVec] = {};
-    if (on) {
+    const int c = (blockIdx.y * kBackGroups + threadIdx.x) * kC;
+    float2 dw[K + 1][kP];
+#pragma unroll
+    for (int k = 0; k <= K; ++k)
+#pragma unroll
+        for (int p = 0; p < kP; ++p) dw[k][p] = both(0.f);
+    if (slot < slots && c < a.D) {
         const Slot f = find_slot(a.rows, slot);
-        Taps<T, K> taps;
+        Taps<K> taps;
         taps.load(a.w, a.bias, c);
-        float past[K - 1][kVec], ds[K][kVec] = {};
+        float2 past[K - 1][kP], ds[K][kP];
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) input_row<T, K>(a, f, f.first - (K - 1) + j, c, past[j]);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int p = 0; p < kP; ++p) ds[k][p] = both(0.f);
         const T* x = static_cast<const T*>(a.x) + f.row0 * a.ldx + c;
         const T* dy = static_cast<const T*>(g.dy) + f.row0 * a.D + c;
         T* dx = static_cast<T*>(g.dx) + f.row0 * a.D + c;
-        const int end = f.first + f.len, tail_at = f.seq_len - (K - 1);
+        const int end = f.first + f.len, tail_at = f.seq_len - (K - 1), stop = end + K - 1;
         const int lo = f.first == 0 ? (g.dtail0 ? -(K - 1) : 0) : f.first;
-        for (int t = f.first; t < end + K - 1; ++t) {
+        Four<T> in_next[kBackBatch], up_next[kBackBatch];
+        auto fetch = [&](int t0) {
 #pragma unroll
-            for (int k = 0; k + 1 < K; ++k)
+            for (int i = 0; i < kBackBatch; ++i) {
+                if (t0 + i < min(stop, f.seq_len)) {
+                    in_next[i].load(x + (t0 + i) * a.ldx);
+                    up_next[i].load(dy + (size_t)(t0 + i) * a.D);
+                } else {
+                    in_next[i].zero();
+                    up_next[i].zero();                      // no gradient from behind the last token
+                }
+            }
+        };
+        fetch(f.first);
+        for (int t0 = f.first; t0 < stop; t0 += kBackBatch) {
+            Four<T> in[kBackBatch], up[kBackBatch];
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) ds[k][e] = ds[k + 1][e];
-            if (t < f.seq_len) {
-                float now[kVec], up[kVec];
-                load8(x + t * a.ldx, now);
-                load8(dy + (size_t)t * a.D, up);
+            for (int i = 0; i < kBackBatch; ++i) {
+                in[i] = in_next[i];
+                up[i] = up_next[i];
+            }
+            fetch(t0 + kBackBatch);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    float s = taps.b[e];
+            for (int i = 0; i < kBackBatch; ++i) {
+                const int t = t0 + i;
+                if (t >= stop) break;
+                float2 now[kP], d[kP];
+                in[i].get(now);
+                up[i].get(d);
 #pragma unroll
-                    for (int k = 0; k < K - 1; ++k) s = fmaf(taps.w[k][e], past[k][e], s);
-                    s = fmaf(taps.w[K - 1][e], now[e], s);
-                    const float d = a.swish ? up[e] * swish_slope(s, sigmoidf_(s)) : up[e];
-                    ds[K - 1][e] = d;
+                for (int p = 0; p < kP; ++p) {
+                    const float2 s = taps.sum(past, now[p], p);
+                    if (a.swish) d[p] = mul2(d[p], swish_slope2(s, sigmoid2(s)));
+#pragma unroll
+                    for (int k = 0; k + 1 < K; ++k) ds[k][p] = ds[k + 1][p];
+                    ds[K - 1][p] = d[p];
                     if (t < end) {
 #pragma unroll
-                        for (int k = 0; k < K - 1; ++k) dw[k][e] = fmaf(d, past[k][e], dw[k][e]);
-                        dw[K - 1][e] = fmaf(d, now[e], dw[K - 1][e]);
-                        dw[K][e] += d;
+                        for (int k = 0; k < K - 1; ++k) dw[k][p] = fma2(d[p], past[k][p], dw[k][p]);
+                        dw[K - 1][p] = fma2(d[p], now[p], dw[K - 1][p]);
+                        dw[K][p] = add2(dw[K][p], d[p]);
                     }
-#pragma unroll
-                    for (int k = 0; k + 1 < K - 1; ++k) past[k][e] = past[k + 1][e];
-                    past[K - 2][e] = now[e];
                 }
-            } else {
+                shift_in<K>(past, now);
+                const int r = t - (K - 1);
+                if (r < lo) continue;
+                float2 out[kP];
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) ds[K - 1][e] = 0.f;
+                for (int p = 0; p < kP; ++p) out[p] = both(0.f);
+                if (g.dtail && r >= tail_at) {
+                    Four<T> x0;
+                    x0.load(static_cast<const T*>(g.dtail) + ((size_t)f.b * (K - 1) + (r - tail_at)) * a.D + c);
+                    x0.get(out);
+                }
+#pragma unroll
+                for (int p = 0; p < kP; ++p)
+#pragma unroll
+                    for (int j = 0; j < K; ++j) out[p] = fma2(taps.w[K - 1 - j][p], ds[j][p], out[p]);
+                if (r >= 0)
+                    store4(dx + (size_t)r * a.D, out);
+                else
+                    store4(static_cast<T*>(g.dtail0) + ((size_t)f.b * (K - 1) + (K - 1 + r)) * a.D + c, out);
             }
-            const int r = t - (K - 1);
-            if (r < lo) continue;
-            float out[kVec] = {};
-            if (g.dtail && r >= tail_at)
-                load8(static_cast<const T*>(g.dtail) + ((size_t)f.b * (K - 1) + (r - tail_at)) * a.D + c, out);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-#pragma unroll
-                for (int j = 0; j < K; ++j) out[e] = fmaf(taps.w[K - 1 - j][e], ds[j][e], out[e]);
-            if (r >= 0)
-                store8(dx + (size_t)r * a.D, out);
-            else
-                store8(static_cast<T*>(g.dtail0) + ((size_t)f.b * (K - 1) + (K - 1 + r)) * a.D + c, out);
         }
     }
     const int tid = threadIdx.y * kBackGroups + threadIdx.x;
-    const int ch = blockIdx.y * kBackGroups * kVec + tid;
+    const int ch = blockIdx.y * kBackGroups * kC + tid;
 #pragma unroll
     for (int k = 0; k <= K; ++k) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) red[threadIdx.y][threadIdx.x * kVec + e] = dw[k][e];
+        for (int p = 0; p < kP; ++p) {
+            red[threadIdx.y][threadIdx.x * kC + 2 * p] = dw[k][p].x;
+            red[threadIdx.y][threadIdx.x * kC + 2 * p + 1] = dw[k][p].y;
+        }
         __syncthreads();
         if (ch < a.D) {
             float s = 0.f;
@@ -204,14 +294,14 @@ __global__ void __launch_bounds__(kBackGroups* kBackSlots) short_conv_backward_k
         }
     }
 }
-static_assert(kBackGroups * kVec == kBackGroups * kBackSlots, "a thread of the block for each of its channels");
+static_assert(kBackGroups * kC == kBackGroups * kBackSlots, "a thread of the block for each of its channels");
 
 template <typename T, int K>
 cudaError_t conv_backward(ConvBackwardArgs g, cudaStream_t s) {
-    g.f.rows.seg = kBackSeg;
+    g.f.rows.seg = slot_tokens(kBackSeg, (long long)g.f.rows.B * g.f.rows.N, g.f.D);
     const long long slots = slots_of(g.f.rows);
     const int D = g.f.D;
-    const dim3 grid((unsigned)((slots + kBackSlots - 1) / kBackSlots), (D + kBackGroups * kVec - 1) / (kBackGroups * kVec));
+    const dim3 grid((unsigned)((slots + kBackSlots - 1) / kBackSlots), (D + kBackGroups * kC - 1) / (kBackGroups * kC));
     float* partial = static_cast<float*>(g.workspace);
     short_conv_backward_kernel<T, K><<<grid, dim3(kBackGroups, kBackSlots), 0, s>>>(g, partial, (int)slots);
     cudaError_t err = cudaGetLastError();
@@ -229,14 +319,14 @@ cudaError_t conv_backward(ConvBackwardArgs g, cudaStream_t s) {
 
 template <typename T, int K>
 cudaError_t conv(const ConvArgs& a, cudaStream_t s) {
-    const dim3 grid((unsigned)slots_of(a.rows), (a.D / kVec + kThreads - 1) / kThreads);
+    const dim3 grid((unsigned)slots_of(a.rows), (a.D / kC + kThreads - 1) / kThreads);
     short_conv_kernel<T, K><<<grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T, int K>
 cudaError_t conv_step(const ConvArgs& a, cudaStream_t s) {
-    const long long threads = (long long)a.rows.B * (a.D / kVec);
+    const long long threads = (long long)a.rows.B * (a.D / kC);
     short_conv_step_kernel<T, K><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
@@ -244,7 +334,7 @@ cudaError_t conv_step(const ConvArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_short_conv(ConvArgs a, cudaStream_t s) {
-    a.rows.seg = kSeg;
+    a.rows.seg = slot_tokens(kSeg, a.rows.cu ? a.rows.total : (long long)a.rows.B * a.rows.N, a.D);
     if (a.io == GRET_BF16) {
         if (a.K == 2) return conv<__nv_bfloat16, 2>(a, s);
         return a.K == 3 ? conv<__nv_bfloat16, 3>(a, s) : conv<__nv_bfloat16, 4>(a, s);
@@ -263,7 +353,8 @@ cudaError_t launch_short_conv_step(const ConvArgs& a, cudaStream_t s) {
 }
 
 size_t short_conv_backward_ws_bytes(int B, int N, int D, int K) {
-    const long long slots = (long long)B * ((N + kBackSeg - 1) / kBackSeg);
+    const int seg = slot_tokens(kBackSeg, (long long)B * N, D);
+    const long long slots = (long long)B * ((N + seg - 1) / seg);
     return align256((size_t)((slots + kBackSlots - 1) / kBackSlots) * (K + 1) * D * sizeof(float));
 }
 
