@@ -4,95 +4,189 @@
 //   p = rms(y) (.) w_post (.) swish(gate),  r = x + scale (.) p,  n = rms(r) (.) w_next
 //   rms(v) = v / sqrt(mean(v^2) + eps)
 //
-// A block of threads holds one row in registers: every input is read once and
-// every output written once, and both sums are taken from the registers in
-// fp32.  n is formed from r before r is rounded to its storage type.
+// A block of threads walks rows blockIdx.x, + gridDim.x, ...; each thread owns
+// the same 16-byte vectors of every row and copies them asynchronously into
+// shared memory kStages - 1 rows ahead.  It reads back only what it copied
+// itself, so the copies need no barrier; the only ones are the row sums', which
+// are taken from registers in fp32.  Every input is read once and every output
+// written once, and the memory bandwidth bounds the time.  n is formed from r
+// before r is rounded to its storage type.
 #include "gret_block.cuh"
 
 namespace gret {
 namespace {
 
-__device__ __forceinline__ float block_sum(float v, float* red, int warps) {
+// Copies of one thread's vectors of a row: `Parts` 16-byte pieces of each.
+template <typename T> constexpr int kParts = (int)sizeof(T) / 2;
+__device__ __forceinline__ void copy_async(uint4* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                 : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void copy_vector(uint4* to, const T* from) {
+#pragma unroll
+    for (int p = 0; p < kParts<T>; ++p) copy_async(to + p * blockDim.x, reinterpret_cast<const uint4*>(from) + p);
+}
+template <typename T>
+__device__ __forceinline__ void read_vector(const uint4* from, float* v) {
+    Raw<T> r;
+    const uint4 a = from[0];
+    if constexpr (kParts<T> == 1) {
+        r.a = a;
+    } else {
+        const uint4 b = from[blockDim.x];
+        r.a = reinterpret_cast<const float4&>(a);
+        r.b = reinterpret_cast<const float4&>(b);
+    }
+    r.get(v);
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// `red`: 32 words of shared memory; a caller takes others for the next two
+// sums, so that one barrier a sum is enough.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+    const int warps = blockDim.x >> 5;
     v = warp_sum(v);
+    if (warps == 1) return v;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < warps; ++w) s += red[w];
-    return s;
+    return warp_sum((threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f);
 }
 
-// TS: the residual stream's type; T: the block's.  Thread i holds the vectors
-// i, i + blockDim.x, ... of the row.
-template <typename TS, typename T, int V>
-__global__ void residual_norm_kernel(const NormArgs a) {
-    __shared__ float red[2][32];
-    const int warps = blockDim.x >> 5;
-    const long long t = blockIdx.x;
-    const TS* x = static_cast<const TS*>(a.x) + t * a.ldx;
-    const T* y = static_cast<const T*>(a.y) + (a.y ? t * a.ldy : 0);
-    const T* g = static_cast<const T*>(a.gate) + (a.gate ? t * a.ldg : 0);
-    float r[V][kVec], p[V][kVec];
+// Two sums behind one barrier; `red`: 64 words.
+__device__ __forceinline__ float2 block_sum(float2 v, float* red) {
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if (warps == 1) return v;
+    if (lane == 0) reinterpret_cast<float2*>(red)[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < warps ? reinterpret_cast<const float2*>(red)[lane] : make_float2(0.f, 0.f);
+    return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
+
+// A vector as four pairs.
+template <typename T>
+__device__ __forceinline__ void read_pairs(const uint4* from, float2* v) {
+    float x[kVec];
+    read_vector<T>(from, x);
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ void load_pairs(const float* p, float2* v) {
+    float x[kVec];
+    load8(p, x);
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+}
+
+// A parameter's values for the thread's vectors, or 1.
+template <int V>
+__device__ __forceinline__ void load_weights(float (*w)[kVec], const float* p, int D) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int c = (threadIdx.x + j * blockDim.x) * kVec;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) r[j][e] = p[j][e] = 0.f;
-        if (c < a.D) {
-            load8(x + c, r[j]);
-            if (a.y) load8(y + c, p[j]);
-        }
+        for (int e = 0; e < kVec; ++e) w[j][e] = 1.f;
+        if (p && c < D) load8(p + c, w[j]);
     }
-    if (a.y) {
-        float k = 1.f;
-        if (a.w_post) {
+}
+
+// TS: the residual stream's type; T: the block's.
+template <typename TS, typename T, int V, int kStages>
+__global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
+    extern __shared__ __align__(16) uint4 stage[];
+    __shared__ float red[4][32];
+    constexpr int kPieces = V * (kParts<TS> + 2 * kParts<T>);
+    const int D = a.D;
+    float w_post[V][kVec], w_next[V][kVec], scale[V][kVec];
+    load_weights<V>(w_post, a.w_post, D);
+    load_weights<V>(w_next, a.w_next, D);
+    load_weights<V>(scale, a.scale, D);
+    auto fetch = [&](long long t, int s) {
+        if (t < a.T) {
+            uint4* to = stage + (size_t)s * kPieces * blockDim.x + threadIdx.x;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = (threadIdx.x + j * blockDim.x) * kVec;
+                if (c < D) {
+                    copy_vector(to, static_cast<const TS*>(a.x) + t * a.ldx + c);
+                    if (a.y) copy_vector(to + kParts<TS> * blockDim.x, static_cast<const T*>(a.y) + t * a.ldy + c);
+                    if (a.gate)
+                        copy_vector(to + (kParts<TS> + kParts<T>)*blockDim.x, static_cast<const T*>(a.gate) + t * a.ldg + c);
+                }
+                to += (kParts<TS> + 2 * kParts<T>)*blockDim.x;
+            }
+        }
+        copies_end();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
+    int s = 0, turn = 0;
+    for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+        fetch(t + (long long)(kStages - 1) * gridDim.x, s == 0 ? kStages - 1 : s - 1);
+        copies_wait<kStages - 1>();
+        const uint4* from = stage + (size_t)s * kPieces * blockDim.x + threadIdx.x;
+        float r[V][kVec], p[V][kVec];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (threadIdx.x + j * blockDim.x) * kVec;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) r[j][e] = p[j][e] = 0.f;
+            if (c < D) {
+                read_vector<TS>(from, r[j]);
+                if (a.y) read_vector<T>(from + kParts<TS> * blockDim.x, p[j]);
+            }
+            from += (kParts<TS> + 2 * kParts<T>)*blockDim.x;
+        }
+        if (a.y) {
+            float k = 1.f;
+            if (a.w_post) {
+                float sq = 0.f;
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) sq = fmaf(p[j][e], p[j][e], sq);
+                k = rsqrtf(block_sum(sq, red[turn]) / (float)D + a.eps);
+            }
+            from = stage + (size_t)s * kPieces * blockDim.x + threadIdx.x + (kParts<TS> + kParts<T>)*blockDim.x;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = (threadIdx.x + j * blockDim.x) * kVec;
+                if (c < D) {
+                    float g[kVec];
+                    if (a.gate) read_vector<T>(from, g);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) {
+                        float v = p[j][e] * k * w_post[j][e] * scale[j][e];
+                        if (a.gate) v *= g[e] * sigmoid_fast(g[e]);
+                        r[j][e] += v;
+                    }
+                    store8(static_cast<TS*>(a.r) + t * D + c, r[j]);
+                }
+                from += (kParts<TS> + 2 * kParts<T>)*blockDim.x;
+            }
+        }
+        if (a.w_next) {
             float sq = 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j)
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) sq = fmaf(p[j][e], p[j][e], sq);
-            k = rsqrtf(block_sum(sq, red[0], warps) / (float)a.D + a.eps);
+                for (int e = 0; e < kVec; ++e) sq = fmaf(r[j][e], r[j][e], sq);
+            const float k = rsqrtf(block_sum(sq, red[turn + 1]) / (float)D + a.eps);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = (threadIdx.x + j * blockDim.x) * kVec;
+                if (c >= D) continue;
+                float n[kVec];
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) n[e] = w_next[j][e] * (r[j][e] * k);
+                store8(static_cast<T*>(a.n) + t * D + c, n);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (threadIdx.x + j * blockDim.x) * kVec;
-            if (c >= a.D) continue;
-            float w[kVec];
-            if (a.w_post) {
-                load8(a.w_post + c, w);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) p[j][e] *= k * w[e];
-            }
-            if (a.gate) {
-                load8(g + c, w);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) p[j][e] *= w[e] * sigmoidf_(w[e]);
-            }
-            if (a.scale) {
-                load8(a.scale + c, w);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) p[j][e] *= w[e];
-            }
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) r[j][e] += p[j][e];
-            store8(static_cast<TS*>(a.r) + t * a.D + c, r[j]);
-        }
-    }
-    if (!a.w_next) return;
-    float sq = 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sq = fmaf(r[j][e], r[j][e], sq);
-    const float k = rsqrtf(block_sum(sq, red[1], warps) / (float)a.D + a.eps);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int c = (threadIdx.x + j * blockDim.x) * kVec;
-        if (c >= a.D) continue;
-        float w[kVec];
-        load8(a.w_next + c, w);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) w[e] *= r[j][e] * k;
-        store8(static_cast<T*>(a.n) + t * a.D + c, w);
+        turn ^= 2;
+        s = s + 1 == kStages ? 0 : s + 1;
     }
 }
 
@@ -101,180 +195,256 @@ __global__ void residual_norm_kernel(const NormArgs a) {
 //   dx = dr + kr (t - rn mean(t rn)),  dscale = sum dx q swish(gate),  dw_next = sum dn rn
 //   dp = dx scale,  dgate = dp q swish'(gate),  dq = dp swish(gate),  dw_post = sum dq yn
 //   dy = ky (dq w_post - yn mean(dq w_post yn))
-// A block walks rows blockIdx.x, + gridDim.x, ... and keeps its share of the
-// three parameter gradients in registers.
-template <typename TS, typename T, int V>
+// Rows as in the forward; a block keeps its share of the three parameter
+// gradients in registers and leaves it to the column sums.
+template <typename TS, typename T, int V, int kStages>
 __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormBackwardArgs g, float* partial) {
-    __shared__ float red[4][32];
+    extern __shared__ __align__(16) uint4 stage[];
+    __shared__ __align__(16) float red[2][128];
     const NormArgs& a = g.f;
-    const int warps = blockDim.x >> 5;
-    float acc[3][V][kVec] = {};
+    constexpr int kPer = 2 * kParts<TS> + 3 * kParts<T>, kP = kVec / 2;    // pieces of a vector: x, dr; y, gate, dn
+    const int D = a.D;
+    const float2 one = both(1.f), none = both(0.f);
+    // dscale, dw_post, dw_next; and the parameters, where a thread has one vector and registers for them
+    constexpr bool kKeep = V == 1;
+    float2 acc[3][V][kP], kept[3][kP];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+#pragma unroll
+        for (int p = 0; p < V * kP; ++p) acc[i][p / kP][p % kP] = none;
+#pragma unroll
+        for (int p = 0; p < kP; ++p) kept[i][p] = one;
+        const float* w = i == 0 ? a.scale : i == 1 ? a.w_post : a.w_next;
+        if (kKeep && w && threadIdx.x * kVec < D) load_pairs(w + threadIdx.x * kVec, kept[i]);
+    }
+    auto weights = [&](const float* w, int i, int c, float2* to) {
+#pragma unroll
+        for (int p = 0; p < kP; ++p) to[p] = kKeep ? kept[i][p] : one;
+        if (!kKeep && w) load_pairs(w + c, to);
+    };
+    auto fetch = [&](long long t, int s) {
+        if (t < a.T) {
+            uint4* to = stage + (size_t)s * kPer * V * blockDim.x + threadIdx.x;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = (threadIdx.x + j * blockDim.x) * kVec;
+                if (c < D) {
+                    copy_vector(to, static_cast<const TS*>(a.x) + t * a.ldx + c);
+                    if (g.dr) copy_vector(to + kParts<TS> * blockDim.x, static_cast<const TS*>(g.dr) + t * D + c);
+                    uint4* rest = to + 2 * kParts<TS> * blockDim.x;
+                    if (a.y) copy_vector(rest, static_cast<const T*>(a.y) + t * a.ldy + c);
+                    if (a.gate) copy_vector(rest + kParts<T> * blockDim.x, static_cast<const T*>(a.gate) + t * a.ldg + c);
+                    if (g.dn) copy_vector(rest + 2 * kParts<T> * blockDim.x, static_cast<const T*>(g.dn) + t * D + c);
+                }
+                to += kPer * blockDim.x;
+            }
+        }
+        copies_end();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
+    const float over = 1.0f / (float)D;
+    int s = 0, turn = 0;
     for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
-        float x[V][kVec] = {}, y[V][kVec] = {}, gt[V][kVec] = {}, dn[V][kVec] = {}, dr[V][kVec] = {};
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (threadIdx.x + j * blockDim.x) * kVec;
-            if (c >= a.D) continue;
-            load8(static_cast<const TS*>(a.x) + t * a.ldx + c, x[j]);
-            if (a.y) load8(static_cast<const T*>(a.y) + t * a.ldy + c, y[j]);
-            if (a.gate) load8(static_cast<const T*>(a.gate) + t * a.ldg + c, gt[j]);
-            if (a.w_next) load8(static_cast<const T*>(g.dn) + t * a.D + c, dn[j]);
-            if (g.dr) load8(static_cast<const TS*>(g.dr) + t * a.D + c, dr[j]);
-        }
+        fetch(t + (long long)(kStages - 1) * gridDim.x, s == 0 ? kStages - 1 : s - 1);
+        copies_wait<kStages - 1>();
+        const uint4* row = stage + (size_t)s * kPer * V * blockDim.x + threadIdx.x;
+        float* sums = red[turn];
+        float2 r[V][kP], y[V][kP];                          // the sum r; y, then yn
         float ky = 1.f;
-        if (a.w_post) {
-            float sq = 0.f;
+        {
+            float2 sq = none;
 #pragma unroll
-            for (int j = 0; j < V; ++j)
+            for (int j = 0; j < V; ++j) {
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) sq = fmaf(y[j][e], y[j][e], sq);
-            ky = rsqrtf(block_sum(sq, red[0], warps) / (float)a.D + a.eps);
+                for (int p = 0; p < kP; ++p) y[j][p] = none;
+                if (a.y && (threadIdx.x + j * blockDim.x) * kVec < D)
+                    read_pairs<T>(row + (j * kPer + 2 * kParts<TS>)*blockDim.x, y[j]);
+#pragma unroll
+                for (int p = 0; p < kP; ++p) sq = fma2(y[j][p], y[j][p], sq);
+            }
+            if (a.w_post) ky = rsqrtf(block_sum(sq.x + sq.y, sums) * over + a.eps);
         }
-        if (a.y) {
+        float kr = 0.f, m = 0.f;
+        {
+            float2 s2 = none, s3 = none;                    // r^2, t r
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (c >= a.D) continue;
-                float wp[kVec], sc[kVec];
-                if (a.w_post) load8(a.w_post + c, wp);
-                if (a.scale) load8(a.scale + c, sc);
+                const uint4* from = row + j * kPer * blockDim.x;
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    float p = y[j][e] * ky;
-                    if (a.w_post) p *= wp[e];
-                    if (a.gate) p *= gt[j][e] * sigmoidf_(gt[j][e]);
-                    if (a.scale) p *= sc[e];
-                    x[j][e] += p;                               // r
+                for (int p = 0; p < kP; ++p) r[j][p] = none;
+                if (c >= D) continue;
+                read_pairs<TS>(from, r[j]);
+                from += 2 * kParts<TS> * blockDim.x;
+                float2 w[kP];
+                if (a.y) {
+                    float2 gt[kP], sc[kP];
+                    weights(a.w_post, 1, c, w);
+                    weights(a.scale, 0, c, sc);
+                    if (a.gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
+#pragma unroll
+                    for (int p = 0; p < kP; ++p) {
+                        y[j][p] = mul2(y[j][p], both(ky));
+                        float2 v = mul2(y[j][p], mul2(w[p], sc[p]));
+                        if (a.gate) v = mul2(v, mul2(gt[p], sigmoid2(gt[p])));
+                        r[j][p] = add2(r[j][p], v);
+                    }
                 }
+                if (a.w_next) {
+                    float2 dn[kP];
+                    weights(a.w_next, 2, c, w);
+                    read_pairs<T>(from + 2 * kParts<T> * blockDim.x, dn);
+#pragma unroll
+                    for (int p = 0; p < kP; ++p) {
+                        s2 = fma2(r[j][p], r[j][p], s2);
+                        s3 = fma2(mul2(dn[p], w[p]), r[j][p], s3);
+                    }
+                }
+            }
+            if (a.w_next) {
+                const float2 v = block_sum(make_float2(s2.x + s2.y, s3.x + s3.y), sums + 32);
+                kr = rsqrtf(v.x * over + a.eps);
+                m = v.y * kr * over;
             }
         }
-        if (a.w_next) {
-            float s2 = 0.f, s3 = 0.f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (c >= a.D) continue;
-                float wn[kVec];
-                load8(a.w_next + c, wn);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    s2 = fmaf(x[j][e], x[j][e], s2);
-                    s3 = fmaf(dn[j][e] * wn[e], x[j][e], s3);
-                }
-            }
-            s2 = block_sum(s2, red[1], warps);
-            s3 = block_sum(s3, red[2], warps);
-            const float kr = rsqrtf(s2 / (float)a.D + a.eps), m = s3 * kr / (float)a.D;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (c >= a.D) continue;
-                float wn[kVec];
-                load8(a.w_next + c, wn);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float rn = x[j][e] * kr;
-                    acc[2][j][e] = fmaf(dn[j][e], rn, acc[2][j][e]);
-                    dr[j][e] += kr * (dn[j][e] * wn[e] - rn * m);
-                }
-            }
-        }
-        float s4 = 0.f;
+        float2 s4 = none;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (threadIdx.x + j * blockDim.x) * kVec;
-            if (c >= a.D) continue;
-            store8(static_cast<TS*>(g.dx) + t * a.D + c, dr[j]);
-            if (!a.y) continue;
-            float wp[kVec], sc[kVec], dg[kVec];
-            if (a.w_post) load8(a.w_post + c, wp);
-            if (a.scale) load8(a.scale + c, sc);
+            if (c >= D) continue;
+            const uint4* from = row + j * kPer * blockDim.x;
+            float2 dr[kP], w[kP];
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const float yn = y[j][e] * ky, q = a.w_post ? yn * wp[e] : yn;
-                const float sig = a.gate ? sigmoidf_(gt[j][e]) : 1.f, sw = a.gate ? gt[j][e] * sig : 1.f;
-                const float dp = a.scale ? dr[j][e] * sc[e] : dr[j][e];
-                const float dq = dp * sw;
-                acc[0][j][e] = fmaf(dr[j][e], q * sw, acc[0][j][e]);
-                acc[1][j][e] = fmaf(dq, yn, acc[1][j][e]);
-                dg[e] = dp * q * swish_slope(gt[j][e], sig);
-                const float up = a.w_post ? dq * wp[e] : dq;
-                s4 = fmaf(up, yn, s4);
-                y[j][e] = yn;
-                dr[j][e] = up;
+            for (int p = 0; p < kP; ++p) dr[p] = none;
+            if (g.dr) read_pairs<TS>(from + kParts<TS> * blockDim.x, dr);
+            from += 2 * kParts<TS> * blockDim.x;
+            if (a.w_next) {
+                float2 dn[kP];
+                weights(a.w_next, 2, c, w);
+                read_pairs<T>(from + 2 * kParts<T> * blockDim.x, dn);
+#pragma unroll
+                for (int p = 0; p < kP; ++p) {
+                    const float2 rn = mul2(r[j][p], both(kr));
+                    acc[2][j][p] = fma2(dn[p], rn, acc[2][j][p]);
+                    dr[p] = fma2(both(kr), fma2(rn, both(-m), mul2(dn[p], w[p])), dr[p]);
+                }
             }
-            if (a.gate) store8(static_cast<T*>(g.dgate) + t * a.D + c, dg);
+            store_pairs(static_cast<TS*>(g.dx) + t * D + c, dr);
+            if (!a.y) continue;
+            float2 gt[kP], sc[kP], dg[kP];
+            weights(a.w_post, 1, c, w);
+            weights(a.scale, 0, c, sc);
+            if (a.gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                const float2 yn = y[j][p], q = mul2(yn, w[p]);
+                const float2 sig = a.gate ? sigmoid2(gt[p]) : one, sw = a.gate ? mul2(gt[p], sig) : one;
+                const float2 dp = mul2(dr[p], sc[p]), dq = mul2(dp, sw);
+                acc[0][j][p] = fma2(dr[p], mul2(q, sw), acc[0][j][p]);
+                acc[1][j][p] = fma2(dq, yn, acc[1][j][p]);
+                if (a.gate) dg[p] = mul2(mul2(dp, q), swish_slope2(gt[p], sig));
+                r[j][p] = mul2(dq, w[p]);                   // the gradient of yn
+                s4 = fma2(r[j][p], yn, s4);
+            }
+            if (a.gate) store_pairs(static_cast<T*>(g.dgate) + t * D + c, dg);
         }
         if (a.y) {
-            const float m = a.w_post ? block_sum(s4, red[3], warps) / (float)a.D : 0.f;
+            const float m4 = a.w_post ? block_sum(s4.x + s4.y, sums + 96) * over : 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (c >= a.D) continue;
+                if (c >= D) continue;
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) dr[j][e] = ky * (dr[j][e] - y[j][e] * m);
-                store8(static_cast<T*>(g.dy) + t * a.D + c, dr[j]);
+                for (int p = 0; p < kP; ++p) r[j][p] = mul2(both(ky), fma2(y[j][p], both(-m4), r[j][p]));
+                store_pairs(static_cast<T*>(g.dy) + t * D + c, r[j]);
             }
         }
-        __syncthreads();                                        // the sums' shared words are used again
+        turn ^= 1;
+        s = s + 1 == kStages ? 0 : s + 1;
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (threadIdx.x + j * blockDim.x) * kVec;
-            if (c < a.D) store8(partial + ((size_t)blockIdx.x * 3 + i) * a.D + c, acc[i][j]);
+            if (c < D) store_pairs(partial + ((size_t)blockIdx.x * 3 + i) * D + c, acc[i][j]);
         }
 }
 
+// Threads of a block for D channels, V vectors each.
+int block_threads(int D, int V) { return ((D / kVec + V - 1) / V + 31) & ~31; }
+int rows_grid(long long T, long long most) { return (int)(T < most ? T : most); }
+
+template <typename K>
+cudaError_t shared_limit(K kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename TS, typename T, int V>
+cudaError_t norm(const NormArgs& a, int num_sms, cudaStream_t s) {
+    constexpr int kStages = V == 2 && sizeof(T) == 4 ? 2 : 3;   // what fits in shared memory at 8192 channels
+    const int threads = block_threads(a.D, V), per_sm = (V == 1 ? 768 : 512) / threads;
+    const int bytes = kStages * V * (kParts<TS> + 2 * kParts<T>)*threads * 16;
+    auto k = residual_norm_kernel<TS, T, V, kStages>;
+    cudaError_t err = shared_limit(k, bytes);
+    if (err != cudaSuccess) return err;
+    k<<<rows_grid(a.T, (long long)num_sms * (per_sm > 0 ? per_sm : 1)), threads, bytes, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename TS, typename T>
+cudaError_t norm(const NormArgs& a, int num_sms, cudaStream_t s) {
+    return a.D <= 2048 ? norm<TS, T, 1>(a, num_sms, s) : norm<TS, T, 2>(a, num_sms, s);
+}
+
+int backward_vectors(int D) { return D <= 4096 ? 1 : 2; }
+int backward_grid(long long T, int D, int num_sms) {
+    const int per_sm = 512 / block_threads(D, backward_vectors(D));
+    return rows_grid(T, (long long)num_sms * per_sm);
+}
+
+template <typename TS, typename T, int V, int kStages>
 cudaError_t norm_backward(const NormBackwardArgs& g, int grid, cudaStream_t s) {
-    const int vecs = g.f.D / kVec, V = vecs <= 512 ? 1 : 2;
-    const int threads = ((vecs + V - 1) / V + 31) & ~31;
+    const int threads = block_threads(g.f.D, V);
+    const int bytes = kStages * V * (2 * kParts<TS> + 3 * kParts<T>)*threads * 16;
+    auto k = residual_norm_backward_kernel<TS, T, V, kStages>;
     float* partial = static_cast<float*>(g.workspace);
-    if (V == 1)
-        residual_norm_backward_kernel<TS, T, 1><<<grid, threads, 0, s>>>(g, partial);
-    else
-        residual_norm_backward_kernel<TS, T, 2><<<grid, threads, 0, s>>>(g, partial);
-    cudaError_t err = cudaGetLastError();
+    cudaError_t err = shared_limit(k, bytes);
+    if (err != cudaSuccess) return err;
+    k<<<grid, threads, bytes, s>>>(g, partial);
+    err = cudaGetLastError();
     if (err != cudaSuccess || (!g.dscale && !g.dw_post && !g.dw_next)) return err;
     const long long D = g.f.D;
     const ColumnOutputs out = {3, {0, D, 2 * D, 3 * D}, {g.dscale, g.dw_post, g.dw_next}, {1, 1, 1}};
     return launch_column_sums(partial, grid, out, s);
 }
 
+// Three rows in flight where they fit in shared memory.
 template <typename TS, typename T>
-cudaError_t norm(const NormArgs& a, cudaStream_t s) {
-    const int vecs = a.D / kVec;
-    const int V = vecs <= 256 ? 1 : 2;
-    const int threads = ((vecs + V - 1) / V + 31) & ~31;
-    if (V == 1)
-        residual_norm_kernel<TS, T, 1><<<(unsigned)a.T, threads, 0, s>>>(a);
-    else
-        residual_norm_kernel<TS, T, 2><<<(unsigned)a.T, threads, 0, s>>>(a);
-    return cudaGetLastError();
+cudaError_t norm_backward(const NormBackwardArgs& g, int grid, cudaStream_t s) {
+    if (backward_vectors(g.f.D) == 1) {
+        if constexpr (sizeof(T) == 2) return norm_backward<TS, T, 1, 3>(g, grid, s);
+        else return norm_backward<TS, T, 1, 2>(g, grid, s);
+    }
+    if constexpr (sizeof(T) == 2) return norm_backward<TS, T, 2, 2>(g, grid, s);
+    else return norm_backward<TS, T, 2, 1>(g, grid, s);
 }
 
 }  // namespace
 
 cudaError_t launch_residual_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
-    (void)num_sms;
-    if (a.io == GRET_F32) return norm<float, float>(a, s);
-    if (a.stream_type == GRET_F32) return norm<float, __nv_bfloat16>(a, s);
-    return norm<__nv_bfloat16, __nv_bfloat16>(a, s);
-}
-
-static int backward_grid(long long T, int num_sms) {
-    const long long most = 2LL * num_sms;
-    return (int)(T < most ? T : most);
+    if (a.io == GRET_F32) return norm<float, float>(a, num_sms, s);
+    if (a.stream_type == GRET_F32) return norm<float, __nv_bfloat16>(a, num_sms, s);
+    return norm<__nv_bfloat16, __nv_bfloat16>(a, num_sms, s);
 }
 
 size_t residual_norm_backward_ws_bytes(long long T, int D, int num_sms) {
-    return align256((size_t)backward_grid(T, num_sms) * 3 * D * sizeof(float));
+    return align256((size_t)backward_grid(T, D, num_sms) * 3 * D * sizeof(float));
 }
 
 cudaError_t launch_residual_norm_backward(NormBackwardArgs g, int num_sms, cudaStream_t s) {
-    const int grid = backward_grid(g.f.T, num_sms);
+    const int grid = backward_grid(g.f.T, g.f.D, num_sms);
     if (g.f.io == GRET_F32) return norm_backward<float, float>(g, grid, s);
     if (g.f.stream_type == GRET_F32) return norm_backward<float, __nv_bfloat16>(g, grid, s);
     return norm_backward<__nv_bfloat16, __nv_bfloat16>(g, grid, s);
