@@ -54,16 +54,29 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return warp_sum((threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f);
 }
 
-// Two sums behind one barrier; `red`: 64 words.
-__device__ __forceinline__ float2 block_sum(float2 v, float* red) {
+// N sums behind one barrier; `red`: 16 N words (at most 16 warps).
+template <int N>
+__device__ __forceinline__ void block_sums(float* v, float* red) {
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
-    if (warps == 1) return v;
-    if (lane == 0) reinterpret_cast<float2*>(red)[threadIdx.x >> 5] = v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    if (warps == 1) return;
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[i * 16 + (threadIdx.x >> 5)] = v[i];
     __syncthreads();
-    v = lane < warps ? reinterpret_cast<const float2*>(red)[lane] : make_float2(0.f, 0.f);
-    return make_float2(warp_sum(v.x), warp_sum(v.y));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        // four lanes' worth of words each, then over the four lanes
+        v[i] = 0.f;
+        if ((lane & 3) * 4 < warps) {
+            const float4 x = *reinterpret_cast<const float4*>(red + i * 16 + (lane & 3) * 4);
+            const int left = warps - (lane & 3) * 4;
+            v[i] = x.x + (left > 1 ? x.y : 0.f) + (left > 2 ? x.z : 0.f) + (left > 3 ? x.w : 0.f);
+        }
+        v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1);
+        v[i] += __shfl_xor_sync(0xffffffffu, v[i], 2);
+    }
 }
 
 // A vector as four pairs.
@@ -196,17 +209,20 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
 //   dp = dx scale,  dgate = dp q swish'(gate),  dq = dp swish(gate),  dw_post = sum dq yn
 //   dy = ky (dq w_post - yn mean(dq w_post yn))
 // Rows as in the forward; a block keeps its share of the three parameter
-// gradients in registers and leaves it to the column sums.
+// gradients in registers and leaves it to the column sums.  The last mean is
+// sum(dx v) / D with v = r - x, and dx is linear in dr, t and r: its parts are
+// summed with r^2 and t r, and the next row's y^2 with them, so that a row
+// costs one barrier.
 template <typename TS, typename T, int V, int kStages>
 __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormBackwardArgs g, float* partial) {
     extern __shared__ __align__(16) uint4 stage[];
-    __shared__ __align__(16) float red[2][128];
+    __shared__ __align__(16) float red[4][96];
     const NormArgs& a = g.f;
     constexpr int kPer = 2 * kParts<TS> + 3 * kParts<T>, kP = kVec / 2;    // pieces of a vector: x, dr; y, gate, dn
     const int D = a.D;
     const float2 one = both(1.f), none = both(0.f);
     // dscale, dw_post, dw_next; and the parameters, where a thread has one vector and registers for them
-    constexpr bool kKeep = V == 1;
+    constexpr bool kKeep = V == 1, kAhead = kStages >= 3;
     float2 acc[3][V][kP], kept[3][kP];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
@@ -244,71 +260,89 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
     const float over = 1.0f / (float)D;
+    // sum of y^2 over the thread's share of the row in stage s
+    auto square = [&](int s) {
+        float2 sq = none;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if ((threadIdx.x + j * blockDim.x) * kVec >= D) continue;
+            float2 y[kP];
+            read_pairs<T>(stage + (size_t)s * kPer * V * blockDim.x + threadIdx.x + (j * kPer + 2 * kParts<TS>)*blockDim.x, y);
+#pragma unroll
+            for (int p = 0; p < kP; ++p) sq = fma2(y[p], y[p], sq);
+        }
+        return sq.x + sq.y;
+    };
     int s = 0, turn = 0;
+    float y2 = 0.f;                                         // sum of y^2 of the row
+    if (kAhead && a.w_post) {
+        copies_wait<kStages - 2>();
+        y2 = square(0);
+        block_sums<1>(&y2, red[2]);
+    }
     for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
         fetch(t + (long long)(kStages - 1) * gridDim.x, s == 0 ? kStages - 1 : s - 1);
-        copies_wait<kStages - 1>();
+        copies_wait<kAhead ? kStages - 2 : kStages - 1>();
         const uint4* row = stage + (size_t)s * kPer * V * blockDim.x + threadIdx.x;
-        float* sums = red[turn];
-        float2 r[V][kP], y[V][kP];                          // the sum r; y, then yn
-        float ky = 1.f;
-        {
-            float2 sq = none;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-#pragma unroll
-                for (int p = 0; p < kP; ++p) y[j][p] = none;
-                if (a.y && (threadIdx.x + j * blockDim.x) * kVec < D)
-                    read_pairs<T>(row + (j * kPer + 2 * kParts<TS>)*blockDim.x, y[j]);
-#pragma unroll
-                for (int p = 0; p < kP; ++p) sq = fma2(y[j][p], y[j][p], sq);
-            }
-            if (a.w_post) ky = rsqrtf(block_sum(sq.x + sq.y, sums) * over + a.eps);
+        const int after = s + 1 == kStages ? 0 : s + 1;
+        if (!kAhead && a.w_post) {
+            y2 = square(s);
+            block_sums<1>(&y2, red[2 + turn]);
         }
-        float kr = 0.f, m = 0.f;
-        {
-            float2 s2 = none, s3 = none;                    // r^2, t r
+        const float ky = a.w_post ? rsqrtf(y2 * over + a.eps) : 1.f;
+        float2 r[V][kP], yn[V][kP];
+        // dr v, t v, r v, r^2, t r with v = r - x; and the next row's y^2
+        float2 sum[5] = {none, none, none, none, none};
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                const uint4* from = row + j * kPer * blockDim.x;
+        for (int j = 0; j < V; ++j) {
+            const int c = (threadIdx.x + j * blockDim.x) * kVec;
+            const uint4* from = row + j * kPer * blockDim.x;
 #pragma unroll
-                for (int p = 0; p < kP; ++p) r[j][p] = none;
-                if (c >= D) continue;
-                read_pairs<TS>(from, r[j]);
-                from += 2 * kParts<TS> * blockDim.x;
-                float2 w[kP];
-                if (a.y) {
-                    float2 gt[kP], sc[kP];
-                    weights(a.w_post, 1, c, w);
-                    weights(a.scale, 0, c, sc);
-                    if (a.gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
+            for (int p = 0; p < kP; ++p) r[j][p] = yn[j][p] = none;
+            if (c >= D) continue;
+            read_pairs<TS>(from, r[j]);
+            float2 v[kP], dr[kP], w[kP], dn[kP];
 #pragma unroll
-                    for (int p = 0; p < kP; ++p) {
-                        y[j][p] = mul2(y[j][p], both(ky));
-                        float2 v = mul2(y[j][p], mul2(w[p], sc[p]));
-                        if (a.gate) v = mul2(v, mul2(gt[p], sigmoid2(gt[p])));
-                        r[j][p] = add2(r[j][p], v);
-                    }
-                }
-                if (a.w_next) {
-                    float2 dn[kP];
-                    weights(a.w_next, 2, c, w);
-                    read_pairs<T>(from + 2 * kParts<T> * blockDim.x, dn);
+            for (int p = 0; p < kP; ++p) v[p] = dr[p] = none;
+            if (g.dr) read_pairs<TS>(from + kParts<TS> * blockDim.x, dr);
+            from += 2 * kParts<TS> * blockDim.x;
+            if (a.y) {
+                float2 gt[kP], sc[kP];
+                read_pairs<T>(from, yn[j]);
+                weights(a.w_post, 1, c, w);
+                weights(a.scale, 0, c, sc);
+                if (a.gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
 #pragma unroll
-                    for (int p = 0; p < kP; ++p) {
-                        s2 = fma2(r[j][p], r[j][p], s2);
-                        s3 = fma2(mul2(dn[p], w[p]), r[j][p], s3);
-                    }
+                for (int p = 0; p < kP; ++p) {
+                    yn[j][p] = mul2(yn[j][p], both(ky));
+                    v[p] = mul2(yn[j][p], mul2(w[p], sc[p]));
+                    if (a.gate) v[p] = mul2(v[p], mul2(gt[p], sigmoid2(gt[p])));
+                    r[j][p] = add2(r[j][p], v[p]);
+                    sum[0] = fma2(dr[p], v[p], sum[0]);
                 }
             }
             if (a.w_next) {
-                const float2 v = block_sum(make_float2(s2.x + s2.y, s3.x + s3.y), sums + 32);
-                kr = rsqrtf(v.x * over + a.eps);
-                m = v.y * kr * over;
+                weights(a.w_next, 2, c, w);
+                read_pairs<T>(from + 2 * kParts<T> * blockDim.x, dn);
+#pragma unroll
+                for (int p = 0; p < kP; ++p) {
+                    const float2 tt = mul2(dn[p], w[p]);
+                    sum[1] = fma2(tt, v[p], sum[1]);
+                    sum[2] = fma2(r[j][p], v[p], sum[2]);
+                    sum[3] = fma2(r[j][p], r[j][p], sum[3]);
+                    sum[4] = fma2(tt, r[j][p], sum[4]);
+                }
             }
         }
-        float2 s4 = none;
+        float all[6];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) all[i] = sum[i].x + sum[i].y;
+        all[5] = kAhead && a.w_post && t + gridDim.x < a.T ? square(after) : 0.f;
+        block_sums<6>(all, red[turn]);
+        y2 = all[5];
+        const float kr = a.w_next ? rsqrtf(all[3] * over + a.eps) : 0.f, m = all[4] * kr * over;
+        // mean of (gradient of yn) yn: the total gradient of r is dr + kr (t - r kr m)
+        const float m4 = a.w_post ? (all[0] + kr * (all[1] - kr * m * all[2])) * over : 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (threadIdx.x + j * blockDim.x) * kVec;
@@ -332,36 +366,25 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
             }
             store_pairs(static_cast<TS*>(g.dx) + t * D + c, dr);
             if (!a.y) continue;
-            float2 gt[kP], sc[kP], dg[kP];
+            float2 gt[kP], sc[kP], dy[kP];
             weights(a.w_post, 1, c, w);
             weights(a.scale, 0, c, sc);
             if (a.gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
-                const float2 yn = y[j][p], q = mul2(yn, w[p]);
+                const float2 q = mul2(yn[j][p], w[p]);
                 const float2 sig = a.gate ? sigmoid2(gt[p]) : one, sw = a.gate ? mul2(gt[p], sig) : one;
                 const float2 dp = mul2(dr[p], sc[p]), dq = mul2(dp, sw);
                 acc[0][j][p] = fma2(dr[p], mul2(q, sw), acc[0][j][p]);
-                acc[1][j][p] = fma2(dq, yn, acc[1][j][p]);
-                if (a.gate) dg[p] = mul2(mul2(dp, q), swish_slope2(gt[p], sig));
-                r[j][p] = mul2(dq, w[p]);                   // the gradient of yn
-                s4 = fma2(r[j][p], yn, s4);
+                acc[1][j][p] = fma2(dq, yn[j][p], acc[1][j][p]);
+                dy[p] = mul2(both(ky), fma2(yn[j][p], both(-m4), mul2(dq, w[p])));
+                if (a.gate) gt[p] = mul2(mul2(dp, q), swish_slope2(gt[p], sig));
             }
-            if (a.gate) store_pairs(static_cast<T*>(g.dgate) + t * D + c, dg);
-        }
-        if (a.y) {
-            const float m4 = a.w_post ? block_sum(s4.x + s4.y, sums + 96) * over : 0.f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (c >= D) continue;
-#pragma unroll
-                for (int p = 0; p < kP; ++p) r[j][p] = mul2(both(ky), fma2(y[j][p], both(-m4), r[j][p]));
-                store_pairs(static_cast<T*>(g.dy) + t * D + c, r[j]);
-            }
+            if (a.gate) store_pairs(static_cast<T*>(g.dgate) + t * D + c, gt);
+            store_pairs(static_cast<T*>(g.dy) + t * D + c, dy);
         }
         turn ^= 1;
-        s = s + 1 == kStages ? 0 : s + 1;
+        s = after;
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i)
