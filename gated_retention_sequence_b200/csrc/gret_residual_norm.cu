@@ -54,29 +54,38 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return warp_sum((threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f);
 }
 
-// N sums behind one barrier; `red`: 16 N words (at most 16 warps).
-template <int N>
+// Eight sums behind one barrier; `red`: 128 words (at most 16 warps).  Each
+// round halves the values a lane keeps, so that a lane ends with one of the
+// eight over its warp, and after the barrier with one over four warps.
 __device__ __forceinline__ void block_sums(float* v, float* red) {
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    float x[4];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-    if (warps == 1) return;
-    if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) red[i * 16 + (threadIdx.x >> 5)] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        // four lanes' worth of words each, then over the four lanes
-        v[i] = 0.f;
-        if ((lane & 3) * 4 < warps) {
-            const float4 x = *reinterpret_cast<const float4*>(red + i * 16 + (lane & 3) * 4);
-            const int left = warps - (lane & 3) * 4;
-            v[i] = x.x + (left > 1 ? x.y : 0.f) + (left > 2 ? x.z : 0.f) + (left > 3 ? x.w : 0.f);
-        }
-        v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1);
-        v[i] += __shfl_xor_sync(0xffffffffu, v[i], 2);
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 16;
+        x[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 8;
+        x[i] = (up ? x[i + 2] : x[i]) + __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + 2], 8);
+    }
+    const bool up = lane & 4;
+    float sum = (up ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, up ? x[0] : x[1], 4);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    if (warps > 1) {
+        // value lane / 4 of every warp: a quarter of the warps for each of its four lanes
+        if ((lane & 3) == 0) red[(lane >> 2) * 16 + (threadIdx.x >> 5)] = sum;
+        __syncthreads();
+        const float4 q = *reinterpret_cast<const float4*>(red + (lane >> 2) * 16 + (lane & 3) * 4);
+        const int left = warps - (lane & 3) * 4;
+        sum = (left > 0 ? q.x : 0.f) + (left > 1 ? q.y : 0.f) + (left > 2 ? q.z : 0.f) + (left > 3 ? q.w : 0.f);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, sum, 4 * i);
 }
 
 // A vector as four pairs.
@@ -212,14 +221,18 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
 // gradients in registers and leaves it to the column sums.  The last mean is
 // sum(dx v) / D with v = r - x, and dx is linear in dr, t and r: its parts are
 // summed with r^2 and t r, and the next row's y^2 with them, so that a row
-// costs one barrier.
-template <typename TS, typename T, int V, int kStages>
+// costs one barrier.  kFull: every part is given and the threads' vectors fill
+// the row, so that no part's absence cuts the code into pieces that loads
+// cannot cross.
+template <typename TS, typename T, int V, int kStages, bool kFull>
 __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormBackwardArgs g, float* partial) {
     extern __shared__ __align__(16) uint4 stage[];
-    __shared__ __align__(16) float red[4][96];
+    __shared__ __align__(16) float red[2][128], first[2][32];
     const NormArgs& a = g.f;
     constexpr int kPer = 2 * kParts<TS> + 3 * kParts<T>, kP = kVec / 2;    // pieces of a vector: x, dr; y, gate, dn
     const int D = a.D;
+    const bool has_y = kFull || a.y, has_gate = kFull || a.gate, has_next = kFull || a.w_next, has_dr = kFull || g.dr,
+               has_post = kFull || a.w_post;
     const float2 one = both(1.f), none = both(0.f);
     // dscale, dw_post, dw_next; and the parameters, where a thread has one vector and registers for them
     constexpr bool kKeep = V == 1, kAhead = kStages >= 3;
@@ -244,13 +257,13 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (c < D) {
+                if (kFull || c < D) {
                     copy_vector(to, static_cast<const TS*>(a.x) + t * a.ldx + c);
-                    if (g.dr) copy_vector(to + kParts<TS> * blockDim.x, static_cast<const TS*>(g.dr) + t * D + c);
+                    if (has_dr) copy_vector(to + kParts<TS> * blockDim.x, static_cast<const TS*>(g.dr) + t * D + c);
                     uint4* rest = to + 2 * kParts<TS> * blockDim.x;
-                    if (a.y) copy_vector(rest, static_cast<const T*>(a.y) + t * a.ldy + c);
-                    if (a.gate) copy_vector(rest + kParts<T> * blockDim.x, static_cast<const T*>(a.gate) + t * a.ldg + c);
-                    if (g.dn) copy_vector(rest + 2 * kParts<T> * blockDim.x, static_cast<const T*>(g.dn) + t * D + c);
+                    if (has_y) copy_vector(rest, static_cast<const T*>(a.y) + t * a.ldy + c);
+                    if (has_gate) copy_vector(rest + kParts<T> * blockDim.x, static_cast<const T*>(a.gate) + t * a.ldg + c);
+                    if (has_next) copy_vector(rest + 2 * kParts<T> * blockDim.x, static_cast<const T*>(g.dn) + t * D + c);
                 }
                 to += kPer * blockDim.x;
             }
@@ -265,7 +278,7 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
         float2 sq = none;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            if ((threadIdx.x + j * blockDim.x) * kVec >= D) continue;
+            if (!kFull && (threadIdx.x + j * blockDim.x) * kVec >= D) continue;
             float2 y[kP];
             read_pairs<T>(stage + (size_t)s * kPer * V * blockDim.x + threadIdx.x + (j * kPer + 2 * kParts<TS>)*blockDim.x, y);
 #pragma unroll
@@ -275,21 +288,21 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
     };
     int s = 0, turn = 0;
     float y2 = 0.f;                                         // sum of y^2 of the row
-    if (kAhead && a.w_post) {
+    if (kAhead && has_post) {
         copies_wait<kStages - 2>();
         y2 = square(0);
-        block_sums<1>(&y2, red[2]);
+        y2 = block_sum(y2, first[0]);
     }
     for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
         fetch(t + (long long)(kStages - 1) * gridDim.x, s == 0 ? kStages - 1 : s - 1);
         copies_wait<kAhead ? kStages - 2 : kStages - 1>();
         const uint4* row = stage + (size_t)s * kPer * V * blockDim.x + threadIdx.x;
         const int after = s + 1 == kStages ? 0 : s + 1;
-        if (!kAhead && a.w_post) {
+        if (!kAhead && has_post) {
             y2 = square(s);
-            block_sums<1>(&y2, red[2 + turn]);
+            y2 = block_sum(y2, first[turn]);
         }
-        const float ky = a.w_post ? rsqrtf(y2 * over + a.eps) : 1.f;
+        const float ky = has_post ? rsqrtf(y2 * over + a.eps) : 1.f;
         float2 r[V][kP], yn[V][kP];
         // dr v, t v, r v, r^2, t r with v = r - x; and the next row's y^2
         float2 sum[5] = {none, none, none, none, none};
@@ -299,29 +312,29 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
             const uint4* from = row + j * kPer * blockDim.x;
 #pragma unroll
             for (int p = 0; p < kP; ++p) r[j][p] = yn[j][p] = none;
-            if (c >= D) continue;
+            if (!kFull && c >= D) continue;
             read_pairs<TS>(from, r[j]);
             float2 v[kP], dr[kP], w[kP], dn[kP];
 #pragma unroll
             for (int p = 0; p < kP; ++p) v[p] = dr[p] = none;
-            if (g.dr) read_pairs<TS>(from + kParts<TS> * blockDim.x, dr);
+            if (has_dr) read_pairs<TS>(from + kParts<TS> * blockDim.x, dr);
             from += 2 * kParts<TS> * blockDim.x;
-            if (a.y) {
+            if (has_y) {
                 float2 gt[kP], sc[kP];
                 read_pairs<T>(from, yn[j]);
                 weights(a.w_post, 1, c, w);
                 weights(a.scale, 0, c, sc);
-                if (a.gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
+                if (has_gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
 #pragma unroll
                 for (int p = 0; p < kP; ++p) {
                     yn[j][p] = mul2(yn[j][p], both(ky));
                     v[p] = mul2(yn[j][p], mul2(w[p], sc[p]));
-                    if (a.gate) v[p] = mul2(v[p], mul2(gt[p], sigmoid2(gt[p])));
+                    if (has_gate) v[p] = mul2(v[p], mul2(gt[p], sigmoid2(gt[p])));
                     r[j][p] = add2(r[j][p], v[p]);
                     sum[0] = fma2(dr[p], v[p], sum[0]);
                 }
             }
-            if (a.w_next) {
+            if (has_next) {
                 weights(a.w_next, 2, c, w);
                 read_pairs<T>(from + 2 * kParts<T> * blockDim.x, dn);
 #pragma unroll
@@ -334,26 +347,26 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
                 }
             }
         }
-        float all[6];
+        float all[8] = {};
 #pragma unroll
         for (int i = 0; i < 5; ++i) all[i] = sum[i].x + sum[i].y;
-        all[5] = kAhead && a.w_post && t + gridDim.x < a.T ? square(after) : 0.f;
-        block_sums<6>(all, red[turn]);
+        all[5] = kAhead && has_post && t + gridDim.x < a.T ? square(after) : 0.f;
+        block_sums(all, red[turn]);
         y2 = all[5];
-        const float kr = a.w_next ? rsqrtf(all[3] * over + a.eps) : 0.f, m = all[4] * kr * over;
+        const float kr = has_next ? rsqrtf(all[3] * over + a.eps) : 0.f, m = all[4] * kr * over;
         // mean of (gradient of yn) yn: the total gradient of r is dr + kr (t - r kr m)
-        const float m4 = a.w_post ? (all[0] + kr * (all[1] - kr * m * all[2])) * over : 0.f;
+        const float m4 = has_post ? (all[0] + kr * (all[1] - kr * m * all[2])) * over : 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (threadIdx.x + j * blockDim.x) * kVec;
-            if (c >= D) continue;
+            if (!kFull && c >= D) continue;
             const uint4* from = row + j * kPer * blockDim.x;
             float2 dr[kP], w[kP];
 #pragma unroll
             for (int p = 0; p < kP; ++p) dr[p] = none;
-            if (g.dr) read_pairs<TS>(from + kParts<TS> * blockDim.x, dr);
+            if (has_dr) read_pairs<TS>(from + kParts<TS> * blockDim.x, dr);
             from += 2 * kParts<TS> * blockDim.x;
-            if (a.w_next) {
+            if (has_next) {
                 float2 dn[kP];
                 weights(a.w_next, 2, c, w);
                 read_pairs<T>(from + 2 * kParts<T> * blockDim.x, dn);
@@ -365,22 +378,22 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
                 }
             }
             store_pairs(static_cast<TS*>(g.dx) + t * D + c, dr);
-            if (!a.y) continue;
+            if (!has_y) continue;
             float2 gt[kP], sc[kP], dy[kP];
             weights(a.w_post, 1, c, w);
             weights(a.scale, 0, c, sc);
-            if (a.gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
+            if (has_gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 const float2 q = mul2(yn[j][p], w[p]);
-                const float2 sig = a.gate ? sigmoid2(gt[p]) : one, sw = a.gate ? mul2(gt[p], sig) : one;
+                const float2 sig = has_gate ? sigmoid2(gt[p]) : one, sw = has_gate ? mul2(gt[p], sig) : one;
                 const float2 dp = mul2(dr[p], sc[p]), dq = mul2(dp, sw);
                 acc[0][j][p] = fma2(dr[p], mul2(q, sw), acc[0][j][p]);
                 acc[1][j][p] = fma2(dq, yn[j][p], acc[1][j][p]);
                 dy[p] = mul2(both(ky), fma2(yn[j][p], both(-m4), mul2(dq, w[p])));
-                if (a.gate) gt[p] = mul2(mul2(dp, q), swish_slope2(gt[p], sig));
+                if (has_gate) gt[p] = mul2(mul2(dp, q), swish_slope2(gt[p], sig));
             }
-            if (a.gate) store_pairs(static_cast<T*>(g.dgate) + t * D + c, gt);
+            if (has_gate) store_pairs(static_cast<T*>(g.dgate) + t * D + c, gt);
             store_pairs(static_cast<T*>(g.dy) + t * D + c, dy);
         }
         turn ^= 1;
@@ -431,7 +444,10 @@ template <typename TS, typename T, int V, int kStages>
 cudaError_t norm_backward(const NormBackwardArgs& g, int grid, cudaStream_t s) {
     const int threads = block_threads(g.f.D, V);
     const int bytes = kStages * V * (2 * kParts<TS> + 3 * kParts<T>)*threads * 16;
-    auto k = residual_norm_backward_kernel<TS, T, V, kStages>;
+    const NormArgs& a = g.f;
+    const bool full = a.y && a.gate && a.scale && a.w_post && a.w_next && g.dr && threads * V * kVec == a.D;
+    auto k = full ? residual_norm_backward_kernel<TS, T, V, kStages, true>
+                  : residual_norm_backward_kernel<TS, T, V, kStages, false>;
     float* partial = static_cast<float*>(g.workspace);
     cudaError_t err = shared_limit(k, bytes);
     if (err != cudaSuccess) return err;
