@@ -115,13 +115,16 @@ __device__ __forceinline__ void load_weights(float (*w)[kVec], const float* p, i
     }
 }
 
-// TS: the residual stream's type; T: the block's.
-template <typename TS, typename T, int V, int kStages>
+// TS: the residual stream's type; T: the block's.  kFull: y, gate and both
+// norms are given and the threads' vectors fill the row, so that no part's
+// absence cuts the code into pieces that loads cannot cross.
+template <typename TS, typename T, int V, int kStages, bool kFull>
 __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
     extern __shared__ __align__(16) uint4 stage[];
     __shared__ float red[4][32];
     constexpr int kPieces = V * (kParts<TS> + 2 * kParts<T>);
     const int D = a.D;
+    const bool has_y = kFull || a.y, has_gate = kFull || a.gate, has_post = kFull || a.w_post, has_next = kFull || a.w_next;
     float w_post[V][kVec], w_next[V][kVec], scale[V][kVec];
     load_weights<V>(w_post, a.w_post, D);
     load_weights<V>(w_next, a.w_next, D);
@@ -132,10 +135,10 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (c < D) {
+                if (kFull || c < D) {
                     copy_vector(to, static_cast<const TS*>(a.x) + t * a.ldx + c);
-                    if (a.y) copy_vector(to + kParts<TS> * blockDim.x, static_cast<const T*>(a.y) + t * a.ldy + c);
-                    if (a.gate)
+                    if (has_y) copy_vector(to + kParts<TS> * blockDim.x, static_cast<const T*>(a.y) + t * a.ldy + c);
+                    if (has_gate)
                         copy_vector(to + (kParts<TS> + kParts<T>)*blockDim.x, static_cast<const T*>(a.gate) + t * a.ldg + c);
                 }
                 to += (kParts<TS> + 2 * kParts<T>)*blockDim.x;
@@ -156,15 +159,15 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
             const int c = (threadIdx.x + j * blockDim.x) * kVec;
 #pragma unroll
             for (int e = 0; e < kVec; ++e) r[j][e] = p[j][e] = 0.f;
-            if (c < D) {
+            if (kFull || c < D) {
                 read_vector<TS>(from, r[j]);
-                if (a.y) read_vector<T>(from + kParts<TS> * blockDim.x, p[j]);
+                if (has_y) read_vector<T>(from + kParts<TS> * blockDim.x, p[j]);
             }
             from += (kParts<TS> + 2 * kParts<T>)*blockDim.x;
         }
-        if (a.y) {
+        if (has_y) {
             float k = 1.f;
-            if (a.w_post) {
+            if (has_post) {
                 float sq = 0.f;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
@@ -176,13 +179,13 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (c < D) {
+                if (kFull || c < D) {
                     float g[kVec];
-                    if (a.gate) read_vector<T>(from, g);
+                    if (has_gate) read_vector<T>(from, g);
 #pragma unroll
                     for (int e = 0; e < kVec; ++e) {
                         float v = p[j][e] * k * w_post[j][e] * scale[j][e];
-                        if (a.gate) v *= g[e] * sigmoid_fast(g[e]);
+                        if (has_gate) v *= g[e] * sigmoid_fast(g[e]);
                         r[j][e] += v;
                     }
                     store8(static_cast<TS*>(a.r) + t * D + c, r[j]);
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
                 from += (kParts<TS> + 2 * kParts<T>)*blockDim.x;
             }
         }
-        if (a.w_next) {
+        if (has_next) {
             float sq = 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j)
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (c >= D) continue;
+                if (!kFull && c >= D) continue;
                 float n[kVec];
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) n[e] = w_next[j][e] * (r[j][e] * k);
@@ -422,7 +425,8 @@ cudaError_t norm(const NormArgs& a, int num_sms, cudaStream_t s) {
     constexpr int kStages = V == 2 && sizeof(T) == 4 ? 2 : 3;   // what fits in shared memory at 8192 channels
     const int threads = block_threads(a.D, V), per_sm = (V == 1 ? 768 : 512) / threads;
     const int bytes = kStages * V * (kParts<TS> + 2 * kParts<T>)*threads * 16;
-    auto k = residual_norm_kernel<TS, T, V, kStages>;
+    const bool full = a.y && a.gate && a.w_post && a.w_next && threads * V * kVec == a.D;
+    auto k = full ? residual_norm_kernel<TS, T, V, kStages, true> : residual_norm_kernel<TS, T, V, kStages, false>;
     cudaError_t err = shared_limit(k, bytes);
     if (err != cudaSuccess) return err;
     k<<<rows_grid(a.T, (long long)num_sms * (per_sm > 0 ? per_sm : 1)), threads, bytes, s>>>(a);
