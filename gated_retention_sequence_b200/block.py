@@ -28,83 +28,83 @@ class Activation(enum.IntEnum):
 
 # ---------------------------------------------------------------- raw C calls
 def gret_short_conv(x, ldx, w, bias, tail0, y, tail, B, N, D, K, io_dtype, act, stream) -> int:
-    return _g.load().gret_short_conv(x, ldx, w, bias, tail0, y, tail, B, N, D, K, int(io_dtype), int(act), stream)
+    return (_g._lib or _g.load()).gret_short_conv(x, ldx, w, bias, tail0, y, tail, B, N, D, K, int(io_dtype), int(act), stream)
 
 
 def gret_short_conv_varlen(x, ldx, w, bias, tail0, cu_seqlens, num_seqs, total_tokens, max_seqlen, y, tail, D, K,
                            io_dtype, act, stream) -> int:
-    return _g.load().gret_short_conv_varlen(x, ldx, w, bias, tail0, cu_seqlens, num_seqs, total_tokens, max_seqlen, y,
+    return (_g._lib or _g.load()).gret_short_conv_varlen(x, ldx, w, bias, tail0, cu_seqlens, num_seqs, total_tokens, max_seqlen, y,
                                             tail, D, K, int(io_dtype), int(act), stream)
 
 
 def gret_short_conv_step(x, ldx, w, bias, tail_in, tail_out, y, num_seqs, D, K, io_dtype, act, stream) -> int:
-    return _g.load().gret_short_conv_step(x, ldx, w, bias, tail_in, tail_out, y, num_seqs, D, K, int(io_dtype),
+    return (_g._lib or _g.load()).gret_short_conv_step(x, ldx, w, bias, tail_in, tail_out, y, num_seqs, D, K, int(io_dtype),
                                           int(act), stream)
 
 
 def gret_selective_scan(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, o, h_final, B, N, D, n,
                         io_dtype, workspace, workspace_bytes, stream) -> int:
-    return _g.load().gret_selective_scan(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, o, h_final,
+    return (_g._lib or _g.load()).gret_selective_scan(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, o, h_final,
                                          B, N, D, n, int(io_dtype), workspace, workspace_bytes, stream)
 
 
 def gret_selective_scan_workspace_size(B, N, D, n, io_dtype) -> int:
-    return _g.load().gret_selective_scan_workspace_size(B, N, D, n, int(io_dtype))
+    return (_g._lib or _g.load()).gret_selective_scan_workspace_size(B, N, D, n, int(io_dtype))
 
 
 def gret_selective_scan_varlen(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, cu_seqlens, num_seqs,
                                total_tokens, max_seqlen, o, h_final, D, n, io_dtype, workspace, workspace_bytes,
                                stream) -> int:
-    return _g.load().gret_selective_scan_varlen(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0,
+    return (_g._lib or _g.load()).gret_selective_scan_varlen(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0,
                                                 cu_seqlens, num_seqs, total_tokens, max_seqlen, o, h_final, D, n,
                                                 int(io_dtype), workspace, workspace_bytes, stream)
 
 
 def gret_selective_scan_varlen_workspace_size(num_seqs, total_tokens, max_seqlen, D, n, io_dtype) -> int:
-    return _g.load().gret_selective_scan_varlen_workspace_size(num_seqs, total_tokens, max_seqlen, D, n, int(io_dtype))
+    return (_g._lib or _g.load()).gret_selective_scan_varlen_workspace_size(num_seqs, total_tokens, max_seqlen, D, n, int(io_dtype))
 
 
 def gret_selective_step(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h_in, h_out, o, num_seqs, D, n,
                         io_dtype, stream) -> int:
-    return _g.load().gret_selective_step(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h_in, h_out, o,
+    return (_g._lib or _g.load()).gret_selective_step(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h_in, h_out, o,
                                          num_seqs, D, n, int(io_dtype), stream)
 
 
 def gret_residual_norm(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, r, n, T, D, eps, stream_dtype, io_dtype,
                        stream) -> int:
-    return _g.load().gret_residual_norm(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, r, n, T, D, eps,
+    return (_g._lib or _g.load()).gret_residual_norm(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, r, n, T, D, eps,
                                         int(stream_dtype), int(io_dtype), stream)
 
 
 def gret_short_conv_backward_workspace_size(B, N, D, K, io_dtype) -> int:
-    return _g.load().gret_short_conv_backward_workspace_size(B, N, D, K, int(io_dtype))
+    return (_g._lib or _g.load()).gret_short_conv_backward_workspace_size(B, N, D, K, int(io_dtype))
 
 
 def gret_short_conv_backward(x, ldx, w, bias, tail0, dy, dtail, dx, dw, dbias, dtail0, B, N, D, K, io_dtype, act,
                              workspace, workspace_bytes, stream) -> int:
-    return _g.load().gret_short_conv_backward(x, ldx, w, bias, tail0, dy, dtail, dx, dw, dbias, dtail0, B, N, D, K,
+    return (_g._lib or _g.load()).gret_short_conv_backward(x, ldx, w, bias, tail0, dy, dtail, dx, dw, dbias, dtail0, B, N, D, K,
                                               int(io_dtype), int(act), workspace, workspace_bytes, stream)
 
 
 def gret_selective_scan_backward_workspace_size(B, N, D, n, io_dtype) -> int:
-    return _g.load().gret_selective_scan_backward_workspace_size(B, N, D, n, int(io_dtype))
+    return (_g._lib or _g.load()).gret_selective_scan_backward_workspace_size(B, N, D, n, int(io_dtype))
 
 
 def gret_selective_scan_backward(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, dout, dh_final, du,
                                  ddt, dA, dBm, dCm, dskip, dz, ddt_bias, dh0, B, N, D, n, io_dtype, workspace,
                                  workspace_bytes, stream) -> int:
-    return _g.load().gret_selective_scan_backward(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0,
+    return (_g._lib or _g.load()).gret_selective_scan_backward(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0,
                                                   dout, dh_final, du, ddt, dA, dBm, dCm, dskip, dz, ddt_bias, dh0, B,
                                                   N, D, n, int(io_dtype), workspace, workspace_bytes, stream)
 
 
 def gret_residual_norm_backward_workspace_size(T, D) -> int:
-    return _g.load().gret_residual_norm_backward_workspace_size(T, D)
+    return (_g._lib or _g.load()).gret_residual_norm_backward_workspace_size(T, D)
 
 
 def gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, dr, dn, dx, dy, dgate, dscale, dw_post,
                                 dw_next, T, D, eps, stream_dtype, io_dtype, workspace, workspace_bytes, stream) -> int:
-    return _g.load().gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, dr, dn, dx, dy,
+    return (_g._lib or _g.load()).gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, dr, dn, dx, dy,
                                                  dgate, dscale, dw_post, dw_next, T, D, eps, int(stream_dtype),
                                                  int(io_dtype), workspace, workspace_bytes, stream)
 
@@ -112,17 +112,18 @@ def gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next
 # ---------------------------------------------------------------- helpers
 def _rows(t, name, dtype, shape, dev) -> int:
     """Check an activation and return its row stride."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous() and t.is_cuda:
+        return shape[-1]
     if not t.is_cuda or t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}" if t.is_cuda else f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.is_contiguous():
-        return shape[-1]
     # the dimensions with more than one entry lie `ld` rows apart, in order
+    strides = t.stride()
     ld, rows = 0, 1
-    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if size == 1:
             continue
         if not ld:
@@ -131,16 +132,22 @@ def _rows(t, name, dtype, shape, dev) -> int:
             ld = -1
             break
         rows *= size
-    if t.stride(-1) != 1 or (ld and ld < shape[-1]):
-        raise ValueError(f"the rows of {name} must be dense and equally far apart (strides {t.stride()})")
+    if strides[-1] != 1 or (rows > 1 and ld < shape[-1]):
+        raise ValueError(f"the rows of {name} must be dense and equally far apart (strides {strides})")
     if (ld * t.element_size()) % 16:
         raise ValueError(f"the rows of {name} must lie on 16-byte boundaries (row stride {ld})")
     return ld or shape[-1]
 
 
+def _dense(t, name, dtype, shape, dev):
+    """``_check``, quick where all is well."""
+    if not (t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous() and t.is_cuda):
+        _check(t, name, dtype, shape, dev)
+
+
 def _opt(t, name, dtype, shape, dev):
     if t is not None:
-        _check(t, name, dtype, shape, dev)
+        _dense(t, name, dtype, shape, dev)
 
 
 def _act(activation) -> Activation:
@@ -151,6 +158,20 @@ def _act(activation) -> Activation:
     raise ValueError(f"activation is 'swish' or 'none', got {activation!r}")
 
 
+class _Here:
+    """A call on the current stream of the current device: nothing to switch."""
+    __slots__ = ("handle",)
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return False
+
+
 @contextlib.contextmanager
 def _elsewhere(dev, stream):
     torch = _g._torch()
@@ -158,18 +179,13 @@ def _elsewhere(dev, stream):
         yield stream.cuda_stream
 
 
-@contextlib.contextmanager
-def _here(handle):
-    yield handle
-
-
 def _on(dev, stream):
     """The device and stream a call runs on, made current while it allocates and launches; gives the raw stream."""
     torch = _g._torch()
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
         if torch.cuda.current_device() == dev.index:
-            return _here(stream.cuda_stream)
+            return _Here(torch._C._cuda_getCurrentRawStream(dev.index))
+        stream = torch.cuda.current_stream(dev)
     return _elsewhere(dev, stream)
 
 
@@ -193,7 +209,7 @@ def _conv_weights(w, bias, D, dev):
     torch = _g._torch()
     if w.dim() != 2:
         raise ValueError(f"w has shape {tuple(w.shape)}, expected ({D}, taps)")
-    _check(w, "w", torch.float32, (D, w.shape[1]), dev)
+    _dense(w, "w", torch.float32, (D, w.shape[1]), dev)
     _opt(bias, "bias", torch.float32, (D,), dev)
     return w.shape[1]
 
@@ -216,9 +232,9 @@ def short_conv(x, w, bias=None, tail0=None, activation: Optional[str] = "swish",
     act = _act(activation)
     with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty((B, N, D), dtype=x.dtype, device=dev)
+            y = x.new_empty((B, N, D))
         if tail is None and want_tail:
-            tail = torch.empty((B, K - 1, D), dtype=x.dtype, device=dev)
+            tail = x.new_empty((B, K - 1, D))
         _raise_if(gret_short_conv(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(y), _ptr(tail), B, N, D, K, io,
                                   act, st), "gret_short_conv")
     return y, tail
@@ -236,16 +252,16 @@ def short_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, tail0=None, activ
     dev, io = x.device, _io_of(x)
     ldx = _rows(x, "x", x.dtype, x.shape, dev)
     K = _conv_weights(w, bias, D, dev)
-    _check(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev)
+    _dense(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev)
     _opt(tail0, "tail0", x.dtype, (S, K - 1, D), dev)
     _opt(y, "y", x.dtype, (T, D), dev)
     _opt(tail, "tail", x.dtype, (S, K - 1, D), dev)
     act = _act(activation)
     with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty((T, D), dtype=x.dtype, device=dev)
+            y = x.new_empty((T, D))
         if tail is None and want_tail:
-            tail = torch.empty((S, K - 1, D), dtype=x.dtype, device=dev)
+            tail = x.new_empty((S, K - 1, D))
         _raise_if(gret_short_conv_varlen(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(cu_seqlens), S, T,
                                          int(max_seqlen), _ptr(y), _ptr(tail), D, K, io, act, st),
                   "gret_short_conv_varlen")
@@ -261,7 +277,7 @@ def short_conv_step(x, w, bias, tail, activation: Optional[str] = "swish", y=Non
     dev, io = x.device, _io_of(x)
     ldx = _rows(x, "x", x.dtype, x.shape, dev)
     K = _conv_weights(w, bias, D, dev)
-    _check(tail, "tail", x.dtype, (S, K - 1, D), dev)
+    _dense(tail, "tail", x.dtype, (S, K - 1, D), dev)
     _opt(tail_out, "tail_out", x.dtype, (S, K - 1, D), dev)
     _opt(y, "y", x.dtype, (S, D), dev)
     act = _act(activation)
@@ -269,7 +285,7 @@ def short_conv_step(x, w, bias, tail, activation: Optional[str] = "swish", y=Non
         tail_out = tail
     with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty((S, D), dtype=x.dtype, device=dev)
+            y = x.new_empty((S, D))
         _raise_if(gret_short_conv_step(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail), _ptr(tail_out), _ptr(y), S, D, K,
                                        io, act, st), "gret_short_conv_step")
     return y, tail_out
@@ -286,12 +302,12 @@ def short_conv_backward(x, w, bias, dy, tail0=None, dtail=None, activation: Opti
     dev, io = x.device, _io_of(x)
     ldx = _rows(x, "x", x.dtype, x.shape, dev)
     K = _conv_weights(w, bias, D, dev)
-    _check(dy, "dy", x.dtype, (B, N, D), dev)
+    _dense(dy, "dy", x.dtype, (B, N, D), dev)
     _opt(tail0, "tail0", x.dtype, (B, K - 1, D), dev)
     _opt(dtail, "dtail", x.dtype, (B, K - 1, D), dev)
     act = _act(activation)
     with _on(dev, stream) as st:
-        g = {"dx": torch.empty((B, N, D), dtype=x.dtype, device=dev), "dw": torch.empty_like(w),
+        g = {"dx": x.new_empty((B, N, D)), "dw": torch.empty_like(w),
              "dbias": None if bias is None else torch.empty_like(bias),
              "dtail0": None if tail0 is None else torch.empty_like(tail0)}
         need = gret_short_conv_backward_workspace_size(B, N, D, K, io)
@@ -314,7 +330,7 @@ def _scan_inputs(u, dt, A, B, C, skip, z, dt_bias):
     ld = (_rows(u, "u", u.dtype, u.shape, dev), _rows(dt, "dt", u.dtype, u.shape, dev),
           _rows(B, "B", u.dtype, rows + (n,), dev), _rows(C, "C", u.dtype, rows + (n,), dev),
           _rows(z, "z", u.dtype, u.shape, dev) if z is not None else 0)
-    _check(A, "A", torch.float32, (D, n), dev)
+    _dense(A, "A", torch.float32, (D, n), dev)
     _opt(skip, "skip", torch.float32, (D,), dev)
     _opt(dt_bias, "dt_bias", torch.float32, (D,), dev)
     return dev, io, D, n, ld
@@ -334,7 +350,7 @@ def selective_scan(u, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, o=N
     _opt(h_final, "h_final", torch.float32, (b, D, n), dev)
     with _on(dev, stream) as st:
         if o is None:
-            o = torch.empty((b, N, D), dtype=u.dtype, device=dev)
+            o = u.new_empty((b, N, D))
         if h_final is None and want_state:
             h_final = torch.empty((b, D, n), dtype=torch.float32, device=dev)
         need = gret_selective_scan_workspace_size(b, N, D, n, io)
@@ -355,13 +371,13 @@ def selective_scan_varlen(u, dt, A, B, C, cu_seqlens, max_seqlen: int, skip=None
     T, D = u.shape
     S = cu_seqlens.numel() - 1
     dev, io, D, n, ld = _scan_inputs(u, dt, A, B, C, skip, z, dt_bias)
-    _check(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev)
+    _dense(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev)
     _opt(h0, "h0", torch.float32, (S, D, n), dev)
     _opt(o, "o", u.dtype, (T, D), dev)
     _opt(h_final, "h_final", torch.float32, (S, D, n), dev)
     with _on(dev, stream) as st:
         if o is None:
-            o = torch.empty((T, D), dtype=u.dtype, device=dev)
+            o = u.new_empty((T, D))
         if h_final is None and want_state:
             h_final = torch.empty((S, D, n), dtype=torch.float32, device=dev)
         need = gret_selective_scan_varlen_workspace_size(S, T, int(max_seqlen), D, n, io)
@@ -380,14 +396,14 @@ def selective_step(u, dt, A, B, C, h, skip=None, z=None, dt_bias=None, h_out=Non
     torch = _g._torch()
     S, D = u.shape
     dev, io, D, n, ld = _scan_inputs(u, dt, A, B, C, skip, z, dt_bias)
-    _check(h, "h", torch.float32, (S, D, n), dev)
+    _dense(h, "h", torch.float32, (S, D, n), dev)
     _opt(h_out, "h_out", torch.float32, (S, D, n), dev)
     _opt(o, "o", u.dtype, (S, D), dev)
     if h_out is None:
         h_out = h
     with _on(dev, stream) as st:
         if o is None:
-            o = torch.empty((S, D), dtype=u.dtype, device=dev)
+            o = u.new_empty((S, D))
         _raise_if(gret_selective_step(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
                                       _ptr(skip), _ptr(z), ld[4], _ptr(dt_bias), _ptr(h), _ptr(h_out), _ptr(o), S, D, n,
                                       io, st), "gret_selective_step")
@@ -403,11 +419,11 @@ def selective_scan_backward(u, dt, A, B, C, do, skip=None, z=None, dt_bias=None,
     torch = _g._torch()
     b, N, D = u.shape
     dev, io, D, n, ld = _scan_inputs(u, dt, A, B, C, skip, z, dt_bias)
-    _check(do, "do", u.dtype, (b, N, D), dev)
+    _dense(do, "do", u.dtype, (b, N, D), dev)
     _opt(h0, "h0", torch.float32, (b, D, n), dev)
     _opt(dh_final, "dh_final", torch.float32, (b, D, n), dev)
     with _on(dev, stream) as st:
-        row = lambda w: torch.empty((b, N, w), dtype=u.dtype, device=dev)  # noqa: E731
+        row = lambda w: u.new_empty((b, N, w))  # noqa: E731
         g = {"du": row(D), "ddt": row(D), "dA": torch.empty_like(A), "dB": row(n), "dC": row(n),
              "dz": None if z is None else row(D), "dskip": None if skip is None else torch.empty_like(skip),
              "ddt_bias": None if dt_bias is None else torch.empty_like(dt_bias),
@@ -463,9 +479,9 @@ def residual_norm(x, y=None, gate=None, scale=None, w_post=None, w_next=None, ep
         if y is None:
             r = x
         elif r is None:
-            r = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            r = x.new_empty(x.shape)
         if n is None and w_next is not None:
-            n = torch.empty(x.shape, dtype=io_torch, device=dev)
+            n = x.new_empty(x.shape, dtype=io_torch)
         _raise_if(gret_residual_norm(_ptr(x), ld[0], _ptr(y), ld[1], _ptr(gate), ld[2], _ptr(scale), _ptr(w_post),
                                      _ptr(w_next), _ptr(r) if y is not None else None, _ptr(n), T, D, float(eps), sd,
                                      io, st), "gret_residual_norm")
