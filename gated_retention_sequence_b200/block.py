@@ -189,6 +189,13 @@ def _on(dev, stream):
     return _elsewhere(dev, stream)
 
 
+def _like(t, dtype=None):
+    """A dense tensor of t's shape (torch's quicker allocation where t is dense itself)."""
+    if t.is_contiguous():
+        return _g._torch().empty_like(t, dtype=dtype)
+    return t.new_empty(t.shape, dtype=dtype)
+
+
 def _raise_if(status, what):
     if status:
         raise GretError(status, what)
@@ -232,7 +239,7 @@ def short_conv(x, w, bias=None, tail0=None, activation: Optional[str] = "swish",
     act = _act(activation)
     with _on(dev, stream) as st:
         if y is None:
-            y = x.new_empty((B, N, D))
+            y = _like(x)
         if tail is None and want_tail:
             tail = x.new_empty((B, K - 1, D))
         _raise_if(gret_short_conv(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(y), _ptr(tail), B, N, D, K, io,
@@ -259,7 +266,7 @@ def short_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, tail0=None, activ
     act = _act(activation)
     with _on(dev, stream) as st:
         if y is None:
-            y = x.new_empty((T, D))
+            y = _like(x)
         if tail is None and want_tail:
             tail = x.new_empty((S, K - 1, D))
         _raise_if(gret_short_conv_varlen(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(cu_seqlens), S, T,
@@ -285,7 +292,7 @@ def short_conv_step(x, w, bias, tail, activation: Optional[str] = "swish", y=Non
         tail_out = tail
     with _on(dev, stream) as st:
         if y is None:
-            y = x.new_empty((S, D))
+            y = _like(x)
         _raise_if(gret_short_conv_step(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail), _ptr(tail_out), _ptr(y), S, D, K,
                                        io, act, st), "gret_short_conv_step")
     return y, tail_out
@@ -307,7 +314,7 @@ def short_conv_backward(x, w, bias, dy, tail0=None, dtail=None, activation: Opti
     _opt(dtail, "dtail", x.dtype, (B, K - 1, D), dev)
     act = _act(activation)
     with _on(dev, stream) as st:
-        g = {"dx": x.new_empty((B, N, D)), "dw": torch.empty_like(w),
+        g = {"dx": _like(x), "dw": torch.empty_like(w),
              "dbias": None if bias is None else torch.empty_like(bias),
              "dtail0": None if tail0 is None else torch.empty_like(tail0)}
         need = gret_short_conv_backward_workspace_size(B, N, D, K, io)
@@ -350,7 +357,7 @@ def selective_scan(u, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, o=N
     _opt(h_final, "h_final", torch.float32, (b, D, n), dev)
     with _on(dev, stream) as st:
         if o is None:
-            o = u.new_empty((b, N, D))
+            o = _like(u)
         if h_final is None and want_state:
             h_final = torch.empty((b, D, n), dtype=torch.float32, device=dev)
         need = gret_selective_scan_workspace_size(b, N, D, n, io)
@@ -377,7 +384,7 @@ def selective_scan_varlen(u, dt, A, B, C, cu_seqlens, max_seqlen: int, skip=None
     _opt(h_final, "h_final", torch.float32, (S, D, n), dev)
     with _on(dev, stream) as st:
         if o is None:
-            o = u.new_empty((T, D))
+            o = _like(u)
         if h_final is None and want_state:
             h_final = torch.empty((S, D, n), dtype=torch.float32, device=dev)
         need = gret_selective_scan_varlen_workspace_size(S, T, int(max_seqlen), D, n, io)
@@ -403,7 +410,7 @@ def selective_step(u, dt, A, B, C, h, skip=None, z=None, dt_bias=None, h_out=Non
         h_out = h
     with _on(dev, stream) as st:
         if o is None:
-            o = u.new_empty((S, D))
+            o = _like(u)
         _raise_if(gret_selective_step(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
                                       _ptr(skip), _ptr(z), ld[4], _ptr(dt_bias), _ptr(h), _ptr(h_out), _ptr(o), S, D, n,
                                       io, st), "gret_selective_step")
@@ -479,9 +486,9 @@ def residual_norm(x, y=None, gate=None, scale=None, w_post=None, w_next=None, ep
         if y is None:
             r = x
         elif r is None:
-            r = x.new_empty(x.shape)
+            r = _like(x)
         if n is None and w_next is not None:
-            n = x.new_empty(x.shape, dtype=io_torch)
+            n = _like(x, io_torch)
         _raise_if(gret_residual_norm(_ptr(x), ld[0], _ptr(y), ld[1], _ptr(gate), ld[2], _ptr(scale), _ptr(w_post),
                                      _ptr(w_next), _ptr(r) if y is not None else None, _ptr(n), T, D, float(eps), sd,
                                      io, st), "gret_residual_norm")
@@ -504,7 +511,7 @@ def residual_norm_backward(x, y=None, dr=None, dn=None, gate=None, scale=None, w
     _opt(dr, "dr", x.dtype, x.shape, dev)
     _opt(dn, "dn", io_torch, x.shape, dev)
     with _on(dev, stream) as st:
-        row = lambda t, dtype: None if t is None else torch.empty(x.shape, dtype=dtype, device=dev)  # noqa: E731
+        row = lambda t, dtype: None if t is None else _like(x, dtype)  # noqa: E731
         par = lambda w: None if w is None else torch.empty_like(w)  # noqa: E731
         g = {"dx": row(x, x.dtype), "dy": row(y, io_torch), "dgate": row(gate, io_torch), "dscale": par(scale),
              "dw_post": par(w_post), "dw_next": par(w_next)}
