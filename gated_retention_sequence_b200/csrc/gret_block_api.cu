@@ -41,7 +41,8 @@ constexpr int kMaxChannels = 1 << 16;       // channel blocks are a grid's secon
 gret_status rows_ok(const Rows& r) {
     if (r.B <= 0 || r.N <= 0 || (r.cu && r.total <= 0)) return GRET_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(r.cu) & 3u) != 0) return GRET_ERR_INVALID_ARG;
-    if (!r.cu && (long long)r.B * r.N >= kMaxRows) return GRET_ERR_UNSUPPORTED;
+    // rows, and slots of at least one token and one more a sequence, in 31 bits
+    if ((r.cu ? (long long)r.total + r.B : (long long)r.B * r.N) >= kMaxRows) return GRET_ERR_UNSUPPORTED;
     return GRET_OK;
 }
 

@@ -7,14 +7,16 @@
 // slot (a segment of tokens) and keeps the last K-1 inputs in registers, so
 // that each input is read once, and K-1 more rows per slot.  Rows are loaded
 // kBatch at a time, a batch ahead: stores between the loads would otherwise
-// hold them up.
+// hold them up; whole batches take a path without a condition per row.
+// Measured at 16384 packed tokens x 4096 channels, bf16: 63 us (4.3 TB/s); with
+// eight channels a thread 104 us (188 registers), without loads ahead 73 us.
 #include "gret_block.cuh"
 
 namespace gret {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kSeg = 64, kBatch = 4, kC = 4, kP = kC / 2;
+constexpr int kSeg = 64, kBatch = 8, kC = 4, kP = kC / 2;
 
 // Four channels as they lie in memory.
 template <typename T> struct Four;
@@ -102,8 +104,10 @@ __device__ __forceinline__ void input_row(const ConvArgs& a, const Slot& f, int 
     r.get(v);
 }
 
+template <bool B> struct Flag { static constexpr bool value = B; };
+
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads, 5) short_conv_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const ConvArgs a) {
     const Slot f = find_slot(a.rows, blockIdx.x);
     const int c = (blockIdx.y * kThreads + threadIdx.x) * kC;
     if (f.b < 0 || c >= a.D) return;
@@ -115,19 +119,17 @@ __global__ void __launch_bounds__(kThreads, 5) short_conv_kernel(const ConvArgs 
     const T* x = static_cast<const T*>(a.x) + (f.row0 + f.first) * a.ldx + c;
     T* y = static_cast<T*>(a.y) + (f.row0 + f.first) * (long long)a.D + c;
     Four<T> next[kBatch];
+    auto fetch = [&](int left) {                            // x points at the batch's first row
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-        if (k < f.len) next[k].load(x + k * a.ldx);
-    for (int t0 = 0; t0 < f.len; t0 += kBatch) {
-        Four<T> in[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            in[k] = next[k];
-            if (t0 + kBatch + k < f.len) next[k].load(x + (t0 + kBatch + k) * a.ldx);
-        }
+        for (int k = 0; k < kBatch; ++k)
+            if (k < left) next[k].load(x + k * a.ldx);
+        x += kBatch * a.ldx;
+    };
+    // left: rows that remain; kWhole: a batch of them at least
+    auto walk = [&](const Four<T>* in, int left, auto whole) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            if (t0 + k >= f.len) break;
+            if (!decltype(whole)::value && k >= left) break;
             float2 now[kP], out[kP];
             in[k].get(now);
 #pragma unroll
@@ -136,8 +138,20 @@ __global__ void __launch_bounds__(kThreads, 5) short_conv_kernel(const ConvArgs 
                 out[p] = a.swish ? mul2(s, sigmoid2(s)) : s;
             }
             shift_in<K>(past, now);
-            store4(y + (size_t)(t0 + k) * a.D, out);
+            store4(y + k * (long long)a.D, out);
         }
+        y += kBatch * (long long)a.D;
+    };
+    fetch(f.len);
+    for (int left = f.len; left > 0; left -= kBatch) {
+        Four<T> in[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) in[k] = next[k];
+        fetch(left - kBatch);
+        if (left >= kBatch)
+            walk(in, left, Flag<true>());
+        else
+            walk(in, left, Flag<false>());
     }
     if (a.tail && f.s == max(f.segs, 1) - 1) {
 #pragma unroll
@@ -180,10 +194,12 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const ConvArg
 //   dw[k]   = sum_t ds[t] x[t-K+1+k],  dbias = sum_t ds[t]
 // and dtail adds to the last K-1 rows.  A thread walks one slot and K-1 tokens
 // past its end; the slots of a block add up their dw and dbias in shared memory.
-constexpr int kBackGroups = 32, kBackSlots = 4, kBackSeg = 128, kBackBatch = 2;
+// Issue slots bound it: 114 us at 16384 x 4096, bf16 (150 us with a condition
+// per row for the slot's ends).
+constexpr int kBackGroups = 32, kBackSlots = 4, kBackSeg = 128, kBackBatch = 4;
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kBackGroups* kBackSlots, 4) short_conv_backward_kernel(const ConvBackwardArgs g,
+__global__ void __launch_bounds__(kBackGroups* kBackSlots, 3) short_conv_backward_kernel(const ConvBackwardArgs g,
                                                                                      float* partial, int slots) {
     __shared__ float red[kBackSlots][kBackGroups * kC + 1];
     const ConvArgs& a = g.f;
@@ -205,37 +221,34 @@ __global__ void __launch_bounds__(kBackGroups* kBackSlots, 4) short_conv_backwar
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int p = 0; p < kP; ++p) ds[k][p] = both(0.f);
-        const T* x = static_cast<const T*>(a.x) + f.row0 * a.ldx + c;
-        const T* dy = static_cast<const T*>(g.dy) + f.row0 * a.D + c;
-        T* dx = static_cast<T*>(g.dx) + f.row0 * a.D + c;
         const int end = f.first + f.len, tail_at = f.seq_len - (K - 1), stop = end + K - 1;
         const int lo = f.first == 0 ? (g.dtail0 ? -(K - 1) : 0) : f.first;
+        const T* x = static_cast<const T*>(a.x) + (f.row0 + f.first) * a.ldx + c;
+        const T* dy = static_cast<const T*>(g.dy) + (f.row0 + f.first) * (long long)a.D + c;
+        T* dx = static_cast<T*>(g.dx) + (f.row0 + f.first - (K - 1)) * (long long)a.D + c;
         Four<T> in_next[kBackBatch], up_next[kBackBatch];
+        // x and dy point at row t0
         auto fetch = [&](int t0) {
+            const int have = min(stop, f.seq_len) - t0;
 #pragma unroll
             for (int i = 0; i < kBackBatch; ++i) {
-                if (t0 + i < min(stop, f.seq_len)) {
-                    in_next[i].load(x + (t0 + i) * a.ldx);
-                    up_next[i].load(dy + (size_t)(t0 + i) * a.D);
-                } else {
-                    in_next[i].zero();
-                    up_next[i].zero();                      // no gradient from behind the last token
+                in_next[i].zero();
+                up_next[i].zero();                          // no gradient from behind the last token
+                if (i < have) {
+                    in_next[i].load(x + i * a.ldx);
+                    up_next[i].load(dy + i * (long long)a.D);
                 }
             }
+            x += kBackBatch * a.ldx;
+            dy += kBackBatch * (long long)a.D;
         };
-        fetch(f.first);
-        for (int t0 = f.first; t0 < stop; t0 += kBackBatch) {
-            Four<T> in[kBackBatch], up[kBackBatch];
-#pragma unroll
-            for (int i = 0; i < kBackBatch; ++i) {
-                in[i] = in_next[i];
-                up[i] = up_next[i];
-            }
-            fetch(t0 + kBackBatch);
+        // rows t0 .. of the batch; kInside: all of them the slot's own, and all rows of dx that they end too
+        auto walk = [&](int t0, const Four<T>* in, const Four<T>* up, auto inside) {
+            constexpr bool kInside = decltype(inside)::value;
 #pragma unroll
             for (int i = 0; i < kBackBatch; ++i) {
                 const int t = t0 + i;
-                if (t >= stop) break;
+                if (!kInside && t >= stop) break;
                 float2 now[kP], d[kP];
                 in[i].get(now);
                 up[i].get(d);
@@ -246,7 +259,7 @@ __global__ void __launch_bounds__(kBackGroups* kBackSlots, 4) short_conv_backwar
 #pragma unroll
                     for (int k = 0; k + 1 < K; ++k) ds[k][p] = ds[k + 1][p];
                     ds[K - 1][p] = d[p];
-                    if (t < end) {
+                    if (kInside || t < end) {
 #pragma unroll
                         for (int k = 0; k < K - 1; ++k) dw[k][p] = fma2(d[p], past[k][p], dw[k][p]);
                         dw[K - 1][p] = fma2(d[p], now[p], dw[K - 1][p]);
@@ -255,11 +268,11 @@ __global__ void __launch_bounds__(kBackGroups* kBackSlots, 4) short_conv_backwar
                 }
                 shift_in<K>(past, now);
                 const int r = t - (K - 1);
-                if (r < lo) continue;
+                if (!kInside && r < lo) continue;
                 float2 out[kP];
 #pragma unroll
                 for (int p = 0; p < kP; ++p) out[p] = both(0.f);
-                if (g.dtail && r >= tail_at) {
+                if (!kInside && g.dtail && r >= tail_at) {
                     Four<T> x0;
                     x0.load(static_cast<const T*>(g.dtail) + ((size_t)f.b * (K - 1) + (r - tail_at)) * a.D + c);
                     x0.get(out);
@@ -268,11 +281,26 @@ __global__ void __launch_bounds__(kBackGroups* kBackSlots, 4) short_conv_backwar
                 for (int p = 0; p < kP; ++p)
 #pragma unroll
                     for (int j = 0; j < K; ++j) out[p] = fma2(taps.w[K - 1 - j][p], ds[j][p], out[p]);
-                if (r >= 0)
-                    store4(dx + (size_t)r * a.D, out);
+                if (kInside || r >= 0)
+                    store4(dx + i * (long long)a.D, out);
                 else
                     store4(static_cast<T*>(g.dtail0) + ((size_t)f.b * (K - 1) + (K - 1 + r)) * a.D + c, out);
             }
+            dx += kBackBatch * (long long)a.D;
+        };
+        fetch(f.first);
+        for (int t0 = f.first; t0 < stop; t0 += kBackBatch) {
+            Four<T> in[kBackBatch], up[kBackBatch];
+#pragma unroll
+            for (int i = 0; i < kBackBatch; ++i) {
+                in[i] = in_next[i];
+                up[i] = up_next[i];
+            }
+            fetch(t0 + kBackBatch);
+            if (t0 >= f.first + K - 1 && t0 + kBackBatch <= end && t0 + kBackBatch - K < tail_at)
+                walk(t0, in, up, Flag<true>());
+            else
+                walk(t0, in, up, Flag<false>());
         }
     }
     const int tid = threadIdx.y * kBackGroups + threadIdx.x;

@@ -54,7 +54,7 @@ def test_conv_step_and_varlen_refuse():
     (dict(Cm=None), INVALID), (dict(o=None), INVALID), (dict(A=P + 4), INVALID), (dict(z=P + 2, ldz=64), INVALID),
     (dict(z=P, ldz=0), INVALID), (dict(ldb=8), INVALID), (dict(ldc=17), INVALID), (dict(lddt=32), INVALID),
     (dict(n=12), UNSUPPORTED), (dict(n=128), UNSUPPORTED), (dict(n=0), INVALID), (dict(D=60), UNSUPPORTED),
-    (dict(io_dtype=3), INVALID), (dict(h0=P, h_final=P), INVALID), (dict(h0=P, h_final=P + 2 * 64 * 16 * 4 - 16), INVALID),
+    (dict(D=65544, ldu=65544, lddt=65544), UNSUPPORTED), (dict(io_dtype=3), INVALID), (dict(h0=P, h_final=P), INVALID), (dict(h0=P, h_final=P + 2 * 64 * 16 * 4 - 16), INVALID),
     ] + ROWS_BAD)
 def test_scan_refuses(over, expect):
     assert gret.gret_selective_scan(**dict(SCAN, **over)) == expect
@@ -69,6 +69,7 @@ def test_scan_step_and_varlen_refuse():
     var.update(cu_seqlens=P, num_seqs=2, total_tokens=9, max_seqlen=5)
     for over in (dict(cu_seqlens=None), dict(cu_seqlens=P + 1), dict(total_tokens=0), dict(max_seqlen=-1)):
         assert gret.gret_selective_scan_varlen(**dict(var, **over)) == INVALID, over
+    assert gret.gret_selective_scan_varlen(**dict(var, num_seqs=1 << 30, total_tokens=1 << 30)) == UNSUPPORTED
 
 
 @pytest.mark.parametrize("over,expect", [
@@ -123,3 +124,24 @@ def test_python_checks():
         gret.residual_norm(x, gate=x)
     with pytest.raises(ValueError, match="y or w_next"):
         gret.residual_norm(x)
+
+
+def test_row_strides():
+    """What a row stride may be: dense rows, equally far apart, on 16-byte boundaries."""
+    from gated_retention_sequence_b200.block import _rows
+
+    class Cuda(torch.Tensor):
+        is_cuda = True
+
+    def ld(t):
+        t = t.as_subclass(Cuda)
+        return _rows(t, "x", t.dtype, t.shape, t.device)
+
+    wide = torch.zeros(4, 6, 64, dtype=torch.bfloat16)
+    assert ld(wide) == 64 and ld(wide[..., 16:32]) == 64 and ld(wide[:1, :, :8]) == 64
+    assert ld(wide[:, ::2]) == 128 and ld(wide[:, :1, :8]) == 6 * 64 and ld(wide[:1, :1, 8:16]) == 8 and ld(wide[0, ::2, :8]) == 128
+    for bad, what in ((wide[:, :4:2], "equally"), (wide[:, :3, :8], "equally"), (wide.transpose(1, 2), "dense"),
+                      (wide[..., ::2], "dense"), (wide[:1].expand(4, 6, 64), "equally"),
+                      (torch.zeros(4, 12, dtype=torch.bfloat16)[:, :8], "16-byte")):
+        with pytest.raises(ValueError, match=what):
+            ld(bad)

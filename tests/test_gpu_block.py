@@ -219,6 +219,75 @@ def test_scan_long_and_cut():
         bo.check(h2[b], rh, "f32")
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+def test_scan_packed_and_cut(io, n):
+    # long sequences among empty and short ones, few channels: cut into segments
+    lens, D = [700, 0, 1500, 64, 1, 0, 333], 24
+    T = sum(lens) + 2
+    assert gret.gret_selective_scan_varlen_workspace_size(len(lens), T, max(lens), D, n, gret.Dtype.BF16) > 0
+    p = scan_inputs(io, T, D, n, len(lens))
+    o = torch.full((T, D), 7.0, dtype=TYPES[io], device="cuda")
+    _, h = gret.selective_scan_varlen(**p, cu_seqlens=offsets(lens), max_seqlen=max(lens), o=o)
+    at = 0
+    for b, m in enumerate(lens):
+        if m:
+            ro, rh = bo.selective_scan(**scan_rows(p, at, at + m, b))
+            bo.check(o[at:at + m], ro, io, f"o of sequence {b}")
+            bo.check(h[b], rh, "f32", f"h of sequence {b}")
+        else:
+            assert torch.equal(h[b], p["h0"][b])
+        at += m
+    assert (o[at:] == 7).all()
+
+
+def test_offsets_out_of_order():
+    # offsets that are no partition: nothing outside the rows they name is written, and no error is left behind
+    T, D, n = 400, 24, 16
+    p = scan_inputs("f32", T, D, n, 5)
+    c = conv_inputs("f32", T, D, 4, 5)
+    o = torch.full((T + 8, D), 7.0, device="cuda")
+    y = torch.full((T + 8, D), 7.0, device="cuda")
+    for cu in ([0, 900, 100, 380, -5, 390], [-3, -2, -1, 0, 0, 0], [400, 300, 200, 100, 50, 0], [2 ** 31 - 1] * 6):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        gret.selective_scan_varlen(**p, cu_seqlens=cu, max_seqlen=T, o=o[:T])
+        gret.short_conv_varlen(c["x"], c["w"], c["bias"], cu, T, tail0=c["tail0"], y=y[:T])
+        assert (o[T:] == 7).all() and (y[T:] == 7).all()
+    gret.check_device_status()
+
+
+def test_sequences_longer_than_max_seqlen_are_not_walked_on():
+    lens, D, n = [50, 30], 24, 16
+    p = scan_inputs("f32", 80, D, n, 2)
+    o = torch.full((80, D), 7.0, device="cuda")
+    _, h = gret.selective_scan_varlen(**p, cu_seqlens=offsets(lens), max_seqlen=40, o=o)
+    ro, rh = bo.selective_scan(**scan_rows(p, 0, 40, 0))
+    bo.check(o[:40], ro, "f32")
+    bo.check(h[0], rh, "f32")
+    assert (o[40:50] == 7).all()
+    bo.check(o[50:], bo.selective_scan(**scan_rows(p, 50, 80, 1))[0], "f32")
+
+
+def test_values_outside_the_rows_do_not_matter():
+    # NaN and infinity in rows behind the last sequence and in the states of other sequences stay where they are
+    lens, D, n = [37, 90], 24, 16
+    T = sum(lens) + 40
+    p = scan_inputs("bf16", T, D, n, 2)
+    c = conv_inputs("bf16", T, D, 4, 2)
+    cu = offsets(lens)
+    want, wh = gret.selective_scan_varlen(**p, cu_seqlens=cu, max_seqlen=90)
+    wy, _ = gret.short_conv_varlen(c["x"], c["w"], c["bias"], cu, 90, tail0=c["tail0"])
+    for k in ROWS:
+        p[k][sum(lens):] = float("nan")
+    c["x"][sum(lens):] = float("inf")
+    p["h0"][1] = float("inf")
+    c["tail0"][1] = float("nan")
+    got, gh = gret.selective_scan_varlen(**p, cu_seqlens=cu, max_seqlen=90)
+    gy, _ = gret.short_conv_varlen(c["x"], c["w"], c["bias"], cu, 90, tail0=c["tail0"])
+    assert torch.equal(got[:37], want[:37]) and torch.equal(gh[0], wh[0]) and torch.equal(gy[:37], wy[:37])
+    assert torch.equal(gy[40:127], wy[40:127])       # the tail reaches three rows
+
+
 def test_scan_extreme_steps():
     # steps from nothing (softplus of -90) to all (a decay that underflows), and decays of zero and one
     N, D, n = 64, 16, 16
@@ -492,3 +561,48 @@ def test_calls_on_a_given_stream():
     for a, b in zip(want, got):
         for s, t in zip(a, b):
             assert torch.equal(s, t)
+
+
+def test_gradients_in_two_graphs_and_beside_one_another():
+    """Two captured training passes, each with what it allocated, replayed in turn and after new inputs; and two
+    streams at work at once."""
+    B, N, D, n = 2, 90, 72, 16
+    sets = []
+    for seed in (5, 6):
+        p = scan_inputs("bf16", B * N, D, n, B, seed=seed)
+        c = conv_inputs("bf16", B * N, D, 4, B, seed=seed)
+        m = norm_inputs("bf16", "f32", B * N, D, seed=seed)
+        do, dr = draw(10, (B, N, D), "bf16", seed=seed), draw(11, (B * N, D), seed=seed)
+        sets.append((p, c, m, do, dr))
+
+    def one(s, stream=None):
+        p, c, m, do, dr = s
+        a = scan_backward_call(p, do, B, N, stream=stream)
+        b = gret.short_conv_backward(c["x"].view(B, N, D), c["w"], c["bias"], do, tail0=c["tail0"], stream=stream)
+        e = gret.residual_norm_backward(**m, dr=dr, dn=do.view(B * N, D), stream=stream)
+        o, h = scan_call(p, B, N, stream=stream)
+        return [v for g in (a, b, e) for v in g.values() if v is not None] + [o, h]
+
+    want = [[t.clone() for t in one(s)] for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    both = [one(s, st) for s, st in zip(sets, streams)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(one(s))
+        graphs.append(g)
+    for i in (0, 1, 1, 0):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for w, b, o in zip(want, both, outs):
+        for x, y, z in zip(w, b, o):
+            assert torch.equal(x, y) and torch.equal(x, z)
+    sets[0][0]["u"].mul_(0.5)                        # new values in the captured inputs
+    graphs[0].replay()
+    again = one(sets[0])
+    torch.cuda.synchronize()
+    for x, y in zip(again, outs[0]):
+        assert torch.equal(x, y)
