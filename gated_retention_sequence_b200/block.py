@@ -26,85 +26,89 @@ class Activation(enum.IntEnum):
     SWISH = 1
 
 
+def _lib():
+    return _g._lib or _g.load()
+
+
 # ---------------------------------------------------------------- raw C calls
 def gret_short_conv(x, ldx, w, bias, tail0, y, tail, B, N, D, K, io_dtype, act, stream) -> int:
-    return (_g._lib or _g.load()).gret_short_conv(x, ldx, w, bias, tail0, y, tail, B, N, D, K, int(io_dtype), int(act), stream)
+    return _lib().gret_short_conv(x, ldx, w, bias, tail0, y, tail, B, N, D, K, int(io_dtype), int(act), stream)
 
 
 def gret_short_conv_varlen(x, ldx, w, bias, tail0, cu_seqlens, num_seqs, total_tokens, max_seqlen, y, tail, D, K,
                            io_dtype, act, stream) -> int:
-    return (_g._lib or _g.load()).gret_short_conv_varlen(x, ldx, w, bias, tail0, cu_seqlens, num_seqs, total_tokens, max_seqlen, y,
+    return _lib().gret_short_conv_varlen(x, ldx, w, bias, tail0, cu_seqlens, num_seqs, total_tokens, max_seqlen, y,
                                             tail, D, K, int(io_dtype), int(act), stream)
 
 
 def gret_short_conv_step(x, ldx, w, bias, tail_in, tail_out, y, num_seqs, D, K, io_dtype, act, stream) -> int:
-    return (_g._lib or _g.load()).gret_short_conv_step(x, ldx, w, bias, tail_in, tail_out, y, num_seqs, D, K, int(io_dtype),
+    return _lib().gret_short_conv_step(x, ldx, w, bias, tail_in, tail_out, y, num_seqs, D, K, int(io_dtype),
                                           int(act), stream)
 
 
 def gret_selective_scan(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, o, h_final, B, N, D, n,
                         io_dtype, workspace, workspace_bytes, stream) -> int:
-    return (_g._lib or _g.load()).gret_selective_scan(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, o, h_final,
+    return _lib().gret_selective_scan(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, o, h_final,
                                          B, N, D, n, int(io_dtype), workspace, workspace_bytes, stream)
 
 
 def gret_selective_scan_workspace_size(B, N, D, n, io_dtype) -> int:
-    return (_g._lib or _g.load()).gret_selective_scan_workspace_size(B, N, D, n, int(io_dtype))
+    return _lib().gret_selective_scan_workspace_size(B, N, D, n, int(io_dtype))
 
 
 def gret_selective_scan_varlen(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, cu_seqlens, num_seqs,
                                total_tokens, max_seqlen, o, h_final, D, n, io_dtype, workspace, workspace_bytes,
                                stream) -> int:
-    return (_g._lib or _g.load()).gret_selective_scan_varlen(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0,
+    return _lib().gret_selective_scan_varlen(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0,
                                                 cu_seqlens, num_seqs, total_tokens, max_seqlen, o, h_final, D, n,
                                                 int(io_dtype), workspace, workspace_bytes, stream)
 
 
 def gret_selective_scan_varlen_workspace_size(num_seqs, total_tokens, max_seqlen, D, n, io_dtype) -> int:
-    return (_g._lib or _g.load()).gret_selective_scan_varlen_workspace_size(num_seqs, total_tokens, max_seqlen, D, n, int(io_dtype))
+    return _lib().gret_selective_scan_varlen_workspace_size(num_seqs, total_tokens, max_seqlen, D, n, int(io_dtype))
 
 
 def gret_selective_step(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h_in, h_out, o, num_seqs, D, n,
                         io_dtype, stream) -> int:
-    return (_g._lib or _g.load()).gret_selective_step(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h_in, h_out, o,
+    return _lib().gret_selective_step(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h_in, h_out, o,
                                          num_seqs, D, n, int(io_dtype), stream)
 
 
 def gret_residual_norm(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, r, n, T, D, eps, stream_dtype, io_dtype,
                        stream) -> int:
-    return (_g._lib or _g.load()).gret_residual_norm(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, r, n, T, D, eps,
+    return _lib().gret_residual_norm(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, r, n, T, D, eps,
                                         int(stream_dtype), int(io_dtype), stream)
 
 
 def gret_short_conv_backward_workspace_size(B, N, D, K, io_dtype) -> int:
-    return (_g._lib or _g.load()).gret_short_conv_backward_workspace_size(B, N, D, K, int(io_dtype))
+    return _lib().gret_short_conv_backward_workspace_size(B, N, D, K, int(io_dtype))
 
 
 def gret_short_conv_backward(x, ldx, w, bias, tail0, dy, dtail, dx, dw, dbias, dtail0, B, N, D, K, io_dtype, act,
                              workspace, workspace_bytes, stream) -> int:
-    return (_g._lib or _g.load()).gret_short_conv_backward(x, ldx, w, bias, tail0, dy, dtail, dx, dw, dbias, dtail0, B, N, D, K,
+    return _lib().gret_short_conv_backward(x, ldx, w, bias, tail0, dy, dtail, dx, dw, dbias, dtail0, B, N, D, K,
                                               int(io_dtype), int(act), workspace, workspace_bytes, stream)
 
 
 def gret_selective_scan_backward_workspace_size(B, N, D, n, io_dtype) -> int:
-    return (_g._lib or _g.load()).gret_selective_scan_backward_workspace_size(B, N, D, n, int(io_dtype))
+    return _lib().gret_selective_scan_backward_workspace_size(B, N, D, n, int(io_dtype))
 
 
 def gret_selective_scan_backward(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0, dout, dh_final, du,
                                  ddt, dA, dBm, dCm, dskip, dz, ddt_bias, dh0, B, N, D, n, io_dtype, workspace,
                                  workspace_bytes, stream) -> int:
-    return (_g._lib or _g.load()).gret_selective_scan_backward(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0,
+    return _lib().gret_selective_scan_backward(u, ldu, dt, lddt, A, Bm, ldb, Cm, ldc, skip, z, ldz, dt_bias, h0,
                                                   dout, dh_final, du, ddt, dA, dBm, dCm, dskip, dz, ddt_bias, dh0, B,
                                                   N, D, n, int(io_dtype), workspace, workspace_bytes, stream)
 
 
 def gret_residual_norm_backward_workspace_size(T, D) -> int:
-    return (_g._lib or _g.load()).gret_residual_norm_backward_workspace_size(T, D)
+    return _lib().gret_residual_norm_backward_workspace_size(T, D)
 
 
 def gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, dr, dn, dx, dy, dgate, dscale, dw_post,
                                 dw_next, T, D, eps, stream_dtype, io_dtype, workspace, workspace_bytes, stream) -> int:
-    return (_g._lib or _g.load()).gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, dr, dn, dx, dy,
+    return _lib().gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next, dr, dn, dx, dy,
                                                  dgate, dscale, dw_post, dw_next, T, D, eps, int(stream_dtype),
                                                  int(io_dtype), workspace, workspace_bytes, stream)
 
@@ -112,7 +116,7 @@ def gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next
 # ---------------------------------------------------------------- helpers
 def _rows(t, name, dtype, shape, dev) -> int:
     """Check an activation and return its row stride."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous() and t.is_cuda:
+    if t.is_cuda and t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
         return shape[-1]
     if not t.is_cuda or t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}" if t.is_cuda else f"{name} must be a CUDA tensor")
@@ -242,7 +246,7 @@ def short_conv(x, w, bias=None, tail0=None, activation: Optional[str] = "swish",
             y = _like(x)
         if tail is None and want_tail:
             tail = x.new_empty((B, K - 1, D))
-        _raise_if(gret_short_conv(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(y), _ptr(tail), B, N, D, K, io,
+        _raise_if(_lib().gret_short_conv(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(y), _ptr(tail), B, N, D, K, io,
                                   act, st), "gret_short_conv")
     return y, tail
 
@@ -269,7 +273,7 @@ def short_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, tail0=None, activ
             y = _like(x)
         if tail is None and want_tail:
             tail = x.new_empty((S, K - 1, D))
-        _raise_if(gret_short_conv_varlen(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(cu_seqlens), S, T,
+        _raise_if(_lib().gret_short_conv_varlen(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(cu_seqlens), S, T,
                                          int(max_seqlen), _ptr(y), _ptr(tail), D, K, io, act, st),
                   "gret_short_conv_varlen")
     return y, tail
@@ -293,7 +297,7 @@ def short_conv_step(x, w, bias, tail, activation: Optional[str] = "swish", y=Non
     with _on(dev, stream) as st:
         if y is None:
             y = _like(x)
-        _raise_if(gret_short_conv_step(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail), _ptr(tail_out), _ptr(y), S, D, K,
+        _raise_if(_lib().gret_short_conv_step(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail), _ptr(tail_out), _ptr(y), S, D, K,
                                        io, act, st), "gret_short_conv_step")
     return y, tail_out
 
@@ -319,7 +323,7 @@ def short_conv_backward(x, w, bias, dy, tail0=None, dtail=None, activation: Opti
              "dtail0": None if tail0 is None else torch.empty_like(tail0)}
         need = gret_short_conv_backward_workspace_size(B, N, D, K, io)
         workspace = _workspace(workspace, need, dev)
-        _raise_if(gret_short_conv_backward(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(dy), _ptr(dtail),
+        _raise_if(_lib().gret_short_conv_backward(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(dy), _ptr(dtail),
                                            _ptr(g["dx"]), _ptr(g["dw"]), _ptr(g["dbias"]), _ptr(g["dtail0"]), B, N, D,
                                            K, io, act, _ptr(workspace), need, st), "gret_short_conv_backward")
     return g
@@ -362,7 +366,7 @@ def selective_scan(u, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, o=N
             h_final = torch.empty((b, D, n), dtype=torch.float32, device=dev)
         need = gret_selective_scan_workspace_size(b, N, D, n, io)
         workspace = _workspace(workspace, need, dev)
-        _raise_if(gret_selective_scan(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
+        _raise_if(_lib().gret_selective_scan(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
                                       _ptr(skip), _ptr(z), ld[4], _ptr(dt_bias), _ptr(h0), _ptr(o), _ptr(h_final), b, N,
                                       D, n, io, _ptr(workspace), need, st), "gret_selective_scan")
     return o, h_final
@@ -389,7 +393,7 @@ def selective_scan_varlen(u, dt, A, B, C, cu_seqlens, max_seqlen: int, skip=None
             h_final = torch.empty((S, D, n), dtype=torch.float32, device=dev)
         need = gret_selective_scan_varlen_workspace_size(S, T, int(max_seqlen), D, n, io)
         workspace = _workspace(workspace, need, dev)
-        _raise_if(gret_selective_scan_varlen(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
+        _raise_if(_lib().gret_selective_scan_varlen(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
                                              _ptr(skip), _ptr(z), ld[4], _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), S,
                                              T, int(max_seqlen), _ptr(o), _ptr(h_final), D, n, io, _ptr(workspace),
                                              need, st), "gret_selective_scan_varlen")
@@ -411,7 +415,7 @@ def selective_step(u, dt, A, B, C, h, skip=None, z=None, dt_bias=None, h_out=Non
     with _on(dev, stream) as st:
         if o is None:
             o = _like(u)
-        _raise_if(gret_selective_step(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
+        _raise_if(_lib().gret_selective_step(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
                                       _ptr(skip), _ptr(z), ld[4], _ptr(dt_bias), _ptr(h), _ptr(h_out), _ptr(o), S, D, n,
                                       io, st), "gret_selective_step")
     return o, h_out
@@ -437,7 +441,7 @@ def selective_scan_backward(u, dt, A, B, C, do, skip=None, z=None, dt_bias=None,
              "dh0": torch.empty((b, D, n), dtype=torch.float32, device=dev) if h0 is not None or want_dh0 else None}
         need = gret_selective_scan_backward_workspace_size(b, N, D, n, io)
         workspace = _workspace(workspace, need, dev)
-        _raise_if(gret_selective_scan_backward(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
+        _raise_if(_lib().gret_selective_scan_backward(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
                                                _ptr(skip), _ptr(z), ld[4], _ptr(dt_bias), _ptr(h0), _ptr(do),
                                                _ptr(dh_final), _ptr(g["du"]), _ptr(g["ddt"]), _ptr(g["dA"]),
                                                _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dskip"]), _ptr(g["dz"]),
@@ -489,7 +493,7 @@ def residual_norm(x, y=None, gate=None, scale=None, w_post=None, w_next=None, ep
             r = _like(x)
         if n is None and w_next is not None:
             n = _like(x, io_torch)
-        _raise_if(gret_residual_norm(_ptr(x), ld[0], _ptr(y), ld[1], _ptr(gate), ld[2], _ptr(scale), _ptr(w_post),
+        _raise_if(_lib().gret_residual_norm(_ptr(x), ld[0], _ptr(y), ld[1], _ptr(gate), ld[2], _ptr(scale), _ptr(w_post),
                                      _ptr(w_next), _ptr(r) if y is not None else None, _ptr(n), T, D, float(eps), sd,
                                      io, st), "gret_residual_norm")
     return r, n
@@ -517,7 +521,7 @@ def residual_norm_backward(x, y=None, dr=None, dn=None, gate=None, scale=None, w
              "dw_post": par(w_post), "dw_next": par(w_next)}
         need = gret_residual_norm_backward_workspace_size(T, D)
         workspace = _workspace(workspace, need, dev)
-        _raise_if(gret_residual_norm_backward(_ptr(x), ld[0], _ptr(y), ld[1], _ptr(gate), ld[2], _ptr(scale),
+        _raise_if(_lib().gret_residual_norm_backward(_ptr(x), ld[0], _ptr(y), ld[1], _ptr(gate), ld[2], _ptr(scale),
                                               _ptr(w_post), _ptr(w_next), _ptr(dr), _ptr(dn), _ptr(g["dx"]),
                                               _ptr(g["dy"]), _ptr(g["dgate"]), _ptr(g["dscale"]), _ptr(g["dw_post"]),
                                               _ptr(g["dw_next"]), T, D, float(eps), sd, io, _ptr(workspace), need, st),

@@ -274,7 +274,7 @@ struct ScanArgs {
 bool selective_states_supported(int n);
 size_t selective_scan_ws_bytes(int B, int N, int total, int D, int n, bool packed, int num_sms);
 cudaError_t launch_selective_scan(ScanArgs a, int num_sms, cudaStream_t s);
-cudaError_t launch_selective_step(const ScanArgs& a, int num_sms, cudaStream_t s);   // h0 -> h, B rows
+cudaError_t launch_selective_step(const ScanArgs& a, cudaStream_t s);   // h0 -> h, B rows
 
 struct ScanBackwardArgs {
     ScanArgs f;          // inputs of the forward

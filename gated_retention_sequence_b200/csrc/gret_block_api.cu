@@ -192,9 +192,7 @@ gret_status gret_selective_step(const void* u, long long ldu, const void* dt, lo
                         Rows{nullptr, num_seqs, 1, 0, 0}, D, n, io_dtype, nullptr};
     if (gret_status e = scan_check(a)) return e;
     if (h_in != h_out && overlap(h_in, h_out, (size_t)num_seqs * D * n * sizeof(float))) return GRET_ERR_INVALID_ARG;
-    int sms = 0;
-    if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
-    return done(launch_selective_step(a, sms, cu_stream(stream)));
+    return done(launch_selective_step(a, cu_stream(stream)));
 }
 
 gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long long ldy, const void* gate,

@@ -417,6 +417,7 @@ int rows_grid(long long T, long long most) { return (int)(T < most ? T : most); 
 
 template <typename K>
 cudaError_t shared_limit(K kernel, int bytes) {
+    if (bytes <= 46 * 1024) return cudaSuccess;             // every kernel may have 48 KB, its static words included
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 

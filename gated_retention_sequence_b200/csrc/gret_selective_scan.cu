@@ -417,8 +417,7 @@ cudaError_t launch_selective_scan(ScanArgs a, int num_sms, cudaStream_t s) {
     }
 }
 
-cudaError_t launch_selective_step(const ScanArgs& a, int num_sms, cudaStream_t s) {
-    (void)num_sms;
+cudaError_t launch_selective_step(const ScanArgs& a, cudaStream_t s) {
     const bool bf = a.io == GRET_BF16;
     switch (a.n) {
         case 8: return bf ? step<__nv_bfloat16, 8>(a, s) : step<float, 8>(a, s);
