@@ -34,6 +34,78 @@ __device__ __forceinline__ void store_states(float* to, const float2 (*v)[SPL / 
                     make_float4(v[c][i].x, v[c][i].y, v[c][i + 1].x, v[c][i + 1].y);
 }
 
+// The fold that joins segments: x <- exp(A s_k) x + v_k for k = 0 .. count - 1,
+// four states a thread.  v_k, kFoldX threads next to one another, lies at
+// v + k stride and s_k at sums + k step; each is replaced by x after it
+// (kAfter) or before it.  Few threads walk many segments here, and one after
+// another their loads would bound the time, so Y threads take kFoldU segments
+// each: every thread folds its own from zero, the block (128 / Y, Y) carries x
+// through the parts, and each thread goes over its own again.  All threads of
+// the block call it; x has to be the same for all of a column, and is returned
+// after the last segment.  Y is 8 where a sequence may have more than
+// kFoldSerial segments, else 1: 127 segments of 512 channels x 16 states take
+// 10 us against 31, but 38 sequences of at most five segments x 4096 channels
+// 44 us against 9, as most of their threads have none.
+constexpr int kFoldU = 8, kFoldSerial = 16, kFoldThreads = 128;
+template <int Y> constexpr int kFoldX = kFoldThreads / Y;
+template <int Y>
+struct FoldShared {
+    float4 decay[Y][kFoldX<Y>], local[Y][kFoldX<Y>];
+};
+__device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
+    return make_float4(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y), fmaf(a.z, b.z, c.z), fmaf(a.w, b.w, c.w));
+}
+template <bool kAfter, int Y>
+__device__ __forceinline__ float4 fold_segments(FoldShared<Y>& shared, bool on, float* v, long long stride, const float* sums,
+                                                long long step, int count, float4 A, float4 x) {
+    const int tx = threadIdx.x, ty = threadIdx.y;
+    A = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
+    for (int base = 0; base < count; base += Y * kFoldU) {
+        const int first = base + ty * kFoldU, mine = on ? min(kFoldU, count - first) : 0;
+        float4 l[kFoldU];
+        float s[kFoldU];
+#pragma unroll
+        for (int j = 0; j < kFoldU; ++j)
+            if (j < mine) {
+                l[j] = *reinterpret_cast<const float4*>(v + (first + j) * stride);
+                s[j] = sums[(first + j) * step];
+            }
+        float4 here = x;
+        if constexpr (Y > 1) {
+            float4 own = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < kFoldU; ++j)
+                if (j < mine) {
+                    own = fma4(make_float4(exp2_approx(s[j] * A.x), exp2_approx(s[j] * A.y), exp2_approx(s[j] * A.z),
+                                           exp2_approx(s[j] * A.w)), own, l[j]);
+                    sum += s[j];
+                }
+            shared.decay[ty][tx] = make_float4(exp2_approx(sum * A.x), exp2_approx(sum * A.y), exp2_approx(sum * A.z),
+                                               exp2_approx(sum * A.w));
+            shared.local[ty][tx] = own;
+            __syncthreads();
+#pragma unroll
+            for (int y = 0; y < Y; ++y) {
+                if (y == ty) here = x;
+                x = fma4(shared.decay[y][tx], x, shared.local[y][tx]);
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int j = 0; j < kFoldU; ++j)
+            if (j < mine) {
+                float4* to = reinterpret_cast<float4*>(v + (first + j) * stride);
+                if (!kAfter) *to = here;
+                here = fma4(make_float4(exp2_approx(s[j] * A.x), exp2_approx(s[j] * A.y), exp2_approx(s[j] * A.z),
+                                        exp2_approx(s[j] * A.w)), here, l[j]);
+                if (kAfter) *to = here;
+            }
+        if (Y == 1) x = here;
+    }
+    return x;
+}
+
 // COUNT values, each held in parts by the lanes that differ in the bits First,
 // First / 2, ... Last of the lane: every round halves what a lane keeps, by the
 // bit, while the count is even, and otherwise adds all of it.  Returns how many

@@ -195,46 +195,21 @@ __global__ void __launch_bounds__(kScanWarps * 32, 4) ends_kernel(const ScanBack
 
 // h: the state before each segment; g: the gradient carried into its last token
 // from behind; both over the segments' own, in place.
-template <int NS>
-__global__ void __launch_bounds__(64) fold_kernel(const ScanBackwardArgs g, const Work w, int segs) {
+template <int NS, int Y>
+__global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanBackwardArgs g, const Work w, int segs) {
+    __shared__ FoldShared<Y> shared;
     const ScanArgs& a = g.f;
-    const int i = blockIdx.y * 64 + threadIdx.x, b = blockIdx.x;
-    if (i >= a.D * (NS / 4)) return;
-    const int d = i / (NS / 4), q = i % (NS / 4) * 4;
-    const size_t stride = (size_t)a.D * NS, own = ((size_t)b * a.D + d) * NS + q;
-    float4 A = *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q);
-    A = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 8;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        const float* start = side ? g.dh_final : a.h0;
-        float4 x = start ? *reinterpret_cast<const float4*>(start + own) : zero;
-        const long long first = (long long)b * segs + (side ? segs - 1 : 0);
-        const long long step = side ? -1 : 1;
-        float* v = (side ? w.g : w.h) + first * stride + (size_t)d * NS + q;
-        const float* s = w.steps + first * a.D + d;
-        for (int k = 0; k < segs; k += U) {
-            float4 local[U];
-            float sum[U];
-#pragma unroll
-            for (int j = 0; j < U; ++j)
-                if (k + j < segs) {
-                    local[j] = *reinterpret_cast<const float4*>(v + (k + j) * step * (long long)stride);
-                    sum[j] = s[(k + j) * step * a.D];
-                }
-#pragma unroll
-            for (int j = 0; j < U; ++j)
-                if (k + j < segs) {
-                    *reinterpret_cast<float4*>(v + (k + j) * step * (long long)stride) = x;
-                    x.x = fmaf(exp2_approx(sum[j] * A.x), x.x, local[j].x);
-                    x.y = fmaf(exp2_approx(sum[j] * A.y), x.y, local[j].y);
-                    x.z = fmaf(exp2_approx(sum[j] * A.z), x.z, local[j].z);
-                    x.w = fmaf(exp2_approx(sum[j] * A.w), x.w, local[j].w);
-                }
-        }
-        if (side && g.dh0) *reinterpret_cast<float4*>(g.dh0 + own) = x;
-    }
+    const int i = blockIdx.y * kFoldX<Y> + threadIdx.x, b = blockIdx.x;
+    const bool on = i < a.D * (NS / 4);
+    const int d = on ? i / (NS / 4) : 0, q = on ? i % (NS / 4) * 4 : 0;
+    const long long stride = (long long)a.D * NS, first = (long long)b * segs, last = first + segs - 1;
+    const size_t own = ((size_t)b * a.D + d) * NS + q, at = (size_t)d * NS + q;
+    const float4 A = *reinterpret_cast<const float4*>(a.A + at), none = make_float4(0.f, 0.f, 0.f, 0.f);
+    fold_segments<false, Y>(shared, on, w.h + first * stride + at, stride, w.steps + first * a.D + d, a.D, segs, A,
+                         a.h0 ? *reinterpret_cast<const float4*>(a.h0 + own) : none);
+    const float4 x = fold_segments<false, Y>(shared, on, w.g + last * stride + at, -stride, w.steps + last * a.D + d, -a.D,
+                                          segs, A, g.dh_final ? *reinterpret_cast<const float4*>(g.dh_final + own) : none);
+    if (g.dh0 && on && threadIdx.y == 0) *reinterpret_cast<float4*>(g.dh0 + own) = x;
 }
 
 template <typename T, int NS>
@@ -516,6 +491,12 @@ Parts parts_of(int B, int N, int D, int n) {
     return p;
 }
 
+template <int NS, int Y>
+void launch_fold(const ScanBackwardArgs& g, const Work& w, int segs, cudaStream_t s) {
+    const dim3 grid(g.f.rows.B, (g.f.D * (NS / 4) + kFoldX<Y> - 1) / kFoldX<Y>);
+    fold_kernel<NS, Y><<<grid, dim3(kFoldX<Y>, Y), 0, s>>>(g, w, segs);
+}
+
 template <typename T, int NS>
 cudaError_t backward(ScanBackwardArgs g, cudaStream_t s) {
     using L = Layout<NS>;
@@ -533,7 +514,11 @@ cudaError_t backward(ScanBackwardArgs g, cudaStream_t s) {
         err = cudaFuncSetAttribute(walk_kernel<T, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk_bytes);
     if (err != cudaSuccess) return err;
     ends_kernel<T, NS><<<grid, kScanWarps * 32, ends_bytes, s>>>(g, w);
-    fold_kernel<NS><<<dim3(a.rows.B, (a.D * (NS / 4) + 63) / 64), 64, 0, s>>>(g, w, (int)(slots / a.rows.B));
+    const int segs = (int)(slots / a.rows.B);
+    if (segs > kFoldSerial)
+        launch_fold<NS, 8>(g, w, segs, s);
+    else
+        launch_fold<NS, 1>(g, w, segs, s);
     walk_kernel<T, NS><<<grid, kScanWarps * 32, walk_bytes, s>>>(g, w);
     join_kernel<T><<<(unsigned)((rows * 2 * NS / 4 + 255) / 256), 256, 0, s>>>(w.bc, grid.y, rows, NS,
                                                                               static_cast<T*>(g.dBm), static_cast<T*>(g.dCm));

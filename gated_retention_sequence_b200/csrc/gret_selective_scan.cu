@@ -243,13 +243,13 @@ __global__ void __launch_bounds__(kWarps * 32, NS >= 32 ? 3 : 4) selective_scan_
 }
 
 // The state after every segment but the last, from the first one's and the
-// local ones of the others: h <- exp(A sum of the segment's steps) h + local,
-// over local in place.
-template <int NS>
-__global__ void __launch_bounds__(128) fold_kernel(const ScanArgs a, float* local, const float* steps) {
-    const int i = blockIdx.y * 128 + threadIdx.x, b = blockIdx.x;
-    if (i >= a.D * (NS / 4)) return;
-    const int d = i / (NS / 4), q = i % (NS / 4) * 4;
+// local ones of the others, over the local ones in place.
+template <int NS, int Y>
+__global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs a, float* local, const float* steps) {
+    __shared__ FoldShared<Y> shared;
+    const int i = blockIdx.y * kFoldX<Y> + threadIdx.x, b = blockIdx.x;
+    const bool on = i < a.D * (NS / 4);
+    const int d = on ? i / (NS / 4) : 0, q = on ? i % (NS / 4) * 4 : 0;
     int len = a.rows.N;
     if (a.rows.cu) {
         int row0;
@@ -258,32 +258,10 @@ __global__ void __launch_bounds__(128) fold_kernel(const ScanArgs a, float* loca
     }
     const int cuts = (len + a.rows.seg - 1) / a.rows.seg - 1;
     if (cuts <= 1) return;
-    const long long slot = slot_start(a.rows, b);
-    float4 A = *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q);
-    A = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
-    float* l = local + ((size_t)slot * a.D + d) * NS + q;
-    const float* s = steps + (size_t)slot * a.D + d;
-    float4 h = *reinterpret_cast<const float4*>(l);
-    constexpr int U = 8;
-    for (int k = 1; k < cuts; k += U) {
-        float4 v[U];
-        float w[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (k + j < cuts) {
-                v[j] = *reinterpret_cast<const float4*>(l + (size_t)(k + j) * a.D * NS);
-                w[j] = s[(size_t)(k + j) * a.D];
-            }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (k + j < cuts) {
-                h.x = fmaf(exp2_approx(w[j] * A.x), h.x, v[j].x);
-                h.y = fmaf(exp2_approx(w[j] * A.y), h.y, v[j].y);
-                h.z = fmaf(exp2_approx(w[j] * A.z), h.z, v[j].z);
-                h.w = fmaf(exp2_approx(w[j] * A.w), h.w, v[j].w);
-                *reinterpret_cast<float4*>(l + (size_t)(k + j) * a.D * NS) = h;
-            }
-    }
+    const long long slot = slot_start(a.rows, b), stride = (long long)a.D * NS;
+    float* first = local + slot * stride + (size_t)d * NS + q;
+    fold_segments<true, Y>(shared, on, first + stride, stride, steps + (slot + 1) * a.D + d, a.D, cuts - 1,
+                        *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q), *reinterpret_cast<const float4*>(first));
 }
 
 // Tokens of a segment: N leaves the sequences whole.  Measured with 16 states,
@@ -371,6 +349,12 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Scan
     }
 }
 
+template <int NS, int Y>
+void launch_fold(const ScanArgs& a, float* local, const float* steps, cudaStream_t s) {
+    const dim3 grid(a.rows.B, (a.D * (NS / 4) + kFoldX<Y> - 1) / kFoldX<Y>);
+    fold_kernel<NS, Y><<<grid, dim3(kFoldX<Y>, Y), 0, s>>>(a, local, steps);
+}
+
 template <typename T, int NS>
 cudaError_t scan(const ScanArgs& a, cudaStream_t s) {
     constexpr int W = Layout<NS>::W;
@@ -380,8 +364,12 @@ cudaError_t scan(const ScanArgs& a, cudaStream_t s) {
     float* steps = local + (size_t)slots * a.D * NS;
     selective_scan_kernel<T, NS, true><<<grid, kWarps * 32, 0, s>>>(a, local, steps);
     if (a.rows.seg < a.rows.N) {
-        if (2LL * a.rows.seg < a.rows.N)
-            fold_kernel<NS><<<dim3(a.rows.B, (a.D * (NS / 4) + 127) / 128), 128, 0, s>>>(a, local, steps);
+        if (2LL * a.rows.seg < a.rows.N) {
+            if ((long long)kFoldSerial * a.rows.seg < a.rows.N)
+                launch_fold<NS, 8>(a, local, steps, s);
+            else
+                launch_fold<NS, 1>(a, local, steps, s);
+        }
         selective_scan_kernel<T, NS, false><<<grid, kWarps * 32, 0, s>>>(a, local, steps);
     }
     return cudaGetLastError();
