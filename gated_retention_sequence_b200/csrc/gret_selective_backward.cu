@@ -299,6 +299,8 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
             }
             // and the way back; sums[token][channel]: y, sum of A g a h[t-1] (in log2 units), sum of g B
             float sums[G * kPair * 3];
+            constexpr int kLeft = parts_left<2 * SPL, 16, LPC>();  // of the lane's dB and dC values of a token
+            float left[G][kLeft];
 #pragma unroll
             for (int j = G - 1; j >= 0; --j) {
                 const int t = k * G + j;
@@ -336,21 +338,25 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
                     v[2 * i + 1] = bc[i].y;
                 }
                 add_parts<2 * SPL, 16, LPC>(v, lane);
-                constexpr int R = parts_left<2 * SPL, 16, LPC>();
-                constexpr int HOLDERS = 32 / LPC, TWINS = HOLDERS * R / (2 * SPL);
-                __syncwarp();
-                if (cg % TWINS == 0) {
-                    const int at = cg / TWINS * R;                     // of the lane's dB and dC values
-                    float* to = starts + k * L::START + j * 2 * NS + (at / SPL) * NS + q * SPL + at % SPL;
 #pragma unroll
-                    for (int i = 0; i < R; ++i) to[i] = v[i];
-                }
+                for (int i = 0; i < kLeft; ++i) left[j][i] = v[i];
             }
             add_parts<G * kPair * 3, LPC / 2, 1>(sums, lane);
             constexpr int R = parts_left<G * kPair * 3, LPC / 2, 1>();
             constexpr int TWINS = LPC * R / (G * kPair * 3);
             static_assert(R % 3 == 0, "whole channels");
             __syncwarp();
+            {
+                // dB, dC where the group's start was
+                constexpr int HOLDERS = 32 / LPC, SAME = HOLDERS * kLeft / (2 * SPL);
+                const int at = cg / SAME * kLeft;
+                float* to = starts + k * L::START + (at / SPL) * NS + q * SPL + at % SPL;
+                if (cg % SAME == 0)
+#pragma unroll
+                    for (int j = 0; j < G; ++j)
+#pragma unroll
+                        for (int i = 0; i < kLeft; ++i) to[j * 2 * NS + i] = left[j][i];
+            }
             if (q % TWINS == 0) {
                 // where the tokens' delta u and dy were: A g a h[t-1], g B, y
 #pragma unroll
