@@ -127,15 +127,15 @@ def _rows(t, name, dtype, shape, dev) -> int:
     # the dimensions with more than one entry lie `ld` rows apart, in order
     strides = t.stride()
     ld, rows = 0, 1
-    for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
-        if size == 1:
-            continue
-        if not ld:
-            ld = stride
-        elif stride != rows * ld:
-            ld = -1
-            break
-        rows *= size
+    for i in range(len(shape) - 2, -1, -1):
+        size = shape[i]
+        if size != 1:
+            if not ld:
+                ld = strides[i]
+            elif strides[i] != rows * ld:
+                ld = -1
+                break
+            rows *= size
     if strides[-1] != 1 or (rows > 1 and ld < shape[-1]):
         raise ValueError(f"the rows of {name} must be dense and equally far apart (strides {strides})")
     if (ld * t.element_size()) % 16:
