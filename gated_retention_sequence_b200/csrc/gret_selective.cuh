@@ -42,10 +42,9 @@ __device__ __forceinline__ void store_states(float* to, const float2 (*v)[SPL / 
 // each: every thread folds its own from zero, the block (128 / Y, Y) carries x
 // through the parts, and each thread goes over its own again.  All threads of
 // the block call it; x has to be the same for all of a column, and is returned
-// after the last segment.  Y is 8 where a sequence may have more than
-// kFoldSerial segments, else 1: 127 segments of 512 channels x 16 states take
-// 10 us against 31, but 38 sequences of at most five segments x 4096 channels
-// 44 us against 9, as most of their threads have none.
+// after the last segment.  Y is 8 for sequences of more than kFoldSerial
+// segments: 127 segments of 512 channels x 16 states take 10 us, and 31 with
+// one thread for all of a state's segments.
 constexpr int kFoldU = 8, kFoldSerial = 16, kFoldThreads = 128;
 template <int Y> constexpr int kFoldX = kFoldThreads / Y;
 template <int Y>

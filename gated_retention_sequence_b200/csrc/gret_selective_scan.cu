@@ -36,10 +36,12 @@ struct Layout {
 // scanned from shared memory, then gated and stored; the next tile's inputs are
 // in flight meanwhile.  kFinal: the outputs, from the state before the slot.
 // Otherwise the state that the slot alone leaves, from zero, and the sum of its
-// steps.  `leave`: where the state after the slot goes as well.
+// steps.  `before`: the state that the slot starts from, or the one `apart`
+// segments before it, whose own states and steps follow.  `leave`: where the
+// state after the slot goes as well.
 template <typename T, int NS, bool kFinal>
-__device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* shared, const float* before, float* leave,
-                                     float* steps) {
+__device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* shared, const float* before, int apart,
+                                     float* leave, float* steps) {
     using L = Layout<NS>;
     constexpr int SPL = L::SPL, LPC = L::LPC, W = L::W, LD = L::LD, LY = L::LY, V = L::V, BV = L::BV, H = SPL / 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.D;
@@ -56,6 +58,22 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* sh
     for (int c = 0; c < kPair; ++c)
 #pragma unroll
         for (int i = 0; i < H; ++i) A[c][i] = mul2(A[c][i], both(kLog2e));
+    if (kFinal) {
+#pragma unroll 2
+        for (int k = 1; k <= apart; ++k) {
+            const int d = d0 + g * kPair;
+            float2 own[kPair][H];
+            load_states<SPL>(own, before + (size_t)k * D * NS, NS, q, d, D);
+            const float2 sum = d < D ? *reinterpret_cast<const float2*>(steps + (size_t)k * D + d) : both(0.f);
+#pragma unroll
+            for (int c = 0; c < kPair; ++c)
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const float2 x = mul2(both(c ? sum.y : sum.x), A[c][i]);
+                    h[c][i] = fma2(make_float2(exp2_approx(x.x), exp2_approx(x.y)), h[c][i], own[c][i]);
+                }
+        }
+    }
 
     // staging: vector lane + 32 j of the tile is row / L::VR, always the same channels
     const int vc = d0 + (lane % L::VR) * kVec, vr = lane / L::VR;
@@ -223,29 +241,35 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* sh
 
 // A sequence that is cut is walked in two launches.  The first gives the first
 // segment's outputs, whose state before is known, and the local states of the
-// segments between the first and the last; the second, after the fold, the
-// other segments' outputs.  So two segments cost no token twice.
+// segments between the first and the last; the second the other segments'
+// outputs.  So two segments cost no token twice.  Up to kFoldSerial segments
+// are folded by the second launch's warps themselves, each from the first to
+// its own, which costs less than a launch; more are folded in between.
 template <typename T, int NS, bool kFirst>
 __global__ void __launch_bounds__(kWarps * 32, NS >= 32 ? 3 : 4) selective_scan_kernel(const ScanArgs a, float* local,
-                                                                                       float* steps) {
+                                                                                       float* steps, bool folded) {
     __shared__ __align__(16) float shared[kWarps * Layout<NS>::FLOATS];
     const Slot f = find_slot(a.rows, blockIdx.x);
     const bool last = f.s + 1 >= f.segs;
     if (f.b < 0 || (kFirst ? f.s > 0 && last : f.s == 0)) return;
     const size_t state = (size_t)a.D * NS;
     float* leave = !last ? local + blockIdx.x * state : a.h ? a.h + f.b * state : nullptr;
-    if (!kFirst)
-        walk<T, NS, true>(a, f, shared, local + (blockIdx.x - 1) * state, last ? leave : nullptr, nullptr);
-    else if (f.s == 0)
-        walk<T, NS, true>(a, f, shared, a.h0 ? a.h0 + f.b * state : nullptr, leave, nullptr);
-    else
-        walk<T, NS, false>(a, f, shared, nullptr, leave, steps + (size_t)blockIdx.x * a.D);
+    if (!kFirst) {
+        const int apart = folded ? 0 : f.s - 1;
+        const size_t from = blockIdx.x - 1 - apart;
+        walk<T, NS, true>(a, f, shared, local + from * state, apart, last ? leave : nullptr, steps + from * a.D);
+    } else if (f.s == 0) {
+        walk<T, NS, true>(a, f, shared, a.h0 ? a.h0 + f.b * state : nullptr, 0, leave, nullptr);
+    } else {
+        walk<T, NS, false>(a, f, shared, nullptr, 0, leave, steps + (size_t)blockIdx.x * a.D);
+    }
 }
 
 // The state after every segment but the last, from the first one's and the
 // local ones of the others, over the local ones in place.
-template <int NS, int Y>
+template <int NS>
 __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs a, float* local, const float* steps) {
+    constexpr int Y = 8;
     __shared__ FoldShared<Y> shared;
     const int i = blockIdx.y * kFoldX<Y> + threadIdx.x, b = blockIdx.x;
     const bool on = i < a.D * (NS / 4);
@@ -349,12 +373,6 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Scan
     }
 }
 
-template <int NS, int Y>
-void launch_fold(const ScanArgs& a, float* local, const float* steps, cudaStream_t s) {
-    const dim3 grid(a.rows.B, (a.D * (NS / 4) + kFoldX<Y> - 1) / kFoldX<Y>);
-    fold_kernel<NS, Y><<<grid, dim3(kFoldX<Y>, Y), 0, s>>>(a, local, steps);
-}
-
 template <typename T, int NS>
 cudaError_t scan(const ScanArgs& a, cudaStream_t s) {
     constexpr int W = Layout<NS>::W;
@@ -362,15 +380,13 @@ cudaError_t scan(const ScanArgs& a, cudaStream_t s) {
     const dim3 grid((unsigned)slots, (a.D + kWarps * W - 1) / (kWarps * W));
     float* local = static_cast<float*>(a.workspace);
     float* steps = local + (size_t)slots * a.D * NS;
-    selective_scan_kernel<T, NS, true><<<grid, kWarps * 32, 0, s>>>(a, local, steps);
+    selective_scan_kernel<T, NS, true><<<grid, kWarps * 32, 0, s>>>(a, local, steps, false);
     if (a.rows.seg < a.rows.N) {
-        if (2LL * a.rows.seg < a.rows.N) {
-            if ((long long)kFoldSerial * a.rows.seg < a.rows.N)
-                launch_fold<NS, 8>(a, local, steps, s);
-            else
-                launch_fold<NS, 1>(a, local, steps, s);
-        }
-        selective_scan_kernel<T, NS, false><<<grid, kWarps * 32, 0, s>>>(a, local, steps);
+        const bool fold = (long long)kFoldSerial * a.rows.seg < a.rows.N;
+        if (fold)
+            fold_kernel<NS><<<dim3(a.rows.B, (a.D * (NS / 4) + kFoldX<8> - 1) / kFoldX<8>), dim3(kFoldX<8>, 8), 0, s>>>(
+                a, local, steps);
+        selective_scan_kernel<T, NS, false><<<grid, kWarps * 32, 0, s>>>(a, local, steps, fold);
     }
     return cudaGetLastError();
 }
