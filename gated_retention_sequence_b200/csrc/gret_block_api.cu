@@ -81,7 +81,8 @@ gret_status scan_check(const ScanArgs& a) {
     if (!stride_ok(a.ldu, a.D, a.io) || !stride_ok(a.lddt, a.D, a.io) || !stride_ok(a.ldb, a.n, a.io) ||
         !stride_ok(a.ldc, a.n, a.io) || (a.z && !stride_ok(a.ldz, a.D, a.io)))
         return GRET_ERR_INVALID_ARG;
-    if ((long long)a.rows.B * a.D * a.n > (1LL << 38)) return GRET_ERR_UNSUPPORTED;
+    const long long rows = a.rows.cu ? (long long)a.rows.total : (long long)a.rows.B * a.rows.N;
+    if ((long long)a.rows.B * a.D * a.n > (1LL << 38) || rows * a.D > (1LL << 40)) return GRET_ERR_UNSUPPORTED;
     return GRET_OK;
 }
 

@@ -40,12 +40,12 @@ struct Layout {
 // segments before it, whose own states and steps follow.  `leave`: where the
 // state after the slot goes as well.
 template <typename T, int NS, bool kFinal>
-__device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* shared, const float* before, int apart,
-                                     float* leave, float* steps) {
+__device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, int block, float* shared, const float* before,
+                                     int apart, float* leave, float* steps) {
     using L = Layout<NS>;
     constexpr int SPL = L::SPL, LPC = L::LPC, W = L::W, LD = L::LD, LY = L::LY, V = L::V, BV = L::BV, H = SPL / 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.D;
-    const int d0 = (blockIdx.y * kWarps + warp) * W;
+    const int d0 = (block * kWarps + warp) * W;
     if (d0 >= D) return;
     // per token: (delta, delta, delta u, delta u) of each two channels; B; C; the sums over the states
     float *sd = shared + warp * L::FLOATS, *sb = sd + kTile * LD, *sc = sb + kTile * NS, *sy = sc + kTile * NS;
@@ -239,29 +239,83 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, float* sh
     }
 }
 
+// The rank-th segment of a packed batch in the order in which they are walked:
+// all whole segments first, then what is left of each sequence, so that the
+// launch does not end on long ones.  All 32 lanes call it together; it goes
+// over the offsets 32 at a time, and many sequences (over kRanked) take
+// find_slot's order.  38 sequences of 16384 tokens: SOMETHING.
+constexpr int kRanked = 256;
+__device__ __forceinline__ Slot find_ranked(const Rows& r, int rank) {
+    if (!r.cu || r.B > kRanked) return find_slot(r, rank);
+    const int lane = threadIdx.x & 31;
+    Slot f;
+    f.b = -1; f.s = 0; f.segs = 0; f.first = 0; f.len = 0; f.seq_len = 0; f.row0 = 0;
+    int b = -1, s = -1, base = 0;
+    for (int b0 = 0; b0 < r.B; b0 += 32) {
+        int row0 = 0, len = 0;
+        if (b0 + lane < r.B) packed_range(r.cu, b0 + lane, r.total, row0, len);
+        const int whole = min(len, r.N) / r.seg;
+        int upto = whole;
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + upto > rank);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            b = b0 + at;
+            s = rank - base - __shfl_sync(0xffffffffu, upto - whole, at);
+            break;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (b < 0) b = rank - base;
+    if (b >= r.B) return f;
+    int row0, len;
+    packed_range(r.cu, b, r.total, row0, len);
+    len = min(len, r.N);
+    const int whole = len / r.seg;
+    if (s < 0) {
+        if (whole > 0 && whole * r.seg == len) return f;
+        s = whole;
+    }
+    f.b = b;
+    f.s = s;
+    f.segs = (len + r.seg - 1) / r.seg;
+    f.seq_len = len;
+    f.row0 = row0;
+    f.first = s * r.seg;
+    f.len = min(r.seg, len - f.first);
+    return f;
+}
+
 // A sequence that is cut is walked in two launches.  The first gives the first
 // segment's outputs, whose state before is known, and the local states of the
 // segments between the first and the last; the second the other segments'
 // outputs.  So two segments cost no token twice.  Up to kFoldSerial segments
 // are folded by the second launch's warps themselves, each from the first to
-// its own, which costs less than a launch; more are folded in between.
+// its own, which costs less than a launch; more are folded in between.  The
+// blocks of a segment, which read the same rows, are next to one another.
 template <typename T, int NS, bool kFirst>
 __global__ void __launch_bounds__(kWarps * 32, NS >= 32 ? 3 : 4) selective_scan_kernel(const ScanArgs a, float* local,
-                                                                                       float* steps, bool folded) {
+                                                                                       float* steps, int blocks,
+                                                                                       bool folded) {
     __shared__ __align__(16) float shared[kWarps * Layout<NS>::FLOATS];
-    const Slot f = find_slot(a.rows, blockIdx.x);
+    const int rank = blockIdx.x / blocks, block = blockIdx.x - rank * blocks;
+    const Slot f = find_ranked(a.rows, rank);
     const bool last = f.s + 1 >= f.segs;
     if (f.b < 0 || (kFirst ? f.s > 0 && last : f.s == 0)) return;
-    const size_t state = (size_t)a.D * NS;
-    float* leave = !last ? local + blockIdx.x * state : a.h ? a.h + f.b * state : nullptr;
+    const size_t state = (size_t)a.D * NS, slot = slot_start(a.rows, f.b) + f.s;
+    float* leave = !last ? local + slot * state : a.h ? a.h + f.b * state : nullptr;
     if (!kFirst) {
         const int apart = folded ? 0 : f.s - 1;
-        const size_t from = blockIdx.x - 1 - apart;
-        walk<T, NS, true>(a, f, shared, local + from * state, apart, last ? leave : nullptr, steps + from * a.D);
+        const size_t from = slot - 1 - apart;
+        walk<T, NS, true>(a, f, block, shared, local + from * state, apart, last ? leave : nullptr, steps + from * a.D);
     } else if (f.s == 0) {
-        walk<T, NS, true>(a, f, shared, a.h0 ? a.h0 + f.b * state : nullptr, 0, leave, nullptr);
+        walk<T, NS, true>(a, f, block, shared, a.h0 ? a.h0 + f.b * state : nullptr, 0, leave, nullptr);
     } else {
-        walk<T, NS, false>(a, f, shared, nullptr, 0, leave, steps + (size_t)blockIdx.x * a.D);
+        walk<T, NS, false>(a, f, block, shared, nullptr, 0, leave, steps + slot * a.D);
     }
 }
 
@@ -377,16 +431,17 @@ template <typename T, int NS>
 cudaError_t scan(const ScanArgs& a, cudaStream_t s) {
     constexpr int W = Layout<NS>::W;
     const long long slots = slots_of(a.rows);
-    const dim3 grid((unsigned)slots, (a.D + kWarps * W - 1) / (kWarps * W));
+    const int blocks = (a.D + kWarps * W - 1) / (kWarps * W);
+    const unsigned grid = (unsigned)(slots * blocks);
     float* local = static_cast<float*>(a.workspace);
     float* steps = local + (size_t)slots * a.D * NS;
-    selective_scan_kernel<T, NS, true><<<grid, kWarps * 32, 0, s>>>(a, local, steps, false);
+    selective_scan_kernel<T, NS, true><<<grid, kWarps * 32, 0, s>>>(a, local, steps, blocks, false);
     if (a.rows.seg < a.rows.N) {
         const bool fold = (long long)kFoldSerial * a.rows.seg < a.rows.N;
         if (fold)
             fold_kernel<NS><<<dim3(a.rows.B, (a.D * (NS / 4) + kFoldX<8> - 1) / kFoldX<8>), dim3(kFoldX<8>, 8), 0, s>>>(
                 a, local, steps);
-        selective_scan_kernel<T, NS, false><<<grid, kWarps * 32, 0, s>>>(a, local, steps, fold);
+        selective_scan_kernel<T, NS, false><<<grid, kWarps * 32, 0, s>>>(a, local, steps, blocks, fold);
     }
     return cudaGetLastError();
 }
