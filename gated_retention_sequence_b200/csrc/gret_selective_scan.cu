@@ -240,21 +240,26 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, int block
 }
 
 // The rank-th segment of a packed batch in the order in which they are walked:
-// all whole segments first, then what is left of each sequence, so that the
-// launch does not end on long ones.  All 32 lanes call it together; it goes
-// over the offsets 32 at a time, and many sequences (over kRanked) take
-// find_slot's order.  38 sequences of 16384 tokens: SOMETHING.
-constexpr int kRanked = 256;
+// all whole segments first, then what is left of each sequence, the longest
+// first, so that the launch does not end on long ones.  All 32 lanes call it
+// together and go over the offsets 32 at a time.  More than kSorted sequences
+// leave their rests in the order of the batch, and more than kRanked take
+// find_slot's order, as the search itself would cost too much.  38 whole
+// sequences of 16384 tokens x 4096 channels: 412 us, 543 in the batch's order.
+constexpr int kRanked = 256, kSorted = 64;
 __device__ __forceinline__ Slot find_ranked(const Rows& r, int rank) {
     if (!r.cu || r.B > kRanked) return find_slot(r, rank);
     const int lane = threadIdx.x & 31;
+    auto tokens = [&](int b) {
+        int row0 = 0, len = 0;
+        if (b < r.B) packed_range(r.cu, b, r.total, row0, len);
+        return min(len, r.N);
+    };
     Slot f;
     f.b = -1; f.s = 0; f.segs = 0; f.first = 0; f.len = 0; f.seq_len = 0; f.row0 = 0;
     int b = -1, s = -1, base = 0;
     for (int b0 = 0; b0 < r.B; b0 += 32) {
-        int row0 = 0, len = 0;
-        if (b0 + lane < r.B) packed_range(r.cu, b0 + lane, r.total, row0, len);
-        const int whole = min(len, r.N) / r.seg;
+        const int whole = tokens(b0 + lane) / r.seg;
         int upto = whole;
 #pragma unroll
         for (int m = 1; m < 32; m *= 2) {
@@ -270,8 +275,31 @@ __device__ __forceinline__ Slot find_ranked(const Rows& r, int rank) {
         }
         base += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (b < 0) b = rank - base;
-    if (b >= r.B) return f;
+    if (b < 0) {
+        const int j = rank - base;
+        if (j >= r.B) return f;
+        b = j;
+        if (r.B <= kSorted) {
+            // the sequence that j others come before: those with more left, or as much and a lower number
+            constexpr int kEach = kSorted / 32;
+            int rest[kEach], before[kEach] = {};
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) rest[k] = lane + 32 * k < r.B ? tokens(lane + 32 * k) % r.seg : -1;
+#pragma unroll
+            for (int o = 0; o < kEach; ++o)
+                for (int l = 0; l < 32; ++l) {
+                    const int v = __shfl_sync(0xffffffffu, rest[o], l);
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k)
+                        before[k] += v > rest[k] || (v == rest[k] && l + 32 * o < lane + 32 * k);
+                }
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const unsigned hit = __ballot_sync(0xffffffffu, lane + 32 * k < r.B && before[k] == j);
+                if (hit) b = __ffs(hit) - 1 + 32 * k;
+            }
+        }
+    }
     int row0, len;
     packed_range(r.cu, b, r.total, row0, len);
     len = min(len, r.N);
@@ -343,25 +371,28 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs a, fl
 }
 
 // Tokens of a segment: N leaves the sequences whole.  Measured with 16 states,
-// a token costs a warp 88 ns when it has its scheduler to itself and 62 ns a
-// warp when two share it; many warps bring that to 53 ns.  A whole sequence
-// therefore costs its length times the former, and cut ones the latter over all
-// tokens, most of them twice.  For example, in us whole / cut: 1 x 4096 tokens
-// x 4096 channels 358 / 189, 2 x 1024 x 4096 94 / 100, 4 x 4096 x 4096 514 /
-// 594, 38 packed sequences of 16384 tokens x 4096 channels 620 / 560.  The
-// segment gives some 8192 warps, about four times what the GPU holds: fewer
-// leave it idle at the end, more cost staging.
+// a token costs a warp 88 ns when it has its scheduler to itself, 62 ns a warp
+// when two share it, and with many warps 53 ns; cut sequences pay the last for
+// most of their tokens twice.  Whole packed sequences, the longest first, take
+// a tenth more than that, or 127 ns for each token of the longest; in the order
+// of the batch the two may come one after the other.  For example, in us whole
+// / cut: 1 x 4096 tokens x 4096 channels 358 / 189, 2 x 1024 x 4096 94 / 100,
+// 4 x 4096 x 4096 514 / 594, 38 packed sequences of 16384 tokens, the longest
+// of 2470, x 4096 channels 412 / 493 and x 2048 channels 314 / 283.  The segment
+// gives some 4096 warps, about twice what the GPU holds: fewer leave it idle at
+// the end, more cost staging.
 int segment(int B, int N, int total, int D, int n, bool packed, int num_sms) {
     const int width = n == 8 ? 32 : n == 64 ? 8 : 16;
     const double warps = (D + width - 1) / width, tokens = packed ? (double)total : (double)B * N;
     const double schedulers = 4.0 * num_sms, filled = 53e-3 * tokens * warps / schedulers;
     const double shared = B * warps / schedulers;
-    const double whole = packed ? filled + 88e-3 * N : N * (shared <= 1 ? 88e-3 : 62e-3 * ceil(shared));
-    long long seg = (long long)ceil(tokens * warps / 8192 / kTile) * kTile;
+    const double whole = !packed ? N * (shared <= 1 ? 88e-3 : 62e-3 * ceil(shared))
+                         : B <= kSorted ? fmax(1.1 * filled, 127e-3 * N) : filled + 127e-3 * N;
+    long long seg = (long long)ceil(tokens * warps / 4096 / kTile) * kTile;
     if (seg < 4 * kTile) seg = 4 * kTile;
     if (seg >= N) return N;
-    const double again = packed ? 1.4 : 2.0 - (double)seg / N;
-    return whole <= 1.1 * again * filled + 10 ? N : (int)seg;
+    const double cut = (packed ? 1.45 : 1.1 * (2.0 - (double)seg / N)) * filled + 10;
+    return whole <= cut ? N : (int)seg;
 }
 
 // Four values next to one another.
