@@ -5,18 +5,18 @@
 // Rows from before a sequence's first token come from its tail (the last K-1
 // inputs of the piece before, or zero).  A thread owns four channels of one
 // slot (a segment of tokens) and keeps the last K-1 inputs in registers, so
-// that each input is read once, and K-1 more rows per slot.  Rows are loaded
-// kBatch at a time, a batch ahead: stores between the loads would otherwise
-// hold them up; whole batches take a path without a condition per row.
-// Measured at 16384 packed tokens x 4096 channels, bf16: 63 us (4.3 TB/s); with
-// eight channels a thread 104 us (188 registers), without loads ahead 73 us.
+// that each input is read once, and K-1 more rows per slot.  Rows are copied
+// kBatch at a time into shared memory, a batch ahead; whole batches take a path
+// without a condition per row.  Measured at 16384 packed tokens x 4096
+// channels, bf16: 58 us (4.7 TB/s); 63 us with the rows held in registers
+// instead, 73 us with none ahead, 104 us with eight channels a thread.
 #include "gret_block.cuh"
 
 namespace gret {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kSeg = 64, kBatch = 8, kC = 4, kP = kC / 2;
+constexpr int kSeg = 64, kBatch = 8, kAhead = 1, kC = 4, kP = kC / 2;
 
 // Four channels as they lie in memory.
 template <typename T> struct Four;
@@ -38,6 +38,16 @@ template <> struct Four<float> {
         v[1] = make_float2(a.z, a.w);
     }
 };
+// A row's four channels copied ahead into shared memory; the thread that copies
+// them is the one that reads them, so no barrier is needed.
+template <typename T>
+__device__ __forceinline__ void copy4(Four<T>* to, const T* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "n"((int)sizeof(T) * kC) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float2* v) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(v[0].x, v[0].y), b = __floats2bfloat162_rn(v[1].x, v[1].y);
     *reinterpret_cast<uint2*>(p) = make_uint2(reinterpret_cast<const uint32_t&>(a), reinterpret_cast<const uint32_t&>(b));
@@ -107,7 +117,8 @@ __device__ __forceinline__ void input_row(const ConvArgs& a, const Slot& f, int 
 template <bool B> struct Flag { static constexpr bool value = B; };
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) short_conv_kernel(const ConvArgs a) {
+    __shared__ __align__(16) Four<T> ring[kAhead + 1][kBatch][kThreads];
     const Slot f = find_slot(a.rows, blockIdx.x);
     const int c = (blockIdx.y * kThreads + threadIdx.x) * kC;
     if (f.b < 0 || c >= a.D) return;
@@ -118,20 +129,20 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const ConvArgs 
     for (int j = 0; j < K - 1; ++j) input_row<T, K>(a, f, f.first - (K - 1) + j, c, past[j]);
     const T* x = static_cast<const T*>(a.x) + (f.row0 + f.first) * a.ldx + c;
     T* y = static_cast<T*>(a.y) + (f.row0 + f.first) * (long long)a.D + c;
-    Four<T> next[kBatch];
-    auto fetch = [&](int left) {                            // x points at the batch's first row
+    auto fetch = [&](int left, int slot) {                  // x points at the batch's first row
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            if (k < left) next[k].load(x + k * a.ldx);
+            if (k < left) copy4(&ring[slot][k][threadIdx.x], x + k * a.ldx);
+        copies_end();
         x += kBatch * a.ldx;
     };
     // left: rows that remain; kWhole: a batch of them at least
-    auto walk = [&](const Four<T>* in, int left, auto whole) {
+    auto walk = [&](int slot, int left, auto whole) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             if (!decltype(whole)::value && k >= left) break;
             float2 now[kP], out[kP];
-            in[k].get(now);
+            ring[slot][k][threadIdx.x].get(now);
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 const float2 s = taps.sum(past, now[p], p);
@@ -142,16 +153,17 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const ConvArgs 
         }
         y += kBatch * (long long)a.D;
     };
-    fetch(f.len);
-    for (int left = f.len; left > 0; left -= kBatch) {
-        Four<T> in[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) in[k] = next[k];
-        fetch(left - kBatch);
+    for (int i = 0; i < kAhead; ++i) fetch(f.len - i * kBatch, i);
+    int slot = 0;
+    for (int left = f.len; left > 0; left -= kBatch) {
+        fetch(left - kAhead * kBatch, slot == 0 ? kAhead : slot - 1);
+        copies_wait<kAhead>();
         if (left >= kBatch)
-            walk(in, left, Flag<true>());
+            walk(slot, left, Flag<true>());
         else
-            walk(in, left, Flag<false>());
+            walk(slot, left, Flag<false>());
+        slot = slot == kAhead ? 0 : slot + 1;
     }
     if (a.tail && f.s == max(f.segs, 1) - 1) {
 #pragma unroll
@@ -194,24 +206,26 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const ConvArg
 //   dw[k]   = sum_t ds[t] x[t-K+1+k],  dbias = sum_t ds[t]
 // and dtail adds to the last K-1 rows.  A thread walks one slot and K-1 tokens
 // past its end; the slots of a block add up their dw and dbias in shared memory.
-// Issue slots bound it: 114 us at 16384 x 4096, bf16 (150 us with a condition
+// Issue slots bound it: 109 us at 16384 x 4096, bf16 (150 us with a condition
 // per row for the slot's ends).
-constexpr int kBackGroups = 32, kBackSlots = 4, kBackSeg = 128, kBackBatch = 4;
+constexpr int kBackGroups = 32, kBackSlots = 4, kBackSeg = 128, kBackBatch = 4, kBackAhead = 1;
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kBackGroups* kBackSlots, 3) short_conv_backward_kernel(const ConvBackwardArgs g,
+__global__ void __launch_bounds__(kBackGroups* kBackSlots, 4) short_conv_backward_kernel(const ConvBackwardArgs g,
                                                                                      float* partial, int slots) {
     __shared__ float red[kBackSlots][kBackGroups * kC + 1];
+    __shared__ __align__(16) Four<T> ring[kBackAhead + 1][2][kBackBatch][kBackGroups * kBackSlots];
+    const int tid = threadIdx.y * kBackGroups + threadIdx.x;
     const ConvArgs& a = g.f;
-    const int slot = blockIdx.x * kBackSlots + threadIdx.y;
+    const int item = blockIdx.x * kBackSlots + threadIdx.y;
     const int c = (blockIdx.y * kBackGroups + threadIdx.x) * kC;
     float2 dw[K + 1][kP];
 #pragma unroll
     for (int k = 0; k <= K; ++k)
 #pragma unroll
         for (int p = 0; p < kP; ++p) dw[k][p] = both(0.f);
-    if (slot < slots && c < a.D) {
-        const Slot f = find_slot(a.rows, slot);
+    if (item < slots && c < a.D) {
+        const Slot f = find_slot(a.rows, item);
         Taps<K> taps;
         taps.load(a.w, a.bias, c);
         float2 past[K - 1][kP], ds[K][kP];
@@ -226,32 +240,33 @@ __global__ void __launch_bounds__(kBackGroups* kBackSlots, 3) short_conv_backwar
         const T* x = static_cast<const T*>(a.x) + (f.row0 + f.first) * a.ldx + c;
         const T* dy = static_cast<const T*>(g.dy) + (f.row0 + f.first) * (long long)a.D + c;
         T* dx = static_cast<T*>(g.dx) + (f.row0 + f.first - (K - 1)) * (long long)a.D + c;
-        Four<T> in_next[kBackBatch], up_next[kBackBatch];
-        // x and dy point at row t0
-        auto fetch = [&](int t0) {
+        // x and dy point at row t0; no gradient comes from behind the last token
+        auto fetch = [&](int t0, int slot) {
             const int have = min(stop, f.seq_len) - t0;
 #pragma unroll
             for (int i = 0; i < kBackBatch; ++i) {
-                in_next[i].zero();
-                up_next[i].zero();                          // no gradient from behind the last token
                 if (i < have) {
-                    in_next[i].load(x + i * a.ldx);
-                    up_next[i].load(dy + i * (long long)a.D);
+                    copy4(&ring[slot][0][i][tid], x + i * a.ldx);
+                    copy4(&ring[slot][1][i][tid], dy + i * (long long)a.D);
+                } else {
+                    ring[slot][0][i][tid].zero();
+                    ring[slot][1][i][tid].zero();
                 }
             }
+            copies_end();
             x += kBackBatch * a.ldx;
             dy += kBackBatch * (long long)a.D;
         };
         // rows t0 .. of the batch; kInside: all of them the slot's own, and all rows of dx that they end too
-        auto walk = [&](int t0, const Four<T>* in, const Four<T>* up, auto inside) {
+        auto walk = [&](int t0, int slot, auto inside) {
             constexpr bool kInside = decltype(inside)::value;
 #pragma unroll
             for (int i = 0; i < kBackBatch; ++i) {
                 const int t = t0 + i;
                 if (!kInside && t >= stop) break;
                 float2 now[kP], d[kP];
-                in[i].get(now);
-                up[i].get(d);
+                ring[slot][0][i][tid].get(now);
+                ring[slot][1][i][tid].get(d);
 #pragma unroll
                 for (int p = 0; p < kP; ++p) {
                     const float2 s = taps.sum(past, now[p], p);
@@ -288,22 +303,19 @@ __global__ void __launch_bounds__(kBackGroups* kBackSlots, 3) short_conv_backwar
             }
             dx += kBackBatch * (long long)a.D;
         };
-        fetch(f.first);
-        for (int t0 = f.first; t0 < stop; t0 += kBackBatch) {
-            Four<T> in[kBackBatch], up[kBackBatch];
 #pragma unroll
-            for (int i = 0; i < kBackBatch; ++i) {
-                in[i] = in_next[i];
-                up[i] = up_next[i];
-            }
-            fetch(t0 + kBackBatch);
+        for (int i = 0; i < kBackAhead; ++i) fetch(f.first + i * kBackBatch, i);
+        int slot = 0;
+        for (int t0 = f.first; t0 < stop; t0 += kBackBatch) {
+            fetch(t0 + kBackAhead * kBackBatch, slot == 0 ? kBackAhead : slot - 1);
+            copies_wait<kBackAhead>();
             if (t0 >= f.first + K - 1 && t0 + kBackBatch <= end && t0 + kBackBatch - K < tail_at)
-                walk(t0, in, up, Flag<true>());
+                walk(t0, slot, Flag<true>());
             else
-                walk(t0, in, up, Flag<false>());
+                walk(t0, slot, Flag<false>());
+            slot = slot == kBackAhead ? 0 : slot + 1;
         }
     }
-    const int tid = threadIdx.y * kBackGroups + threadIdx.x;
     const int ch = blockIdx.y * kBackGroups * kC + tid;
 #pragma unroll
     for (int k = 0; k <= K; ++k) {
