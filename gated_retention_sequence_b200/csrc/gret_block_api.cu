@@ -30,10 +30,17 @@ bool stride_ok(long long ld, int width, gret_dtype t) {
     return ld >= width && ld <= (1LL << 40) && ld * (long long)size_of(t) % 16 == 0;
 }
 
-bool overlap(const void* p, const void* q, size_t bytes) {
+bool overlap(const void* p, size_t p_bytes, const void* q, size_t q_bytes) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return p && q && a < b + bytes && b < a + bytes;
+    return p && q && a < b + q_bytes && b < a + p_bytes;
 }
+bool overlap(const void* p, const void* q, size_t bytes) { return overlap(p, bytes, q, bytes); }
+
+// Bytes from a tensor's first row to the end of its last.
+size_t span(long long rows, long long ld, int width, gret_dtype t) {
+    return ((size_t)(rows - 1) * ld + width) * size_of(t);
+}
+long long rows_of(const Rows& r) { return r.cu ? (long long)r.total : (long long)r.B * r.N; }
 
 constexpr long long kMaxRows = 1LL << 31;
 constexpr int kMaxChannels = 1 << 16;       // channel blocks are a grid's second dimension
@@ -58,6 +65,8 @@ gret_status conv_check(const ConvArgs& a) {
     if (!all_aligned(a.x, a.w, a.bias, a.tail0, a.y, a.tail)) return GRET_ERR_INVALID_ARG;
     if (a.D % kVec != 0 || a.D > kMaxChannels || a.K < 2 || a.K > 4) return GRET_ERR_UNSUPPORTED;
     if (!stride_ok(a.ldx, a.D, a.io)) return GRET_ERR_INVALID_ARG;
+    const long long rows = rows_of(a.rows);
+    if (overlap(a.x, span(rows, a.ldx, a.D, a.io), a.y, span(rows, a.D, a.D, a.io))) return GRET_ERR_INVALID_ARG;
     return GRET_OK;
 }
 
@@ -81,8 +90,13 @@ gret_status scan_check(const ScanArgs& a) {
     if (!stride_ok(a.ldu, a.D, a.io) || !stride_ok(a.lddt, a.D, a.io) || !stride_ok(a.ldb, a.n, a.io) ||
         !stride_ok(a.ldc, a.n, a.io) || (a.z && !stride_ok(a.ldz, a.D, a.io)))
         return GRET_ERR_INVALID_ARG;
-    const long long rows = a.rows.cu ? (long long)a.rows.total : (long long)a.rows.B * a.rows.N;
+    const long long rows = rows_of(a.rows);
     if ((long long)a.rows.B * a.D * a.n > (1LL << 38) || rows * a.D > (1LL << 40)) return GRET_ERR_UNSUPPORTED;
+    const size_t out = span(rows, a.D, a.D, a.io);
+    if (overlap(a.u, span(rows, a.ldu, a.D, a.io), a.o, out) || overlap(a.dt, span(rows, a.lddt, a.D, a.io), a.o, out) ||
+        overlap(a.z, span(rows, a.ldz, a.D, a.io), a.o, out) || overlap(a.Bm, span(rows, a.ldb, a.n, a.io), a.o, out) ||
+        overlap(a.Cm, span(rows, a.ldc, a.n, a.io), a.o, out))
+        return GRET_ERR_INVALID_ARG;
     return GRET_OK;
 }
 
@@ -203,6 +217,14 @@ gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long
     const NormArgs a = {x, y, gate, ldx, ldy, ldg, scale, w_post, w_next, r, n, T, D, eps, stream_dtype, io_dtype};
     if (gret_status e = norm_check(a)) return e;
     if ((y && !r) || (w_next && !n)) return GRET_ERR_INVALID_ARG;
+    // r may be x itself; nothing else may meet
+    const size_t xs = span(T, ldx, D, stream_dtype), ys = span(T, ldy, D, io_dtype), gs = span(T, ldg, D, io_dtype);
+    const size_t rs = span(T, D, D, stream_dtype), ns = span(T, D, D, io_dtype);
+    if (!y) r = nullptr;
+    if (!w_next) n = nullptr;
+    if ((overlap(x, xs, r, rs) && !(r == x && ldx == D)) || overlap(y, ys, r, rs) || overlap(gate, gs, r, rs) ||
+        overlap(x, xs, n, ns) || overlap(y, ys, n, ns) || overlap(gate, gs, n, ns) || overlap(r, rs, n, ns))
+        return GRET_ERR_INVALID_ARG;
     int sms = 0;
     if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
     return done(launch_residual_norm(a, sms, cu_stream(stream)));

@@ -359,7 +359,7 @@ size_t gret_prefill_projected_workspace_size(int B, int H, int N, int dk, int dv
  * at b * N + n.  Outputs, states and parameters are contiguous.  Parameters,
  * states and sums are fp32.  Pointers must be 16-byte aligned; D is a multiple
  * of 8, at most 65536; all rows together number less than 2^31.  An output must
- * not alias an input except where it is said.  A call may be captured into a
+ * not overlap an input except where it is said (the forward calls refuse it).  A call may be captured into a
  * CUDA graph once one like it has run outside a capture.
  * ------------------------------------------------------------------------ */
 typedef enum { GRET_ACT_NONE = 0, GRET_ACT_SWISH = 1 } gret_activation;

@@ -5,7 +5,7 @@ import torch
 
 import gated_retention_sequence_b200 as gret
 
-P = 0x100000                       # an aligned address; validation fails before it is used
+P, Q, R = 0x100000, 0x10000000, 0x20000000      # aligned addresses apart; validation fails before they are used
 INVALID, UNSUPPORTED = gret.Status.ERR_INVALID_ARG, gret.Status.ERR_UNSUPPORTED
 BF = gret.Dtype.BF16
 
@@ -17,11 +17,11 @@ def lib():
     return gret.load()
 
 
-CONV = dict(x=P, ldx=64, w=P, bias=None, tail0=None, y=P, tail=None, B=2, N=5, D=64, K=4, io_dtype=BF,
+CONV = dict(x=P, ldx=64, w=P, bias=None, tail0=None, y=Q, tail=None, B=2, N=5, D=64, K=4, io_dtype=BF,
             act=gret.Activation.SWISH, stream=None)
 SCAN = dict(u=P, ldu=64, dt=P, lddt=64, A=P, Bm=P, ldb=16, Cm=P, ldc=16, skip=None, z=None, ldz=0, dt_bias=None, h0=None,
-            o=P, h_final=None, B=2, N=5, D=64, n=16, io_dtype=BF, workspace=None, workspace_bytes=0, stream=None)
-NORM = dict(x=P, ldx=64, y=P, ldy=64, gate=None, ldg=0, scale=None, w_post=None, w_next=P, r=P, n=P, T=3, D=64, eps=1e-5,
+            o=Q, h_final=None, B=2, N=5, D=64, n=16, io_dtype=BF, workspace=None, workspace_bytes=0, stream=None)
+NORM = dict(x=P, ldx=64, y=P, ldy=64, gate=None, ldg=0, scale=None, w_post=None, w_next=P, r=Q, n=R, T=3, D=64, eps=1e-5,
             stream_dtype=BF, io_dtype=BF, stream=None)
 
 ROWS_BAD = [(dict(B=0), INVALID), (dict(N=0), INVALID), (dict(N=-1), INVALID), (dict(B=1 << 16, N=1 << 16), UNSUPPORTED)]
@@ -32,17 +32,18 @@ ROWS_BAD = [(dict(B=0), INVALID), (dict(N=0), INVALID), (dict(N=-1), INVALID), (
     (dict(tail0=P + 8), INVALID), (dict(D=0), INVALID), (dict(io_dtype=7), INVALID), (dict(act=9), INVALID),
     (dict(ldx=63), INVALID), (dict(ldx=65), INVALID), (dict(ldx=-64), INVALID), (dict(D=60, ldx=64), UNSUPPORTED),
     (dict(K=1), UNSUPPORTED), (dict(K=5), UNSUPPORTED), (dict(K=0), INVALID),
-    (dict(tail0=P, tail=P), INVALID), (dict(tail0=P, tail=P + 2 * 3 * 64 * 2 - 16), INVALID)] + ROWS_BAD)
+    (dict(tail0=P, tail=P), INVALID), (dict(tail0=P, tail=P + 2 * 3 * 64 * 2 - 16), INVALID),
+    (dict(y=P), INVALID), (dict(ldx=128, y=P + (9 * 128 + 64) * 2 - 16), INVALID)] + ROWS_BAD)
 def test_conv_refuses(over, expect):
     assert gret.gret_short_conv(**dict(CONV, **over)) == expect
 
 
 def test_conv_step_and_varlen_refuse():
-    step = dict(x=P, ldx=64, w=P, bias=None, tail_in=P, tail_out=P, y=P, num_seqs=2, D=64, K=4, io_dtype=BF, act=1,
+    step = dict(x=P, ldx=64, w=P, bias=None, tail_in=P, tail_out=P, y=Q, num_seqs=2, D=64, K=4, io_dtype=BF, act=1,
                 stream=None)
     for over in (dict(tail_in=None), dict(tail_out=None), dict(num_seqs=0), dict(tail_out=P + 16)):
         assert gret.gret_short_conv_step(**dict(step, **over)) == INVALID, over
-    var = dict(x=P, ldx=64, w=P, bias=None, tail0=None, cu_seqlens=P, num_seqs=2, total_tokens=10, max_seqlen=6, y=P,
+    var = dict(x=P, ldx=64, w=P, bias=None, tail0=None, cu_seqlens=P, num_seqs=2, total_tokens=10, max_seqlen=6, y=Q,
                tail=None, D=64, K=4, io_dtype=BF, act=1, stream=None)
     for over in (dict(cu_seqlens=None), dict(cu_seqlens=P + 2), dict(num_seqs=0), dict(total_tokens=0),
                  dict(max_seqlen=0)):
@@ -53,6 +54,7 @@ def test_conv_step_and_varlen_refuse():
     (dict(u=None), INVALID), (dict(dt=None), INVALID), (dict(A=None), INVALID), (dict(Bm=None), INVALID),
     (dict(Cm=None), INVALID), (dict(o=None), INVALID), (dict(A=P + 4), INVALID), (dict(z=P + 2, ldz=64), INVALID),
     (dict(z=P, ldz=0), INVALID), (dict(ldb=8), INVALID), (dict(ldc=17), INVALID), (dict(lddt=32), INVALID),
+    (dict(o=P), INVALID), (dict(z=Q + 16, ldz=64), INVALID), (dict(Cm=Q + 10 * 64 * 2 - 16), INVALID),
     (dict(n=12), UNSUPPORTED), (dict(n=128), UNSUPPORTED), (dict(n=0), INVALID), (dict(D=60), UNSUPPORTED),
     (dict(D=65544, ldu=65544, lddt=65544), UNSUPPORTED), (dict(io_dtype=3), INVALID), (dict(h0=P, h_final=P), INVALID), (dict(h0=P, h_final=P + 2 * 64 * 16 * 4 - 16), INVALID),
     ] + ROWS_BAD)
@@ -76,7 +78,8 @@ def test_scan_step_and_varlen_refuse():
     (dict(x=None), INVALID), (dict(r=None), INVALID), (dict(n=None), INVALID), (dict(y=None, w_next=None), INVALID),
     (dict(y=None, gate=P, ldg=64), INVALID), (dict(y=None, scale=P), INVALID), (dict(eps=-1.0), INVALID),
     (dict(eps=float("nan")), INVALID), (dict(T=0), INVALID), (dict(D=0), INVALID), (dict(ldx=60), INVALID),
-    (dict(gate=P, ldg=0), INVALID), (dict(y=P + 4), INVALID), (dict(io_dtype=gret.Dtype.F32), INVALID),
+    (dict(gate=P, ldg=0), INVALID), (dict(n=Q), INVALID), (dict(n=P), INVALID), (dict(r=P + 16), INVALID),
+    (dict(x=Q, ldx=72), INVALID), (dict(y=Q), INVALID), (dict(gate=R + 128, ldg=64), INVALID), (dict(y=P + 4), INVALID), (dict(io_dtype=gret.Dtype.F32), INVALID),
     (dict(D=8200, ldx=8200, ldy=8200), UNSUPPORTED), (dict(D=60), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED)])
 def test_norm_refuses(over, expect):
     assert gret.gret_residual_norm(**dict(NORM, **over)) == expect
@@ -84,13 +87,13 @@ def test_norm_refuses(over, expect):
 
 def test_backwards_refuse():
     ws = dict(workspace=P, workspace_bytes=1 << 40)
-    conv = dict({k: v for k, v in CONV.items() if k not in ("y", "tail")}, dy=P, dtail=None, dx=P, dw=P, dbias=None,
+    conv = dict({k: v for k, v in CONV.items() if k not in ("y", "tail")}, dy=P, dtail=None, dx=Q, dw=P, dbias=None,
                 dtail0=None, **ws)
     for over in (dict(dy=None), dict(dx=None), dict(dw=P + 4), dict(dtail=P + 8), dict(workspace=None),
                  dict(workspace=P + 128), dict(workspace_bytes=0), dict(act=4), dict(N=0)):
         assert gret.gret_short_conv_backward(**dict(conv, **over)) == INVALID, over
     assert gret.gret_short_conv_backward(**dict(conv, K=7)) == UNSUPPORTED
-    scan = dict({k: v for k, v in SCAN.items() if k not in ("o", "h_final")}, dout=P, dh_final=None, du=P, ddt=P, dA=P,
+    scan = dict({k: v for k, v in SCAN.items() if k not in ("o", "h_final")}, dout=P, dh_final=None, du=Q, ddt=P, dA=P,
                 dBm=P, dCm=P, dskip=None, dz=None, ddt_bias=None, dh0=None, **ws)
     for over in (dict(dout=None), dict(du=None), dict(ddt=None), dict(dA=None), dict(dBm=None), dict(dCm=None),
                  dict(z=P, ldz=64), dict(dh0=P + 4), dict(workspace=None), dict(workspace_bytes=0), dict(B=0)):
