@@ -305,6 +305,7 @@ struct NormBackwardArgs {
     void *dx, *dy, *dgate;
     float *dscale, *dw_post, *dw_next;
     void* workspace;
+    unsigned int* status;       // device status word
 };
 constexpr int kNormMaxChannels = 8192;
 size_t residual_norm_backward_ws_bytes(long long T, int D, int num_sms);

@@ -299,7 +299,7 @@ gret_status gret_residual_norm_backward(const void* x, long long ldx, const void
         return GRET_ERR_INVALID_ARG;
     if (!all_aligned(dr, dn, dx, dy, dgate, dscale, dw_post, dw_next)) return GRET_ERR_INVALID_ARG;
     int sms = 148;
-    const bool device = device_info(nullptr, &sms);
+    const bool device = device_info(&g.status, &sms);
     if (!workspace_ok(workspace, workspace_bytes, residual_norm_backward_ws_bytes(T, D, sms))) return GRET_ERR_INVALID_ARG;
     if (!device) return GRET_ERR_CUDA;
     g.dr = dr; g.dn = dn; g.dx = dx; g.dy = dy; g.dgate = dgate;

@@ -12,8 +12,10 @@
 // written once, and the memory bandwidth bounds the time.  n is formed from r
 // before r is rounded to its storage type.
 #include "gret_block.cuh"
+#include "gret_sm100.cuh"
 
 namespace gret {
+using namespace sm100;
 namespace {
 
 // Copies of one thread's vectors of a row: `Parts` 16-byte pieces of each.
@@ -88,19 +90,12 @@ __device__ __forceinline__ void block_sums(float* v, float* red) {
     for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, sum, 4 * i);
 }
 
-// A vector as four pairs.
+// A vector as four pairs, from a row in shared or global memory.
 template <typename T>
-__device__ __forceinline__ void read_pairs(const uint4* from, float2* v) {
-    float x[kVec];
-    read_vector<T>(from, x);
-#pragma unroll
-    for (int i = 0; i < kVec / 2; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
-}
-__device__ __forceinline__ void load_pairs(const float* p, float2* v) {
-    float x[kVec];
-    load8(p, x);
-#pragma unroll
-    for (int i = 0; i < kVec / 2; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+__device__ __forceinline__ void load_pairs(const T* p, float2* v) {
+    Raw<T> r;
+    r.load(p);
+    pairs_of(r, v);
 }
 
 // A parameter's values for the thread's vectors, or 1.
@@ -220,26 +215,80 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const NormArgs a) {
 //   dx = dr + kr (t - rn mean(t rn)),  dscale = sum dx q swish(gate),  dw_next = sum dn rn
 //   dp = dx scale,  dgate = dp q swish'(gate),  dq = dp swish(gate),  dw_post = sum dq yn
 //   dy = ky (dq w_post - yn mean(dq w_post yn))
-// Rows as in the forward; a block keeps its share of the three parameter
-// gradients in registers and leaves it to the column sums.  The last mean is
-// sum(dx v) / D with v = r - x, and dx is linear in dr, t and r: its parts are
-// summed with r^2 and t r, and the next row's y^2 with them, so that a row
-// costs one barrier.  kFull: every part is given and the threads' vectors fill
-// the row, so that no part's absence cuts the code into pieces that loads
-// cannot cross.
+// A block walks rows as in the forward and keeps its share of the three
+// parameter gradients in registers, which it leaves to the column sums.  Its
+// rows come by bulk copies into kStages rows of shared memory, issued by one
+// thread: copies by every thread, as in the forward, took 328 us instead of
+// 254 at 16384 x 4096 beside an fp32 stream, as five inputs a row keep the load
+// and store unit busy.  The last mean is sum(dx v) / D with v = r - x, and
+// dx is linear in dr, t and r: its parts are summed with r^2 and t r, and the
+// next row's y^2 with them, so that a row costs one barrier; the same sums
+// carry the word that a wait gave up, and the block then returns together.
+// kFull: every part is given and the threads' vectors fill the row, so that no
+// part's absence cuts the code into pieces that loads cannot cross.
 template <typename TS, typename T, int V, int kStages, bool kFull>
 __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormBackwardArgs g, float* partial) {
-    extern __shared__ __align__(16) uint4 stage[];
+    extern __shared__ __align__(128) unsigned char rows[];
     __shared__ __align__(16) float red[2][128], first[2][32];
+    __shared__ __align__(8) unsigned long long full[kStages];
+    __shared__ volatile int gave_up;
     const NormArgs& a = g.f;
-    constexpr int kPer = 2 * kParts<TS> + 3 * kParts<T>, kP = kVec / 2;    // pieces of a vector: x, dr; y, gate, dn
+    constexpr int kP = kVec / 2;
     const int D = a.D;
     const bool has_y = kFull || a.y, has_gate = kFull || a.gate, has_next = kFull || a.w_next, has_dr = kFull || g.dr,
                has_post = kFull || a.w_post;
     const float2 one = both(1.f), none = both(0.f);
+    // a row in shared memory: x, dr; y, gate, dn
+    const uint32_t stream_bytes = D * (uint32_t)sizeof(TS), block_bytes = D * (uint32_t)sizeof(T);
+    const uint32_t row_bytes = 2 * stream_bytes + 3 * block_bytes;
+    struct Row {
+        const TS *x, *dr;
+        const T *y, *gate, *dn;
+    };
+    auto row_at = [&](int s) {
+        const unsigned char* p = rows + (size_t)s * row_bytes;
+        Row r;
+        r.x = reinterpret_cast<const TS*>(p);
+        r.dr = r.x + D;
+        r.y = reinterpret_cast<const T*>(r.dr + D);
+        r.gate = r.y + D;
+        r.dn = r.gate + D;
+        return r;
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        gave_up = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    // the block's i-th row into stage i mod kStages (one thread)
+    auto row_of = [&](long long i) { return blockIdx.x + i * gridDim.x; };
+    auto fetch = [&](long long i) {
+        const long long t = row_of(i);
+        if (threadIdx.x != 0 || t >= a.T) return;
+        const int s = (int)(i % kStages);
+        const uint32_t bar = smem_u32(&full[s]);
+        uint32_t to = smem_u32(rows) + s * row_bytes;
+        mbar_arrive_expect_tx(bar, stream_bytes * (has_dr ? 2 : 1) +
+                                       block_bytes * ((has_y ? 1 : 0) + (has_gate ? 1 : 0) + (has_next ? 1 : 0)));
+        bulk_load(to, static_cast<const TS*>(a.x) + t * a.ldx, stream_bytes, bar);
+        to += stream_bytes;
+        if (has_dr) bulk_load(to, static_cast<const TS*>(g.dr) + t * D, stream_bytes, bar);
+        to += stream_bytes;
+        if (has_y) bulk_load(to, static_cast<const T*>(a.y) + t * a.ldy, block_bytes, bar);
+        to += block_bytes;
+        if (has_gate) bulk_load(to, static_cast<const T*>(a.gate) + t * a.ldg, block_bytes, bar);
+        to += block_bytes;
+        if (has_next) bulk_load(to, static_cast<const T*>(g.dn) + t * D, block_bytes, bar);
+    };
+    auto arrived = [&](long long i) {
+        return row_of(i) >= a.T || mbar_wait(smem_u32(&full[i % kStages]), (uint32_t)(i / kStages) & 1u, g.status, &gave_up);
+    };
     // dscale, dw_post, dw_next; and the parameters, where a thread has one vector and registers for them
     constexpr bool kKeep = V == 1, kAhead = kStages >= 3;
     float2 acc[3][V][kP], kept[3][kP];
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
 #pragma unroll
@@ -254,57 +303,38 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
         for (int p = 0; p < kP; ++p) to[p] = kKeep ? kept[i][p] : one;
         if (!kKeep && w) load_pairs(w + c, to);
     };
-    auto fetch = [&](long long t, int s) {
-        if (t < a.T) {
-            uint4* to = stage + (size_t)s * kPer * V * blockDim.x + threadIdx.x;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (threadIdx.x + j * blockDim.x) * kVec;
-                if (kFull || c < D) {
-                    copy_vector(to, static_cast<const TS*>(a.x) + t * a.ldx + c);
-                    if (has_dr) copy_vector(to + kParts<TS> * blockDim.x, static_cast<const TS*>(g.dr) + t * D + c);
-                    uint4* rest = to + 2 * kParts<TS> * blockDim.x;
-                    if (has_y) copy_vector(rest, static_cast<const T*>(a.y) + t * a.ldy + c);
-                    if (has_gate) copy_vector(rest + kParts<T> * blockDim.x, static_cast<const T*>(a.gate) + t * a.ldg + c);
-                    if (has_next) copy_vector(rest + 2 * kParts<T> * blockDim.x, static_cast<const T*>(g.dn) + t * D + c);
-                }
-                to += kPer * blockDim.x;
-            }
-        }
-        copies_end();
-    };
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
     const float over = 1.0f / (float)D;
-    // sum of y^2 over the thread's share of the row in stage s
-    auto square = [&](int s) {
+    // sum of y^2 over the thread's share of a row
+    auto square = [&](const Row& row) {
         float2 sq = none;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            if (!kFull && (threadIdx.x + j * blockDim.x) * kVec >= D) continue;
+            const int c = (threadIdx.x + j * blockDim.x) * kVec;
+            if (!kFull && c >= D) continue;
             float2 y[kP];
-            read_pairs<T>(stage + (size_t)s * kPer * V * blockDim.x + threadIdx.x + (j * kPer + 2 * kParts<TS>)*blockDim.x, y);
+            load_pairs(row.y + c, y);
 #pragma unroll
             for (int p = 0; p < kP; ++p) sq = fma2(y[p], y[p], sq);
         }
         return sq.x + sq.y;
     };
-    int s = 0, turn = 0;
+    int turn = 0;
     float y2 = 0.f;                                         // sum of y^2 of the row
+    bool ok = true;
     if (kAhead && has_post) {
-        copies_wait<kStages - 2>();
-        y2 = square(0);
-        y2 = block_sum(y2, first[0]);
+        ok = arrived(0);
+        y2 = block_sum(square(row_at(0)), first[0]);
     }
-    for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
-        fetch(t + (long long)(kStages - 1) * gridDim.x, s == 0 ? kStages - 1 : s - 1);
-        copies_wait<kAhead ? kStages - 2 : kStages - 1>();
-        const uint4* row = stage + (size_t)s * kPer * V * blockDim.x + threadIdx.x;
-        const int after = s + 1 == kStages ? 0 : s + 1;
-        if (!kAhead && has_post) {
-            y2 = square(s);
-            y2 = block_sum(y2, first[turn]);
+    for (long long i = 0; row_of(i) < a.T; ++i) {
+        const long long t = row_of(i);
+        if (!kAhead) {
+            __syncthreads();                                // everyone is done with the row before
+            fetch(i + kStages - 1);
         }
+        ok = arrived(i) && ok;
+        if (kAhead) ok = arrived(i + 1) && ok;
+        const Row row = row_at((int)(i % kStages));
+        if (!kAhead && has_post) y2 = block_sum(square(row), first[turn]);
         const float ky = has_post ? rsqrtf(y2 * over + a.eps) : 1.f;
         float2 r[V][kP], yn[V][kP];
         // dr v, t v, r v, r^2, t r with v = r - x; and the next row's y^2
@@ -312,22 +342,20 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (threadIdx.x + j * blockDim.x) * kVec;
-            const uint4* from = row + j * kPer * blockDim.x;
 #pragma unroll
             for (int p = 0; p < kP; ++p) r[j][p] = yn[j][p] = none;
             if (!kFull && c >= D) continue;
-            read_pairs<TS>(from, r[j]);
+            load_pairs(row.x + c, r[j]);
             float2 v[kP], dr[kP], w[kP], dn[kP];
 #pragma unroll
             for (int p = 0; p < kP; ++p) v[p] = dr[p] = none;
-            if (has_dr) read_pairs<TS>(from + kParts<TS> * blockDim.x, dr);
-            from += 2 * kParts<TS> * blockDim.x;
+            if (has_dr) load_pairs(row.dr + c, dr);
             if (has_y) {
                 float2 gt[kP], sc[kP];
-                read_pairs<T>(from, yn[j]);
+                load_pairs(row.y + c, yn[j]);
                 weights(a.w_post, 1, c, w);
                 weights(a.scale, 0, c, sc);
-                if (has_gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
+                if (has_gate) load_pairs(row.gate + c, gt);
 #pragma unroll
                 for (int p = 0; p < kP; ++p) {
                     yn[j][p] = mul2(yn[j][p], both(ky));
@@ -339,7 +367,7 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
             }
             if (has_next) {
                 weights(a.w_next, 2, c, w);
-                read_pairs<T>(from + 2 * kParts<T> * blockDim.x, dn);
+                load_pairs(row.dn + c, dn);
 #pragma unroll
                 for (int p = 0; p < kP; ++p) {
                     const float2 tt = mul2(dn[p], w[p]);
@@ -352,9 +380,19 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
         }
         float all[8] = {};
 #pragma unroll
-        for (int i = 0; i < 5; ++i) all[i] = sum[i].x + sum[i].y;
-        all[5] = kAhead && has_post && t + gridDim.x < a.T ? square(after) : 0.f;
+        for (int k = 0; k < 5; ++k) all[k] = sum[k].x + sum[k].y;
+        all[5] = kAhead && has_post && row_of(i + 1) < a.T ? square(row_at((int)((i + 1) % kStages))) : 0.f;
+        all[6] = ok ? 0.f : 1.f;
         block_sums(all, red[turn]);
+        if (!(all[6] == 0.f)) {
+            // a copy did not arrive: let those issued land, as far as they do, and leave
+            if (threadIdx.x == 0)
+                for (long long k = i; k < i + (kAhead ? kStages - 1 : kStages); ++k)
+                    if (row_of(k) < a.T)
+                        mbar_wait_drain(smem_u32(&full[k % kStages]), (uint32_t)(k / kStages) & 1u, kWaitCycles);
+            return;
+        }
+        if (kAhead) fetch(i + kStages - 1);
         y2 = all[5];
         const float kr = has_next ? rsqrtf(all[3] * over + a.eps) : 0.f, m = all[4] * kr * over;
         // mean of (gradient of yn) yn: the total gradient of r is dr + kr (t - r kr m)
@@ -363,16 +401,14 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
         for (int j = 0; j < V; ++j) {
             const int c = (threadIdx.x + j * blockDim.x) * kVec;
             if (!kFull && c >= D) continue;
-            const uint4* from = row + j * kPer * blockDim.x;
             float2 dr[kP], w[kP];
 #pragma unroll
             for (int p = 0; p < kP; ++p) dr[p] = none;
-            if (has_dr) read_pairs<TS>(from + kParts<TS> * blockDim.x, dr);
-            from += 2 * kParts<TS> * blockDim.x;
+            if (has_dr) load_pairs(row.dr + c, dr);
             if (has_next) {
                 float2 dn[kP];
                 weights(a.w_next, 2, c, w);
-                read_pairs<T>(from + 2 * kParts<T> * blockDim.x, dn);
+                load_pairs(row.dn + c, dn);
 #pragma unroll
                 for (int p = 0; p < kP; ++p) {
                     const float2 rn = mul2(r[j][p], both(kr));
@@ -385,7 +421,7 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
             float2 gt[kP], sc[kP], dy[kP];
             weights(a.w_post, 1, c, w);
             weights(a.scale, 0, c, sc);
-            if (has_gate) read_pairs<T>(from + kParts<T> * blockDim.x, gt);
+            if (has_gate) load_pairs(row.gate + c, gt);
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 const float2 q = mul2(yn[j][p], w[p]);
@@ -400,7 +436,6 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
             store_pairs(static_cast<T*>(g.dy) + t * D + c, dy);
         }
         turn ^= 1;
-        s = after;
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i)
@@ -448,8 +483,8 @@ int backward_grid(long long T, int D, int num_sms) {
 template <typename TS, typename T, int V, int kStages>
 cudaError_t norm_backward(const NormBackwardArgs& g, int grid, cudaStream_t s) {
     const int threads = block_threads(g.f.D, V);
-    const int bytes = kStages * V * (2 * kParts<TS> + 3 * kParts<T>)*threads * 16;
     const NormArgs& a = g.f;
+    const int bytes = kStages * a.D * (int)(2 * sizeof(TS) + 3 * sizeof(T));
     const bool full = a.y && a.gate && a.scale && a.w_post && a.w_next && g.dr && threads * V * kVec == a.D;
     auto k = full ? residual_norm_backward_kernel<TS, T, V, kStages, true>
                   : residual_norm_backward_kernel<TS, T, V, kStages, false>;
@@ -464,15 +499,19 @@ cudaError_t norm_backward(const NormBackwardArgs& g, int grid, cudaStream_t s) {
     return launch_column_sums(partial, grid, out, s);
 }
 
-// Three rows in flight where they fit in shared memory.
+// As many rows in shared memory as fit for all blocks of an SM: 512 threads'
+// worth of rows take 14 bytes a channel beside an fp32 stream, so that four rows
+// fit one block (3 rows 299 us, 4 rows 254 us at 16384 x 4096) but not several.
 template <typename TS, typename T>
 cudaError_t norm_backward(const NormBackwardArgs& g, int grid, cudaStream_t s) {
-    if (backward_vectors(g.f.D) == 1) {
-        if constexpr (sizeof(T) == 2) return norm_backward<TS, T, 1, 3>(g, grid, s);
-        else return norm_backward<TS, T, 1, 2>(g, grid, s);
+    constexpr bool kWide = sizeof(TS) == 4, kAll = sizeof(T) == 4;
+    if (backward_vectors(g.f.D) == 2) return norm_backward<TS, T, 2, kAll ? 1 : 2>(g, grid, s);
+    if constexpr (kAll) {
+        return norm_backward<TS, T, 1, 2>(g, grid, s);
+    } else {
+        if (kWide && block_threads(g.f.D, 1) <= 256) return norm_backward<TS, T, 1, 3>(g, grid, s);
+        return norm_backward<TS, T, 1, kWide ? 4 : 5>(g, grid, s);
     }
-    if constexpr (sizeof(T) == 2) return norm_backward<TS, T, 2, 2>(g, grid, s);
-    else return norm_backward<TS, T, 2, 1>(g, grid, s);
 }
 
 }  // namespace

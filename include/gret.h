@@ -359,8 +359,9 @@ size_t gret_prefill_projected_workspace_size(int B, int H, int N, int dk, int dv
  * at b * N + n.  Outputs, states and parameters are contiguous.  Parameters,
  * states and sums are fp32.  Pointers must be 16-byte aligned; D is a multiple
  * of 8, at most 65536; all rows together number less than 2^31.  An output must
- * not overlap an input except where it is said (the forward calls refuse it).  A call may be captured into a
- * CUDA graph once one like it has run outside a capture.
+ * not overlap an input except where it is said (the forward calls refuse it).
+ * A call may be captured into a CUDA graph once one like it has run outside a
+ * capture.
  * ------------------------------------------------------------------------ */
 typedef enum { GRET_ACT_NONE = 0, GRET_ACT_SWISH = 1 } gret_activation;
 
@@ -488,7 +489,8 @@ gret_status gret_selective_scan_backward(const void* u, long long ldu, const voi
 /* gret_residual_norm_backward -- of <r, dr> + <n, dn>: dx in the stream dtype,
  * dy where y is given, dgate where gate is given, and where wanted dscale,
  * dw_post, dw_next [D].  dr (stream dtype) may be NULL (zero); dn goes with
- * w_next. */
+ * w_next.  A bounded device wait that gives up is reported by
+ * gret_last_device_status. */
 size_t gret_residual_norm_backward_workspace_size(long long T, int D);
 gret_status gret_residual_norm_backward(const void* x, long long ldx, const void* y, long long ldy, const void* gate,
                                         long long ldg, const float* scale, const float* w_post, const float* w_next,
