@@ -29,16 +29,8 @@ unsigned int* g_status_ptr[kMaxDevices] = {};
 int g_num_sms[kMaxDevices] = {};
 std::mutex g_mu;
 
-// prefill calls on the tensor-core path still to carry an injected timeout
+// calls with bounded waits still to carry an injected timeout
 std::atomic<int> g_inject_timeouts{0};
-
-// Take one pending injected timeout, if any.
-int take_injected_timeout() {
-    int n = g_inject_timeouts.load();
-    while (n > 0 && !g_inject_timeouts.compare_exchange_weak(n, n - 1)) {
-    }
-    return n > 0 ? 1 : 0;
-}
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -84,6 +76,14 @@ gret_path select_path(int B, int H, int N, int dk, int dv, int chunk, gret_dtype
 }
 
 }  // namespace
+
+// Take one pending injected timeout, if any.
+int take_injected_timeout() {
+    int n = g_inject_timeouts.load();
+    while (n > 0 && !g_inject_timeouts.compare_exchange_weak(n, n - 1)) {
+    }
+    return n > 0 ? 1 : 0;
+}
 
 // Device status word and SM count of the current device (looked up once per
 // device, with that device current).

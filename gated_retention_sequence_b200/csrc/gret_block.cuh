@@ -17,6 +17,8 @@ namespace gret {
 
 // Device status word and SM count of the current device.
 bool device_info(unsigned int** status, int* num_sms);
+// Take one injected timeout, if any is pending (gret_debug_inject_timeout).
+int take_injected_timeout();
 
 struct Rows {
     const int* cu;      // device offsets [B + 1], or null for a uniform batch
@@ -306,6 +308,7 @@ struct NormBackwardArgs {
     float *dscale, *dw_post, *dw_next;
     void* workspace;
     unsigned int* status;       // device status word
+    int fault;                  // test only: inject a timed-out wait
 };
 constexpr int kNormMaxChannels = 8192;
 size_t residual_norm_backward_ws_bytes(long long T, int D, int num_sms);

@@ -304,6 +304,7 @@ gret_status gret_residual_norm_backward(const void* x, long long ldx, const void
     if (!device) return GRET_ERR_CUDA;
     g.dr = dr; g.dn = dn; g.dx = dx; g.dy = dy; g.dgate = dgate;
     g.dscale = dscale; g.dw_post = dw_post; g.dw_next = dw_next; g.workspace = workspace;
+    g.fault = take_injected_timeout();
     return done(launch_residual_norm_backward(g, sms, cu_stream(stream)));
 }
 

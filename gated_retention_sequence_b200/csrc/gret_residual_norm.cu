@@ -230,7 +230,7 @@ template <typename TS, typename T, int V, int kStages, bool kFull>
 __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormBackwardArgs g, float* partial) {
     extern __shared__ __align__(128) unsigned char rows[];
     __shared__ __align__(16) float red[2][128], first[2][32];
-    __shared__ __align__(8) unsigned long long full[kStages];
+    __shared__ __align__(8) unsigned long long full[kStages], never;
     __shared__ volatile int gave_up;
     const NormArgs& a = g.f;
     constexpr int kP = kVec / 2;
@@ -257,8 +257,10 @@ __global__ void __launch_bounds__(512) residual_norm_backward_kernel(const NormB
     };
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        mbar_init(smem_u32(&never), 1);
         gave_up = 0;
         fence_mbar_init();
+        if (g.fault) mbar_wait_injected_timeout(smem_u32(&never), g.status, &gave_up);
     }
     __syncthreads();
     // the block's i-th row into stage i mod kStages (one thread)

@@ -501,7 +501,8 @@ gret_status gret_residual_norm_backward(const void* x, long long ldx, const void
 
 /* Test aid for the give-up path of the bounded device waits.  The next `calls`
  * prefill calls that run the tensor-core kernels (any gret_prefill* entry
- * point on that path, from any host thread) make the fused kernel's TMA warp,
+ * point on that path, from any host thread; gret_residual_norm_backward takes
+ * one too and gives up in the same way) make the fused kernel's TMA warp,
  * before it issues any load, wait on an mbarrier that nothing ever arrives at,
  * with a budget of about 2^20 cycles.  The wait runs out, the kernel records
  * GRET_ERR_TIMEOUT in the device status word, every role of the CTA stops

@@ -468,6 +468,28 @@ def test_norm_backward_left_out_and_strided(io, stream, without):
             bo.check(g[k], v, stream if k == "dx" else io if k in ("dy", "dgate") else "f32", k)
 
 
+@pytest.mark.parametrize("io,stream", KINDS)
+@pytest.mark.parametrize("D", [264, 4096, 8192])
+def test_norm_backward_gives_up(io, stream, D):
+    """A wait that runs out is reported once, the call returns, and the next call is right again."""
+    T = 300
+    p = dict(norm_inputs(io, stream, T, D), dr=draw(8, (T, D), stream), dn=draw(9, (T, D), io))
+    want = gret.residual_norm_backward(**p)
+    gret.check_device_status()
+    gret.gret_debug_inject_timeout(1)
+    try:
+        gret.residual_norm_backward(**p)
+        with pytest.raises(gret.GretError) as e:
+            gret.check_device_status()
+        assert e.value.status == gret.Status.ERR_TIMEOUT
+    finally:
+        gret.gret_debug_inject_timeout(0)
+    got = gret.residual_norm_backward(**p)
+    gret.check_device_status()
+    for k, v in want.items():
+        assert torch.equal(v, got[k]), k
+
+
 # --------------------------------------------------------------------- together
 def block_weights(D, n, R, K=4):
     g = lambda i, *s, std=1.0, mean=0.0: draw(20 + i, s, std=std, mean=mean)  # noqa: E731
