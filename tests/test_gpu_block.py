@@ -68,7 +68,7 @@ def test_conv_from_zero_without_bias_or_activation(io):
         bo.check(y[b], bo.short_conv(x[b], p["w"], swish=False)[0], io)
 
 
-LENS = [[1], [5, 0, 1, 33, 64, 2], [0, 0, 3], [300, 1, 0, 31], [2] * 70]
+LENS = [[1], [5, 0, 1, 33, 64, 2], [0, 0, 3], [300, 1, 0, 31], [2] * 70, [0, 1, 4] * 100]
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
@@ -164,6 +164,20 @@ def test_scan_prompts(io, n, B, N, D):
     for b in range(B):
         ro, rh = bo.selective_scan(**scan_rows(p, b * N, (b + 1) * N, b))
         bo.check(o[b], ro, io, f"o of sequence {b}")
+        bo.check(h[b], rh, "f32", f"h of sequence {b}")
+
+
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("N", [700, 1200])
+def test_scan_prompts_cut(n, N):
+    # few channels: the sequences are cut, into few segments and into many, and joined in their two ways
+    B, D = 3, 16
+    assert gret.gret_selective_scan_workspace_size(B, N, D, n, gret.Dtype.F32) > 0
+    p = scan_inputs("f32", B * N, D, n, B)
+    o, h = scan_call(p, B, N)
+    for b in range(B):
+        ro, rh = bo.selective_scan(**scan_rows(p, b * N, (b + 1) * N, b))
+        bo.check(o[b], ro, "f32", f"o of sequence {b}")
         bo.check(h[b], rh, "f32", f"h of sequence {b}")
 
 
