@@ -28,7 +28,42 @@ struct Layout {
     static constexpr int VR = W / kVec;                     // 16-byte vectors of a row
     static constexpr int V = (kTile * VR + 31) / 32;        // and of a lane
     static constexpr int BV = (kTile * NS / kVec + 31) / 32;    // vectors of B (of C) a lane stages
-    static constexpr int FLOATS = kTile * (LD + 2 * NS + LY);   // shared floats of a warp
+    static constexpr int FLOATS = kTile * (LD + 2 * NS + LY);   // shared floats of a warp, at most
+};
+
+// B and C of a tile in shared memory, in their own type, so that a lane's
+// states of both take as few bytes as they can: the shared memory's data path
+// is what the scan's warps load most.  A lane's states of B, four at a time,
+// are followed by the same of C.
+template <typename T> struct Words;
+template <> struct Words<__nv_bfloat16> {
+    static constexpr int kFour = 2;                         // 32-bit words of four states
+    static __device__ __forceinline__ void put(uint32_t* to, const Raw<__nv_bfloat16>& r) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(r.a.x, r.a.y);
+        *reinterpret_cast<uint2*>(to + 2 * kFour) = make_uint2(r.a.z, r.a.w);
+    }
+    // the first two pairs of B and C
+    static __device__ __forceinline__ void get(const uint32_t* from, float2* b, float2* c) {
+        const uint4 v = *reinterpret_cast<const uint4*>(from);
+        b[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+        b[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+        c[0] = make_float2(__uint_as_float(v.z << 16), __uint_as_float(v.z & 0xffff0000u));
+        c[1] = make_float2(__uint_as_float(v.w << 16), __uint_as_float(v.w & 0xffff0000u));
+    }
+};
+template <> struct Words<float> {
+    static constexpr int kFour = 4;
+    static __device__ __forceinline__ void put(uint32_t* to, const Raw<float>& r) {
+        *reinterpret_cast<float4*>(to) = r.a;
+        *reinterpret_cast<float4*>(to + 2 * kFour) = r.b;
+    }
+    static __device__ __forceinline__ void get(const uint32_t* from, float2* b, float2* c) {
+        const float4 x = reinterpret_cast<const float4*>(from)[0], y = reinterpret_cast<const float4*>(from)[1];
+        b[0] = make_float2(x.x, x.y);
+        b[1] = make_float2(x.z, x.w);
+        c[0] = make_float2(y.x, y.y);
+        c[1] = make_float2(y.z, y.w);
+    }
 };
 
 // A warp walks one slot's tokens for its channels.  Each tile of tokens is
@@ -47,8 +82,10 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, int block
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.D;
     const int d0 = (block * kWarps + warp) * W;
     if (d0 >= D) return;
-    // per token: (delta, delta, delta u, delta u) of each two channels; B; C; the sums over the states
-    float *sd = shared + warp * L::FLOATS, *sb = sd + kTile * LD, *sc = sb + kTile * NS, *sy = sc + kTile * NS;
+    // per token: (delta, delta, delta u, delta u) of each two channels; the sums over the states; B and C
+    constexpr int FOUR = Words<T>::kFour, LB = NS / 4 * 2 * FOUR;   // words of B and C for four states, and of a token
+    float *sd = shared + warp * L::FLOATS, *sy = sd + kTile * LD;
+    uint32_t* sbc = reinterpret_cast<uint32_t*>(sy + kTile * LY);
 
     const int q = lane % LPC, g = lane / LPC;               // states q SPL .., channels d0 + 2 g ..
     float2 A[kPair][H], h[kPair][H];                        // two states each
@@ -153,13 +190,9 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, int block
         for (int j = 0; j < BV; ++j) {
             const int r = br + j * BSTEP;
             if (r < kTile) {
-                float x[kVec];
-                nb[j].get(x);
-                store8(sb + r * NS + bc, x);
-                if (kFinal) {
-                    nc[j].get(x);
-                    store8(sc + r * NS + bc, x);
-                }
+                uint32_t* to = sbc + r * LB + bc / 4 * 2 * FOUR;
+                Words<T>::put(to, nb[j]);
+                if (kFinal) Words<T>::put(to + FOUR, nc[j]);
             }
         }
         __syncwarp();
@@ -173,16 +206,7 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, int block
                 const float dv[2] = {du.x, du.y}, uv[2] = {du.z, du.w};
                 float2 bs[H], cs[H], y[kPair];
 #pragma unroll
-                for (int i = 0; i < H; i += 2) {
-                    const float4 bv = *reinterpret_cast<const float4*>(sb + t * NS + q * SPL + 2 * i);
-                    bs[i] = make_float2(bv.x, bv.y);
-                    bs[i + 1] = make_float2(bv.z, bv.w);
-                    if (kFinal) {
-                        const float4 cv = *reinterpret_cast<const float4*>(sc + t * NS + q * SPL + 2 * i);
-                        cs[i] = make_float2(cv.x, cv.y);
-                        cs[i + 1] = make_float2(cv.z, cv.w);
-                    }
-                }
+                for (int i = 0; i < H; i += 2) Words<T>::get(sbc + t * LB + (q * SPL / 4 + i / 2) * 2 * FOUR, bs + i, cs + i);
 #pragma unroll
                 for (int c = 0; c < kPair; ++c) {
                     const float2 dd = both(dv[c]), uu = both(uv[c]);
