@@ -193,11 +193,9 @@ def _on(dev, stream):
     return _elsewhere(dev, stream)
 
 
-def _like(t, dtype=None):
-    """A dense tensor of t's shape (torch's quicker allocation where t is dense itself)."""
-    if t.is_contiguous():
-        return _g._torch().empty_like(t, dtype=dtype)
-    return t.new_empty(t.shape, dtype=dtype)
+def _like(t):
+    """A dense tensor of t's shape and type (torch's quicker allocation where t is dense itself)."""
+    return _g._torch().empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _raise_if(status, what):
@@ -455,20 +453,28 @@ def _norm_inputs(x, y, gate, scale, w_post, w_next, n=None):
     """Check the norm's inputs; returns (device, stream dtype, io dtype, T, D, row strides).  Without y an fp32 stream's n
     may be bf16: its given buffer says so."""
     torch = _g._torch()
-    dev, D = x.device, x.shape[-1]
-    if y is None and (gate is not None or scale is not None or w_post is not None):
-        raise ValueError("gate, scale and w_post go with y")
-    if y is None and w_next is None:
-        raise ValueError("y or w_next is required")
-    like = y if y is not None else n if n is not None else x
-    stream_dtype, io = _io_of(x), _io_of(like)
-    if io == Dtype.F32 and stream_dtype != Dtype.F32:
-        raise TypeError(f"x has dtype {x.dtype}, expected {like.dtype} or torch.float32")
-    ld = (_rows(x, "x", x.dtype, x.shape, dev),
-          _rows(y, "y", y.dtype, x.shape, dev) if y is not None else 0,
-          _rows(gate, "gate", like.dtype, x.shape, dev) if gate is not None else 0)
-    for t, name in ((scale, "scale"), (w_post, "w_post"), (w_next, "w_next")):
-        _opt(t, name, torch.float32, (D,), dev)
+    shape = x.shape
+    dev, D = x.device, shape[-1]
+    if y is None:
+        if gate is not None or scale is not None or w_post is not None:
+            raise ValueError("gate, scale and w_post go with y")
+        if w_next is None:
+            raise ValueError("y or w_next is required")
+        like = x if n is None else n
+    else:
+        like = y
+    stream_dtype = io = _io_of(x)
+    if like.dtype is not x.dtype:
+        io = _io_of(like)
+        if io == Dtype.F32:
+            raise TypeError(f"x has dtype {x.dtype}, expected {like.dtype} or torch.float32")
+    ld = (_rows(x, "x", x.dtype, shape, dev),
+          _rows(y, "y", y.dtype, shape, dev) if y is not None else 0,
+          _rows(gate, "gate", like.dtype, shape, dev) if gate is not None else 0)
+    par = (D,)
+    _opt(scale, "scale", torch.float32, par, dev)
+    _opt(w_post, "w_post", torch.float32, par, dev)
+    _opt(w_next, "w_next", torch.float32, par, dev)
     return dev, stream_dtype, io, x.numel() // D if D else 0, D, ld
 
 
@@ -492,7 +498,7 @@ def residual_norm(x, y=None, gate=None, scale=None, w_post=None, w_next=None, ep
         elif r is None:
             r = _like(x)
         if n is None and w_next is not None:
-            n = _like(x, io_torch)
+            n = _like(x) if x.dtype == io_torch else x.new_empty(x.shape, dtype=io_torch)
         _raise_if(_lib().gret_residual_norm(_ptr(x), ld[0], _ptr(y), ld[1], _ptr(gate), ld[2], _ptr(scale), _ptr(w_post),
                                      _ptr(w_next), _ptr(r) if y is not None else None, _ptr(n), T, D, float(eps), sd,
                                      io, st), "gret_residual_norm")
@@ -515,7 +521,7 @@ def residual_norm_backward(x, y=None, dr=None, dn=None, gate=None, scale=None, w
     _opt(dr, "dr", x.dtype, x.shape, dev)
     _opt(dn, "dn", io_torch, x.shape, dev)
     with _on(dev, stream) as st:
-        row = lambda t, dtype: None if t is None else _like(x, dtype)  # noqa: E731
+        row = lambda t, dtype: None if t is None else x.new_empty(x.shape, dtype=dtype)  # noqa: E731
         par = lambda w: None if w is None else torch.empty_like(w)  # noqa: E731
         g = {"dx": row(x, x.dtype), "dy": row(y, io_torch), "dgate": row(gate, io_torch), "dscale": par(scale),
              "dw_post": par(w_post), "dw_next": par(w_next)}
