@@ -5,7 +5,15 @@
 //   h[t,d,i]   = exp(delta[t,d] A[d,i]) h[t-1,d,i] + delta[t,d] u[t,d] B[t,i]
 //   o[t,d]     = (sum_i C[t,i] h[t,d,i] + skip[d] u[t,d]) swish(z[t,d])
 //
-// B and C are shared by all channels of a token.
+// B and C are shared by all channels of a token.  One exponential per token,
+// channel and state is all but unavoidable, as A is any matrix, and bounds the
+// time: at 16 a clock and SM they take 239 us for 16384 tokens x 4096 channels x
+// 16 states, whose bytes take 87.  38 packed sequences of that size take 398 us,
+// with the special function unit three quarters busy; evaluating a quarter of
+// the powers by a polynomial instead made it slower (379 -> 408 us at 64 x 256 x
+// 4096), as the instructions then bound it.  The shared memory's data path comes
+// next, hence two channels a lane that share their B and C, and those in their
+// own type.
 #include <math.h>
 
 #include "gret_selective.cuh"
@@ -269,7 +277,8 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, int block
 // together and go over the offsets 32 at a time.  More than kSorted sequences
 // leave their rests in the order of the batch, and more than kRanked take
 // find_slot's order, as the search itself would cost too much.  38 whole
-// sequences of 16384 tokens x 4096 channels: 412 us, 543 in the batch's order.
+// sequences of 16384 tokens x 4096 channels: 398 us (412 before B and C were
+// staged in their own type, and 543 in the batch's order then).
 constexpr int kRanked = 256, kSorted = 64;
 __device__ __forceinline__ Slot find_ranked(const Rows& r, int rank) {
     if (!r.cu || r.B > kRanked) return find_slot(r, rank);
