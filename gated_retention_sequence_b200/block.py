@@ -432,9 +432,8 @@ def selective_scan_backward(u, dt, A, B, C, do, skip=None, z=None, dt_bias=None,
     _opt(h0, "h0", torch.float32, (b, D, n), dev)
     _opt(dh_final, "dh_final", torch.float32, (b, D, n), dev)
     with _on(dev, stream) as st:
-        row = lambda w: u.new_empty((b, N, w))  # noqa: E731
-        g = {"du": row(D), "ddt": row(D), "dA": torch.empty_like(A), "dB": row(n), "dC": row(n),
-             "dz": None if z is None else row(D), "dskip": None if skip is None else torch.empty_like(skip),
+        g = {"du": _like(u), "ddt": _like(dt), "dA": torch.empty_like(A), "dB": _like(B), "dC": _like(C),
+             "dz": None if z is None else _like(z), "dskip": None if skip is None else torch.empty_like(skip),
              "ddt_bias": None if dt_bias is None else torch.empty_like(dt_bias),
              "dh0": torch.empty((b, D, n), dtype=torch.float32, device=dev) if h0 is not None or want_dh0 else None}
         need = gret_selective_scan_backward_workspace_size(b, N, D, n, io)
@@ -521,10 +520,10 @@ def residual_norm_backward(x, y=None, dr=None, dn=None, gate=None, scale=None, w
     _opt(dr, "dr", x.dtype, x.shape, dev)
     _opt(dn, "dn", io_torch, x.shape, dev)
     with _on(dev, stream) as st:
-        row = lambda t, dtype: None if t is None else x.new_empty(x.shape, dtype=dtype)  # noqa: E731
+        row = lambda t: None if t is None else _like(t)  # noqa: E731
         par = lambda w: None if w is None else torch.empty_like(w)  # noqa: E731
-        g = {"dx": row(x, x.dtype), "dy": row(y, io_torch), "dgate": row(gate, io_torch), "dscale": par(scale),
-             "dw_post": par(w_post), "dw_next": par(w_next)}
+        g = {"dx": _like(x), "dy": row(y), "dgate": row(gate), "dscale": par(scale), "dw_post": par(w_post),
+             "dw_next": par(w_next)}
         need = gret_residual_norm_backward_workspace_size(T, D)
         workspace = _workspace(workspace, need, dev)
         _raise_if(_lib().gret_residual_norm_backward(_ptr(x), ld[0], _ptr(y), ld[1], _ptr(gate), ld[2], _ptr(scale),

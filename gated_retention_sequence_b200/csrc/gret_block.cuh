@@ -236,6 +236,32 @@ struct ColumnOutputs {
 };
 cudaError_t launch_column_sums(const float* partial, int groups, const ColumnOutputs& out, cudaStream_t s);
 
+// A block's share of them: kSumCols columns, whose groups kSumThreads / kSumCols
+// lanes take in turn.  The order is fixed, so that the result does not depend on
+// which blocks ended first.
+constexpr int kSumCols = 32, kSumThreads = 256;
+inline long long column_blocks(const ColumnOutputs& out) { return (out.offset[out.count] + kSumCols - 1) / kSumCols; }
+__device__ __forceinline__ void column_sums(const float* partial, int groups, const ColumnOutputs& out, long long block) {
+    constexpr int kLanes = kSumThreads / kSumCols;
+    __shared__ float red[kLanes][kSumCols];
+    const int x = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
+    const long long c = block * kSumCols + x, cols = out.offset[out.count];
+    float s = 0.f;
+    if (c < cols) {
+#pragma unroll 4
+        for (int g = y; g < groups; g += kLanes) s += partial[g * cols + c];
+    }
+    red[y][x] = s;
+    __syncthreads();
+    if (y != 0 || c >= cols) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) s += red[i][x];
+    int j = 0;
+    while (j + 1 < out.count && c >= out.offset[j + 1]) ++j;
+    if (out.dst[j]) out.dst[j][(c - out.offset[j]) * out.stride[j]] = s;
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct ConvArgs {

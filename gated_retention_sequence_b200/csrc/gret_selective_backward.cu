@@ -18,11 +18,11 @@
 //            kGroup tokens in shared memory; then group by group from the last,
 //            the group's states and decays are formed again in registers and
 //            the group is walked in reverse
-//   join     dB, dC: the channel blocks' shares; column sums for the parameters
+//   join     dB, dC: the channel blocks' shares; the parameters' sums over the segments
 //
 // Three exponentials per state and token, all of them parallel over the tokens.
 // 4 x 4096 tokens x 2048 channels x 16 states, bf16: 965 us, of them ends 197,
-// fold 55, walk 662, join and column sums 40.  The walk issues 214 instructions
+// fold 55, walk 662, join 40.  The walk issues 214 instructions
 // per token and 16 channels (59 % of the issue slots, 67 % of the shared memory's
 // cycles); more blocks an SM, at 128 registers and 28 tokens a segment, took
 // 1063 us, and blocks of two, three or eight warps 1015 to 1155.
@@ -450,10 +450,14 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
     }
 }
 
-// dB, dC: the channel blocks' shares, added in order.
+// dB, dC: the channel blocks' shares, added in order, in the launch's first
+// `joins` blocks; the parameters' gradients, over the segments, in the others.
 template <typename T>
-__global__ void __launch_bounds__(256) join_kernel(const float* bc, int blocks, long long rows, int n, T* dB, T* dC) {
-    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4, all = rows * 2 * n;
+__global__ void __launch_bounds__(kSumThreads) join_kernel(const float* bc, int blocks, long long rows, int n, T* dB, T* dC,
+                                                           long long joins, const float* partial, int groups,
+                                                           ColumnOutputs out) {
+    if (blockIdx.x >= joins) return column_sums(partial, groups, out, blockIdx.x - joins);
+    const long long i = ((long long)blockIdx.x * kSumThreads + threadIdx.x) * 4, all = rows * 2 * n;
     if (i >= all) return;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -531,12 +535,11 @@ cudaError_t backward(ScanBackwardArgs g, cudaStream_t s) {
     else
         launch_fold<NS, 1>(g, w, segs, s);
     walk_kernel<T, NS><<<grid, kScanWarps * 32, walk_bytes, s>>>(g, w);
-    join_kernel<T><<<(unsigned)((rows * 2 * NS / 4 + 255) / 256), 256, 0, s>>>(w.bc, grid.y, rows, NS,
-                                                                              static_cast<T*>(g.dBm), static_cast<T*>(g.dCm));
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
     const ColumnOutputs out = {3, {0, D * NS, D * (NS + 1), D * (NS + 2)}, {g.dA, g.dskip, g.ddt_bias}, {1, 1, 1}};
-    return launch_column_sums(w.partial, (int)slots, out, s);
+    const long long joins = (rows * 2 * NS / 4 + kSumThreads - 1) / kSumThreads;
+    join_kernel<T><<<(unsigned)(joins + column_blocks(out)), kSumThreads, 0, s>>>(
+        w.bc, grid.y, rows, NS, static_cast<T*>(g.dBm), static_cast<T*>(g.dCm), joins, w.partial, (int)slots, out);
+    return cudaGetLastError();
 }
 
 }  // namespace

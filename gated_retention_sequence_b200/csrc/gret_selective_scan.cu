@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs a, fl
 // 4 x 4096 x 4096 514 / 594, 38 packed sequences of 16384 tokens, the longest
 // of 2470, x 4096 channels 412 / 493 and x 2048 channels 314 / 283.  The segment
 // gives some 4096 warps, about twice what the GPU holds: fewer leave it idle at
-// the end, more cost staging.
+// the end, more cost staging.  The second launch and its workspace count 16 us,
+// 10 on the GPU and as much again for the host that has to issue them.
 int segment(int B, int N, int total, int D, int n, bool packed, int num_sms) {
     const int width = n == 8 ? 32 : n == 64 ? 8 : 16;
     const double warps = (D + width - 1) / width, tokens = packed ? (double)total : (double)B * N;
@@ -424,7 +425,7 @@ int segment(int B, int N, int total, int D, int n, bool packed, int num_sms) {
     long long seg = (long long)ceil(tokens * warps / 4096 / kTile) * kTile;
     if (seg < 4 * kTile) seg = 4 * kTile;
     if (seg >= N) return N;
-    const double cut = (packed ? 1.45 : 1.1 * (2.0 - (double)seg / N)) * filled + 10;
+    const double cut = (packed ? 1.45 : 1.1 * (2.0 - (double)seg / N)) * filled + 16;
     return whole <= cut ? N : (int)seg;
 }
 
