@@ -20,6 +20,8 @@
 //            the group is walked in reverse
 //   join     dB, dC: the channel blocks' shares; the parameters' sums over the segments
 //
+// A sequence of one segment is walked alone, from h0 and dh_final.
+//
 // Three exponentials per state and token, all of them parallel over the tokens.
 // 4 x 4096 tokens x 2048 channels x 16 states, bf16: 965 us, of them ends 197,
 // fold 55, walk 662, join 40.  The walk issues 214 instructions
@@ -218,7 +220,8 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanBackwardAr
 }
 
 template <typename T, int NS>
-__global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel(const ScanBackwardArgs g, const Work w) {
+__global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel(const ScanBackwardArgs g, const Work w,
+                                                                                          bool alone) {
     using L = Layout<NS>;
     constexpr int SPL = L::SPL, H = SPL / 2, G = L::GROUP, LPC = L::LPC, W = L::W;
     extern __shared__ __align__(16) float shared[];
@@ -232,8 +235,9 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
     const size_t state = (size_t)blockIdx.x * D * NS;
     float2 A[kPair][H], dA[kPair][H], carry[kPair][H], first[kPair][H];
     load_states<SPL>(A, a.A, NS, q, d, D);
-    load_states<SPL>(first, w.h + state, NS, q, d, D);
-    load_states<SPL>(carry, w.g + state, NS, q, d, D);
+    const size_t whole = (size_t)f.b * D * NS;              // of the sequence, when it is one segment
+    load_states<SPL>(first, !alone ? w.h + state : a.h0 ? a.h0 + whole : nullptr, NS, q, d, D);
+    load_states<SPL>(carry, !alone ? w.g + state : g.dh_final ? g.dh_final + whole : nullptr, NS, q, d, D);
     {
         float total[kVec] = {};
         stage<T, NS>(g, f, d0, sd, sy, sbc, total);
@@ -374,6 +378,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
             }
         }
         __syncwarp();
+        if (alone && g.dh0) store_states<SPL>(g.dh0 + whole, carry, NS, q, d, D);
         float* partial = w.partial + (size_t)blockIdx.x * D * (NS + 2);
         store_states<SPL>(partial, dA, NS, q, d, D);
 
@@ -528,13 +533,15 @@ cudaError_t backward(ScanBackwardArgs g, cudaStream_t s) {
     if (err == cudaSuccess)
         err = cudaFuncSetAttribute(walk_kernel<T, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk_bytes);
     if (err != cudaSuccess) return err;
-    ends_kernel<T, NS><<<grid, kScanWarps * 32, ends_bytes, s>>>(g, w);
     const int segs = (int)(slots / a.rows.B);
-    if (segs > kFoldSerial)
-        launch_fold<NS, 8>(g, w, segs, s);
-    else
-        launch_fold<NS, 1>(g, w, segs, s);
-    walk_kernel<T, NS><<<grid, kScanWarps * 32, walk_bytes, s>>>(g, w);
+    if (segs > 1) {
+        ends_kernel<T, NS><<<grid, kScanWarps * 32, ends_bytes, s>>>(g, w);
+        if (segs > kFoldSerial)
+            launch_fold<NS, 8>(g, w, segs, s);
+        else
+            launch_fold<NS, 1>(g, w, segs, s);
+    }
+    walk_kernel<T, NS><<<grid, kScanWarps * 32, walk_bytes, s>>>(g, w, segs == 1);
     const ColumnOutputs out = {3, {0, D * NS, D * (NS + 1), D * (NS + 2)}, {g.dA, g.dskip, g.ddt_bias}, {1, 1, 1}};
     const long long joins = (rows * 2 * NS / 4 + kSumThreads - 1) / kSumThreads;
     join_kernel<T><<<(unsigned)(joins + column_blocks(out)), kSumThreads, 0, s>>>(
