@@ -116,14 +116,14 @@ def gret_residual_norm_backward(x, ldx, y, ldy, gate, ldg, scale, w_post, w_next
 # ---------------------------------------------------------------- helpers
 def _rows(t, name, dtype, shape, dev) -> int:
     """Check an activation and return its row stride."""
-    if t.is_cuda and t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
-        return shape[-1]
-    if not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}" if t.is_cuda else f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
+    if not (t.is_cuda and t.dtype is dtype and t.device == dev and t.shape == shape):
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}" if t.is_cuda else f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return shape[-1]
     # the dimensions with more than one entry lie `ld` rows apart, in order
     strides = t.stride()
     ld, rows = 0, 1
