@@ -236,27 +236,31 @@ struct ColumnOutputs {
 };
 cudaError_t launch_column_sums(const float* partial, int groups, const ColumnOutputs& out, cudaStream_t s);
 
-// A block's share of them: kSumCols columns, whose groups kSumThreads / kSumCols
-// lanes take in turn.  The order is fixed, so that the result does not depend on
-// which blocks ended first.
-constexpr int kSumCols = 32, kSumThreads = 256;
-inline long long column_blocks(const ColumnOutputs& out) { return (out.offset[out.count] + kSumCols - 1) / kSumCols; }
-__device__ __forceinline__ void column_sums(const float* partial, int groups, const ColumnOutputs& out, long long block) {
-    constexpr int kLanes = kSumThreads / kSumCols;
-    __shared__ float red[kLanes][kSumCols];
-    const int x = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
-    const long long c = block * kSumCols + x, cols = out.offset[out.count];
+// A block's share of them: `width` columns, whose groups kSumThreads / width
+// lanes take in turn; 32 columns, or 8 where these are few blocks with many
+// groups each (2368 groups of 216 columns: some 40 us with 32 columns a block,
+// 11 with 8).  The order is fixed, so that the result does not depend on which
+// blocks ended first.
+constexpr int kSumThreads = 256;
+inline int column_width(const ColumnOutputs& out, int groups) {
+    return groups >= 64 && out.offset[out.count] < 32 * 256 ? 8 : 32;
+}
+inline long long column_blocks(const ColumnOutputs& out, int width) { return (out.offset[out.count] + width - 1) / width; }
+__device__ __forceinline__ void column_sums(const float* partial, int groups, const ColumnOutputs& out, int width,
+                                            long long block) {
+    __shared__ float red[kSumThreads];
+    const int x = threadIdx.x % width, y = threadIdx.x / width, lanes = kSumThreads / width;
+    const long long c = block * width + x, cols = out.offset[out.count];
     float s = 0.f;
     if (c < cols) {
-#pragma unroll 4
-        for (int g = y; g < groups; g += kLanes) s += partial[g * cols + c];
+#pragma unroll 8
+        for (int g = y; g < groups; g += lanes) s += partial[g * cols + c];
     }
-    red[y][x] = s;
+    red[threadIdx.x] = s;
     __syncthreads();
     if (y != 0 || c >= cols) return;
     s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kLanes; ++i) s += red[i][x];
+    for (int i = 0; i < lanes; ++i) s += red[i * width + x];
     int j = 0;
     while (j + 1 < out.count && c >= out.offset[j + 1]) ++j;
     if (out.dst[j]) out.dst[j][(c - out.offset[j]) * out.stride[j]] = s;

@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads) join_kernel(const float* bc, int blocks, long long rows, int n, T* dB, T* dC,
                                                            long long joins, const float* partial, int groups,
-                                                           ColumnOutputs out) {
-    if (blockIdx.x >= joins) return column_sums(partial, groups, out, blockIdx.x - joins);
+                                                           ColumnOutputs out, int width) {
+    if (blockIdx.x >= joins) return column_sums(partial, groups, out, width, blockIdx.x - joins);
     const long long i = ((long long)blockIdx.x * kSumThreads + threadIdx.x) * 4, all = rows * 2 * n;
     if (i >= all) return;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -544,8 +544,9 @@ cudaError_t backward(ScanBackwardArgs g, cudaStream_t s) {
     walk_kernel<T, NS><<<grid, kScanWarps * 32, walk_bytes, s>>>(g, w, segs == 1);
     const ColumnOutputs out = {3, {0, D * NS, D * (NS + 1), D * (NS + 2)}, {g.dA, g.dskip, g.ddt_bias}, {1, 1, 1}};
     const long long joins = (rows * 2 * NS / 4 + kSumThreads - 1) / kSumThreads;
-    join_kernel<T><<<(unsigned)(joins + column_blocks(out)), kSumThreads, 0, s>>>(
-        w.bc, grid.y, rows, NS, static_cast<T*>(g.dBm), static_cast<T*>(g.dCm), joins, w.partial, (int)slots, out);
+    const int width = column_width(out, (int)slots);
+    join_kernel<T><<<(unsigned)(joins + column_blocks(out, width)), kSumThreads, 0, s>>>(
+        w.bc, grid.y, rows, NS, static_cast<T*>(g.dBm), static_cast<T*>(g.dCm), joins, w.partial, (int)slots, out, width);
     return cudaGetLastError();
 }
 

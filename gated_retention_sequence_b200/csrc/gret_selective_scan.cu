@@ -414,16 +414,20 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs a, fl
 // of 2470, x 4096 channels 412 / 493 and x 2048 channels 314 / 283.  The segment
 // gives some 4096 warps, about twice what the GPU holds: fewer leave it idle at
 // the end, more cost staging.  The second launch and its workspace count 16 us,
-// 10 on the GPU and as much again for the host that has to issue them.
+// 10 on the GPU and as much again for the host that has to issue them.  A lane of
+// 8 states takes twice as long a token, and half the tokens are then enough for a
+// segment.
 int segment(int B, int N, int total, int D, int n, bool packed, int num_sms) {
     const int width = n == 8 ? 32 : n == 64 ? 8 : 16;
     const double warps = (D + width - 1) / width, tokens = packed ? (double)total : (double)B * N;
-    const double schedulers = 4.0 * num_sms, filled = 53e-3 * tokens * warps / schedulers;
+    const double lane = n >= 32 ? 2 : 1;                    // states of a lane, in fours
+    const double schedulers = 4.0 * num_sms, filled = lane * 53e-3 * tokens * warps / schedulers;
     const double shared = B * warps / schedulers;
-    const double whole = !packed ? N * (shared <= 1 ? 88e-3 : 62e-3 * ceil(shared))
-                         : B <= kSorted ? fmax(1.1 * filled, 127e-3 * N) : filled + 127e-3 * N;
+    const double whole = !packed ? lane * N * (shared <= 1 ? 88e-3 : 62e-3 * ceil(shared))
+                         : B <= kSorted ? fmax(1.1 * filled, lane * 127e-3 * N) : filled + lane * 127e-3 * N;
     long long seg = (long long)ceil(tokens * warps / 4096 / kTile) * kTile;
-    if (seg < 4 * kTile) seg = 4 * kTile;
+    const int least = n >= 32 ? 2 * kTile : 4 * kTile;
+    if (seg < least) seg = least;
     if (seg >= N) return N;
     const double cut = (packed ? 1.45 : 1.1 * (2.0 - (double)seg / N)) * filled + 16;
     return whole <= cut ? N : (int)seg;
