@@ -415,8 +415,9 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs a, fl
 // gives some 4096 warps, about twice what the GPU holds: fewer leave it idle at
 // the end, more cost staging.  The second launch and its workspace count 16 us,
 // 10 on the GPU and as much again for the host that has to issue them.  A lane of
-// 8 states takes twice as long a token, and half the tokens are then enough for a
-// segment.
+// 8 states takes twice as long a token.  A segment has 64 tokens, or down to a
+// tile where all warps still fit the GPU at once (900 tokens x 256 channels x 16
+// states: 64, 32, 16 tokens a segment take 21, 15 and 13 us).
 int segment(int B, int N, int total, int D, int n, bool packed, int num_sms) {
     const int width = n == 8 ? 32 : n == 64 ? 8 : 16;
     const double warps = (D + width - 1) / width, tokens = packed ? (double)total : (double)B * N;
@@ -426,7 +427,8 @@ int segment(int B, int N, int total, int D, int n, bool packed, int num_sms) {
     const double whole = !packed ? lane * N * (shared <= 1 ? 88e-3 : 62e-3 * ceil(shared))
                          : B <= kSorted ? fmax(1.1 * filled, lane * 127e-3 * N) : filled + lane * 127e-3 * N;
     long long seg = (long long)ceil(tokens * warps / 4096 / kTile) * kTile;
-    const int least = n >= 32 ? 2 * kTile : 4 * kTile;
+    int least = 4 * kTile;
+    while (least > kTile && tokens * warps / (least / 2) <= 12.0 * num_sms) least /= 2;
     if (seg < least) seg = least;
     if (seg >= N) return N;
     const double cut = (packed ? 1.45 : 1.1 * (2.0 - (double)seg / N)) * filled + 16;
