@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
     const int d0 = blockIdx.y * L::W4 + warp * W;
     float *sbc = shared, *sd = shared + L::BC + warp * L::WARP, *sy = sd + L::SEG * L::LD, *starts = sd + L::ROWS;
     const long long row0 = f.row0 + f.first;
+    const int groups = (f.len + G - 1) / G;
     const int q = lane % LPC, cg = lane / LPC, d = d0 + cg * kPair;
     const size_t state = (size_t)blockIdx.x * D * NS;
     float2 A[kPair][H], dA[kPair][H], carry[kPair][H], first[kPair][H];
@@ -255,14 +256,14 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
         {
             float2 (&h)[kPair][H] = first;
 #pragma unroll 2
-            for (int k = 0; k < L::SEG / G; ++k) {
+            for (int k = 0; k < groups; ++k) {
                 float4* to = reinterpret_cast<float4*>(starts + k * L::START) + lane;
 #pragma unroll
                 for (int c = 0; c < kPair; ++c)
 #pragma unroll
                     for (int i = 0; i < H; i += 2)
                         to[(c * H + i) / 2 * 32] = make_float4(h[c][i].x, h[c][i].y, h[c][i + 1].x, h[c][i + 1].y);
-                if (k + 1 == L::SEG / G) break;
+                if (k + 1 == groups) break;
 #pragma unroll
                 for (int t = k * G; t < (k + 1) * G; ++t) {
                     const float4 du = *reinterpret_cast<const float4*>(sd + t * L::LD + cg * 4);
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
                 }
             }
         }
-        for (int k = L::SEG / G - 1; k >= 0; --k) {
+        for (int k = groups - 1; k >= 0; --k) {
             // the group's states and decays
             float2 h[G + 1][kPair][H], e[G][kPair][H];
             const float4* from = reinterpret_cast<const float4*>(starts + k * L::START) + lane;
