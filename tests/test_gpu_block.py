@@ -584,6 +584,37 @@ def test_block_step_in_a_graph_and_on_another_stream():
     torch.testing.assert_close(h, want_h, rtol=1e-4, atol=1e-4)
 
 
+def test_row_offsets_past_31_bits():
+    """Columns of a tensor of more than 2^31 entries give what dense copies give."""
+    T, D, n = 70000, 64, 16
+    wide = torch.empty(T, 32768, dtype=torch.bfloat16, device="cuda")
+    p, c, m = scan_inputs("bf16", T, D, n, 1), conv_inputs("bf16", T, D, 4, 1), norm_inputs("bf16", "bf16", T, D)
+
+    def far(t, at):
+        view = wide[:, at:at + t.shape[-1]]
+        view.copy_(t)
+        return view
+
+    q = {k: far(v, 1024 * (i + 1)) if k in ROWS else v for i, (k, v) in enumerate(p.items())}
+    do = draw(10, (1, T, D), "bf16")
+    cu = offsets([T - 9, 9])
+    p2, q2 = (dict(x, h0=torch.cat([x["h0"]] * 2)) for x in (p, q))
+    x = far(c["x"], 16384)
+    y = far(m["y"], 20480)
+    for a, b in ((scan_call(p, 1, T), scan_call(q, 1, T)),
+                 (gret.selective_scan_varlen(**p2, cu_seqlens=cu, max_seqlen=T),
+                  gret.selective_scan_varlen(**q2, cu_seqlens=cu, max_seqlen=T)),
+                 (scan_backward_call(p, do, 1, T).values(), scan_backward_call(q, do, 1, T).values()),
+                 (gret.short_conv(c["x"][None], c["w"]), gret.short_conv(x[None], c["w"])),
+                 (gret.short_conv_backward(c["x"][None], c["w"], None, do).values(),
+                  gret.short_conv_backward(x[None], c["w"], None, do).values()),
+                 (gret.residual_norm(**m), gret.residual_norm(**dict(m, y=y))),
+                 (gret.residual_norm_backward(**m, dr=do[0], dn=do[0]).values(),
+                  gret.residual_norm_backward(**dict(m, y=y), dr=do[0], dn=do[0]).values())):
+        for s, t in zip(a, b):
+            assert s is None and t is None or torch.equal(s, t)
+
+
 def test_calls_on_a_given_stream():
     side = torch.cuda.Stream()
     p = scan_inputs("bf16", 600, 264, 16, 1)
