@@ -23,8 +23,8 @@
 // A sequence of one segment is walked alone, from h0 and dh_final.
 //
 // Three exponentials per state and token, all of them parallel over the tokens.
-// 4 x 4096 tokens x 2048 channels x 16 states, bf16: 965 us, of them ends 197,
-// fold 55, walk 662, join 40.  The walk issues 214 instructions
+// 4 x 4096 tokens x 2048 channels x 16 states, bf16: 962 us, of them ends 200,
+// fold 55, walk 670, join 36.  The walk issues 217 instructions
 // per token and 16 channels (59 % of the issue slots, 67 % of the shared memory's
 // cycles); more blocks an SM, at 128 registers and 28 tokens a segment, took
 // 1063 us, and blocks of two, three or eight warps 1015 to 1155.
