@@ -153,6 +153,14 @@ __device__ __forceinline__ void pairs_of(const Raw<T>& r, float2* v) {
     for (int i = 0; i < kVec / 2; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
 }
 
+// Asynchronous copies into shared memory: the end of a group, and the wait until
+// at most N groups are under way.
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;

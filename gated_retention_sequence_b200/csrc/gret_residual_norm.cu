@@ -43,8 +43,6 @@ __device__ __forceinline__ void read_vector(const uint4* from, float* v) {
     }
     r.get(v);
 }
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // `red`: 32 words of shared memory; a caller takes others for the next two
 // sums, so that one barrier a sum is enough.
