@@ -124,23 +124,25 @@ def _rows(t, name, dtype, shape, dev) -> int:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
         return shape[-1]
-    # the dimensions with more than one entry lie `ld` rows apart, in order
+    # the dimensions with more than one entry lie `ld` rows apart, in order; one broadcast (a stride of 0) has no such rows
     strides = t.stride()
-    ld, rows = 0, 1
+    ld, rows = None, 1
     for i in range(len(shape) - 2, -1, -1):
         size = shape[i]
         if size != 1:
-            if not ld:
+            if ld is None:
                 ld = strides[i]
             elif strides[i] != rows * ld:
                 ld = -1
                 break
             rows *= size
-    if strides[-1] != 1 or (rows > 1 and ld < shape[-1]):
+    if ld is None:
+        ld = shape[-1]
+    if strides[-1] != 1 or ld < shape[-1]:
         raise ValueError(f"the rows of {name} must be dense and equally far apart (strides {strides})")
     if (ld * t.element_size()) % 16:
         raise ValueError(f"the rows of {name} must lie on 16-byte boundaries (row stride {ld})")
-    return ld or shape[-1]
+    return ld
 
 
 def _dense(t, name, dtype, shape, dev):

@@ -148,3 +148,69 @@ def test_row_strides():
                       (torch.zeros(4, 12, dtype=torch.bfloat16)[:, :8], "16-byte")):
         with pytest.raises(ValueError, match=what):
             ld(bad)
+
+
+@pytest.mark.parametrize("shape", [(6, 64), (4, 6, 64), (4, 3, 5, 64), (1, 6, 64), (4, 1, 64)])
+def test_broadcast_rows_are_refused(shape):
+    """A tensor broadcast along rows has fewer rows in memory than its shape says, wherever the dimension stands."""
+    from gated_retention_sequence_b200.block import _rows
+
+    class Cuda(torch.Tensor):
+        is_cuda = True
+
+    def ld(t):
+        t = t.as_subclass(Cuda)
+        return _rows(t, "x", t.dtype, t.shape, t.device)
+
+    outer = len(shape) - 1
+    for mask in range(1, 1 << outer):
+        small = [1 if mask >> i & 1 else shape[i] for i in range(outer)]
+        broadcast = tuple(small) != shape[:-1]
+        for t in (torch.zeros(*small, 64), torch.zeros(*small, 96)[..., 16:80], torch.zeros(*small, 5, 64)[..., 2, :]):
+            if broadcast:
+                with pytest.raises(ValueError, match="equally"):
+                    ld(t.expand(shape))
+        for i in range(outer):                  # cut from a tensor whose entries would otherwise be rows of their own
+            if mask >> i & 1 and shape[i] > 1:
+                with pytest.raises(ValueError, match="equally"):
+                    ld(torch.zeros(shape).narrow(i, 0, 1).expand(shape))
+    assert ld(torch.zeros(shape)) == 64
+
+
+def test_no_call_takes_broadcast_rows():
+    """Every activation of every call is checked."""
+    class Cuda(torch.Tensor):
+        is_cuda = True
+
+    def cuda(*s):
+        return torch.zeros(s).as_subclass(Cuda)
+
+    B, N, D, n = 2, 5, 64, 16
+    flat = cuda(B, 1, D).expand(B, N, D)
+    x, w, A = cuda(B, N, D), cuda(D, 4), cuda(D, n)
+    few, flatn = cuda(B, N, n), cuda(B, 1, n).expand(B, N, n)
+    scan = dict(u=x, dt=x, A=A, B=few, C=few, z=x)
+    for k, v in (("u", flat), ("dt", flat), ("B", flatn), ("C", flatn), ("z", flat)):
+        for call in (gret.selective_scan, lambda **q: gret.selective_scan_backward(do=x, **q)):
+            with pytest.raises(ValueError, match=f"rows of {k} must"):
+                call(**dict(scan, **{k: v}))
+    norm = dict(x=x, y=x, gate=x, w_next=cuda(D))
+    for k in ("x", "y", "gate"):
+        for call in (gret.residual_norm, lambda **q: gret.residual_norm_backward(dn=x, **q)):
+            with pytest.raises(ValueError, match=f"rows of {k} must"):
+                call(**dict(norm, **{k: flat}))
+    for call in (gret.short_conv, lambda x, w: gret.short_conv_backward(x, w, None, x)):
+        with pytest.raises(ValueError, match="rows of x must"):
+            call(flat, w)
+    flat, flatn = cuda(1, D).expand(N, D), cuda(1, n).expand(N, n)
+    cu = torch.zeros(3, dtype=torch.int32).as_subclass(Cuda)
+    h, tail, x, few = cuda(N, D, n), cuda(N, 3, D), cuda(N, D), cuda(N, n)
+    scan = dict(u=x, dt=x, A=A, B=few, C=few, z=x)
+    for k, v in (("u", flat), ("dt", flat), ("B", flatn), ("C", flatn), ("z", flat)):
+        for call in (lambda **q: gret.selective_scan_varlen(cu_seqlens=cu, max_seqlen=3, **q),
+                     lambda **q: gret.selective_step(h=h, **q)):
+            with pytest.raises(ValueError, match=f"rows of {k} must"):
+                call(**dict(scan, **{k: v}))
+    for call in (lambda: gret.short_conv_varlen(flat, w, None, cu, 3), lambda: gret.short_conv_step(flat, w, None, tail)):
+        with pytest.raises(ValueError, match="rows of x must"):
+            call()
