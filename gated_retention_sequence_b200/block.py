@@ -212,6 +212,8 @@ def _workspace(workspace, need, dev):
     if workspace is not None and workspace.numel() * workspace.element_size() >= need:
         if not workspace.is_cuda or workspace.device != dev:
             raise ValueError(f"the workspace is on {workspace.device}, expected {dev}")
+        if not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
         return workspace
     return _g._torch().empty(need, dtype=_g._torch().uint8, device=dev)
 

@@ -214,3 +214,17 @@ def test_no_call_takes_broadcast_rows():
     for call in (lambda: gret.short_conv_varlen(flat, w, None, cu, 3), lambda: gret.short_conv_step(flat, w, None, tail)):
         with pytest.raises(ValueError, match="rows of x must"):
             call()
+
+
+def test_workspace_must_be_contiguous():
+    """A broadcast or strided workspace has other bytes between its entries, or fewer than it counts."""
+    from gated_retention_sequence_b200.block import _workspace
+
+    class Cuda(torch.Tensor):
+        is_cuda = True
+
+    dense = torch.zeros(1024, dtype=torch.uint8).as_subclass(Cuda)
+    assert _workspace(dense, 1024, dense.device) is dense
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(1024), torch.zeros(2048, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            _workspace(bad.as_subclass(Cuda), 1024, dense.device)
