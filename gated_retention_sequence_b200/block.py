@@ -145,6 +145,18 @@ def _rows(t, name, dtype, shape, dev) -> int:
     return ld
 
 
+def _first(t) -> Dtype:
+    """The io dtype of a call's first activation, whose sizes have to fit the library's 31-bit counts."""
+    if t.numel() >> 31 and max(t.shape) >> 31:
+        raise GretError(_g.Status.ERR_UNSUPPORTED, f"sizes {tuple(t.shape)}")
+    return _io_of(t)
+
+
+def _longest(max_seqlen, T) -> int:
+    """The longest sequence of T packed rows, given an upper bound."""
+    return max(min(int(max_seqlen), T), 0)
+
+
 def _dense(t, name, dtype, shape, dev):
     """``_check``, quick where all is well."""
     if not (t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous() and t.is_cuda):
@@ -236,7 +248,7 @@ def short_conv(x, w, bias=None, tail0=None, activation: Optional[str] = "swish",
     tail0 [B,K-1,D], the last inputs of the piece before, or None.  Returns (y [B,N,D], tail [B,K-1,D] or None)."""
     torch = _g._torch()
     B, N, D = x.shape
-    dev, io = x.device, _io_of(x)
+    dev, io = x.device, _first(x)
     ldx = _rows(x, "x", x.dtype, x.shape, dev)
     K = _conv_weights(w, bias, D, dev)
     _opt(tail0, "tail0", x.dtype, (B, K - 1, D), dev)
@@ -261,8 +273,8 @@ def short_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, tail0=None, activ
     Returns (y [T,D], tail [S,K-1,D] or None)."""
     torch = _g._torch()
     T, D = x.shape
-    S = cu_seqlens.numel() - 1
-    dev, io = x.device, _io_of(x)
+    S, longest = cu_seqlens.numel() - 1, _longest(max_seqlen, T)
+    dev, io = x.device, _first(x)
     ldx = _rows(x, "x", x.dtype, x.shape, dev)
     K = _conv_weights(w, bias, D, dev)
     _dense(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev)
@@ -276,7 +288,7 @@ def short_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, tail0=None, activ
         if tail is None and want_tail:
             tail = x.new_empty((S, K - 1, D))
         _raise_if(_lib().gret_short_conv_varlen(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(tail0), _ptr(cu_seqlens), S, T,
-                                         int(max_seqlen), _ptr(y), _ptr(tail), D, K, io, act, st),
+                                         longest, _ptr(y), _ptr(tail), D, K, io, act, st),
                   "gret_short_conv_varlen")
     return y, tail
 
@@ -287,7 +299,7 @@ def short_conv_step(x, w, bias, tail, activation: Optional[str] = "swish", y=Non
     The new tail goes to ``tail_out``, or over ``tail`` where that is None.  Returns (y [S,D], the new tail)."""
     torch = _g._torch()
     S, D = x.shape
-    dev, io = x.device, _io_of(x)
+    dev, io = x.device, _first(x)
     ldx = _rows(x, "x", x.dtype, x.shape, dev)
     K = _conv_weights(w, bias, D, dev)
     _dense(tail, "tail", x.dtype, (S, K - 1, D), dev)
@@ -312,7 +324,7 @@ def short_conv_backward(x, w, bias, dy, tail0=None, dtail=None, activation: Opti
     dtail0 (x's dtype; None without a tail0)."""
     torch = _g._torch()
     B, N, D = x.shape
-    dev, io = x.device, _io_of(x)
+    dev, io = x.device, _first(x)
     ldx = _rows(x, "x", x.dtype, x.shape, dev)
     K = _conv_weights(w, bias, D, dev)
     _dense(dy, "dy", x.dtype, (B, N, D), dev)
@@ -339,7 +351,7 @@ def _scan_inputs(u, dt, A, B, C, skip, z, dt_bias):
     if A.dim() != 2:
         raise ValueError(f"A has shape {tuple(A.shape)}, expected ({D}, states)")
     n = A.shape[1]
-    io = _io_of(u)
+    io = _first(u)
     ld = (_rows(u, "u", u.dtype, u.shape, dev), _rows(dt, "dt", u.dtype, u.shape, dev),
           _rows(B, "B", u.dtype, rows + (n,), dev), _rows(C, "C", u.dtype, rows + (n,), dev),
           _rows(z, "z", u.dtype, u.shape, dev) if z is not None else 0)
@@ -382,7 +394,7 @@ def selective_scan_varlen(u, dt, A, B, C, cu_seqlens, max_seqlen: int, skip=None
     ``selective_scan``.  Returns (o [T,D], h_final [S,D,n] fp32 or None)."""
     torch = _g._torch()
     T, D = u.shape
-    S = cu_seqlens.numel() - 1
+    S, longest = cu_seqlens.numel() - 1, _longest(max_seqlen, T)
     dev, io, D, n, ld = _scan_inputs(u, dt, A, B, C, skip, z, dt_bias)
     _dense(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev)
     _opt(h0, "h0", torch.float32, (S, D, n), dev)
@@ -393,11 +405,11 @@ def selective_scan_varlen(u, dt, A, B, C, cu_seqlens, max_seqlen: int, skip=None
             o = _like(u)
         if h_final is None and want_state:
             h_final = torch.empty((S, D, n), dtype=torch.float32, device=dev)
-        need = gret_selective_scan_varlen_workspace_size(S, T, int(max_seqlen), D, n, io)
+        need = gret_selective_scan_varlen_workspace_size(S, T, longest, D, n, io)
         workspace = _workspace(workspace, need, dev)
         _raise_if(_lib().gret_selective_scan_varlen(_ptr(u), ld[0], _ptr(dt), ld[1], _ptr(A), _ptr(B), ld[2], _ptr(C), ld[3],
                                              _ptr(skip), _ptr(z), ld[4], _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), S,
-                                             T, int(max_seqlen), _ptr(o), _ptr(h_final), D, n, io, _ptr(workspace),
+                                             T, longest, _ptr(o), _ptr(h_final), D, n, io, _ptr(workspace),
                                              need, st), "gret_selective_scan_varlen")
     return o, h_final
 
@@ -466,7 +478,7 @@ def _norm_inputs(x, y, gate, scale, w_post, w_next, n=None):
         like = x if n is None else n
     else:
         like = y
-    stream_dtype = io = _io_of(x)
+    stream_dtype = io = _first(x)
     if like.dtype is not x.dtype:
         io = _io_of(like)
         if io == Dtype.F32:

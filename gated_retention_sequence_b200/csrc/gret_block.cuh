@@ -22,13 +22,15 @@ int take_injected_timeout();
 
 struct Rows {
     const int* cu;      // device offsets [B + 1], or null for a uniform batch
-    int B, N;           // sequences; tokens of each, or the longest
+    int B, N;           // sequences; tokens of each, or the longest (at most `total`)
     int total;          // rows of a packed batch
     int seg;            // tokens of a slot
 };
 
+// Segments of `len` tokens, without a sum that could pass 31 bits.
+__host__ __device__ __forceinline__ int segments_of(int len, int seg) { return len > 0 ? (len - 1) / seg + 1 : 0; }
 inline long long slots_of(const Rows& r) {
-    return r.cu ? (long long)r.total / r.seg + r.B : (long long)r.B * ((r.N + r.seg - 1) / r.seg);
+    return r.cu ? (long long)r.total / r.seg + r.B : (long long)r.B * segments_of(r.N, r.seg);
 }
 
 struct Slot {
@@ -42,7 +44,7 @@ struct Slot {
 };
 
 __device__ __forceinline__ long long slot_start(const Rows& r, int b) {
-    if (!r.cu) return (long long)b * ((r.N + r.seg - 1) / r.seg);
+    if (!r.cu) return (long long)b * segments_of(r.N, r.seg);
     int c = r.cu[b];
     c = c < 0 ? 0 : (c > r.total ? r.total : c);
     return (long long)(c / r.seg) + b;
@@ -56,7 +58,7 @@ __device__ __forceinline__ Slot find_slot(const Rows& r, int slot) {
     Slot f;
     f.b = -1; f.s = 0; f.segs = 0; f.first = 0; f.len = 0; f.seq_len = 0; f.row0 = 0;
     if (!r.cu) {
-        const int per = (r.N + r.seg - 1) / r.seg;
+        const int per = segments_of(r.N, r.seg);
         f.b = slot / per;
         f.s = slot - f.b * per;
         f.segs = per;
@@ -79,7 +81,7 @@ __device__ __forceinline__ Slot find_slot(const Rows& r, int slot) {
         packed_range(r.cu, lo, r.total, row0, len);
         len = min(len, r.N);
         f.s = (int)(slot - slot_start(r, lo));
-        f.segs = (len + r.seg - 1) / r.seg;
+        f.segs = segments_of(len, r.seg);
         if (f.s < 0 || f.s >= max(f.segs, 1)) return f;
         f.b = lo;
         f.seq_len = len;

@@ -42,16 +42,23 @@ size_t span(long long rows, long long ld, int width, gret_dtype t) {
 }
 long long rows_of(const Rows& r) { return r.cu ? (long long)r.total : (long long)r.B * r.N; }
 
-constexpr long long kMaxRows = 1LL << 31;
+constexpr long long kMaxRows = (1LL << 31) - (1 << 20);     // a walk may count a few rows past the end in 31 bits
 constexpr int kMaxChannels = 1 << 16;       // channel blocks are a grid's second dimension
 
-gret_status rows_ok(const Rows& r) {
-    if (r.B <= 0 || r.N <= 0 || (r.cu && r.total <= 0)) return GRET_ERR_INVALID_ARG;
+Rows uniform(int B, int N) { return Rows{nullptr, B, N, 0, 0}; }
+// No sequence of a packed batch is longer than all its rows.
+Rows packed(const int* cu, int num_seqs, int max_seqlen, int total) {
+    return Rows{cu, num_seqs, max_seqlen < total ? max_seqlen : total, total, 0};
+}
+
+gret_status rows_ok(const Rows& r, bool packed) {
+    if (r.B <= 0 || r.N <= 0 || (packed && r.total <= 0)) return GRET_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(r.cu) & 3u) != 0) return GRET_ERR_INVALID_ARG;
-    // rows, and slots of at least one token and one more a sequence, in 31 bits
-    if ((r.cu ? (long long)r.total + r.B : (long long)r.B * r.N) >= kMaxRows) return GRET_ERR_UNSUPPORTED;
+    // rows, and slots of at least one token and one more a sequence
+    if ((packed ? (long long)r.total + r.B : (long long)r.B * r.N) >= kMaxRows) return GRET_ERR_UNSUPPORTED;
     return GRET_OK;
 }
+gret_status rows_ok(const Rows& r) { return rows_ok(r, r.cu != nullptr); }
 
 gret_status done(cudaError_t e) { return e == cudaSuccess ? GRET_OK : GRET_ERR_CUDA; }
 
@@ -115,11 +122,11 @@ gret_status scan(ScanArgs a, size_t workspace_bytes, gret_stream_t stream) {
     return done(launch_selective_scan(a, sms, cu_stream(stream)));
 }
 
-size_t scan_workspace(int B, int N, int total, int D, int n, bool packed) {
-    if (B <= 0 || N <= 0 || (packed && total <= 0) || D <= 0 || D % kVec != 0 || !selective_states_supported(n)) return 0;
+size_t scan_workspace(const Rows& r, int D, int n, bool packed, gret_dtype io) {
+    if (!type_ok(io) || rows_ok(r, packed) || D <= 0 || D % kVec != 0 || !selective_states_supported(n)) return 0;
     int sms = 148;
     device_info(nullptr, &sms);
-    return selective_scan_ws_bytes(B, N, total, D, n, packed, sms);
+    return selective_scan_ws_bytes(r.B, r.N, r.total, D, n, packed, sms);
 }
 
 // ---------------------------------------------------------------- residual norm
@@ -143,7 +150,7 @@ extern "C" {
 gret_status gret_short_conv(const void* x, long long ldx, const float* w, const float* bias, const void* tail0,
                             void* y, void* tail, int B, int N, int D, int K, gret_dtype io_dtype, gret_activation act,
                             gret_stream_t stream) {
-    return conv(x, ldx, w, bias, tail0, y, tail, Rows{nullptr, B, N, 0, 0}, D, K, io_dtype, act, stream);
+    return conv(x, ldx, w, bias, tail0, y, tail, uniform(B, N), D, K, io_dtype, act, stream);
 }
 
 gret_status gret_short_conv_varlen(const void* x, long long ldx, const float* w, const float* bias, const void* tail0,
@@ -151,7 +158,7 @@ gret_status gret_short_conv_varlen(const void* x, long long ldx, const float* w,
                                    void* tail, int D, int K, gret_dtype io_dtype, gret_activation act,
                                    gret_stream_t stream) {
     if (!cu_seqlens) return GRET_ERR_INVALID_ARG;
-    return conv(x, ldx, w, bias, tail0, y, tail, Rows{cu_seqlens, num_seqs, max_seqlen, total_tokens, 0}, D, K,
+    return conv(x, ldx, w, bias, tail0, y, tail, packed(cu_seqlens, num_seqs, max_seqlen, total_tokens), D, K,
                 io_dtype, act, stream);
 }
 
@@ -159,7 +166,7 @@ gret_status gret_short_conv_step(const void* x, long long ldx, const float* w, c
                                  void* tail_out, void* y, int num_seqs, int D, int K, gret_dtype io_dtype,
                                  gret_activation act, gret_stream_t stream) {
     if (!all_set(tail_in, tail_out) || (act != GRET_ACT_NONE && act != GRET_ACT_SWISH)) return GRET_ERR_INVALID_ARG;
-    const ConvArgs a = {x, ldx, w, bias, tail_in, y, tail_out, Rows{nullptr, num_seqs, 1, 0, 0}, D, K,
+    const ConvArgs a = {x, ldx, w, bias, tail_in, y, tail_out, uniform(num_seqs, 1), D, K,
                         act == GRET_ACT_SWISH, io_dtype};
     if (gret_status e = conv_check(a)) return e;
     if (tail_in != tail_out && overlap(tail_in, tail_out, (size_t)num_seqs * (K - 1) * D * size_of(io_dtype)))
@@ -168,7 +175,7 @@ gret_status gret_short_conv_step(const void* x, long long ldx, const float* w, c
 }
 
 size_t gret_selective_scan_workspace_size(int B, int N, int D, int n, gret_dtype io_dtype) {
-    return type_ok(io_dtype) ? scan_workspace(B, N, 0, D, n, false) : 0;
+    return scan_workspace(uniform(B, N), D, n, false, io_dtype);
 }
 
 gret_status gret_selective_scan(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
@@ -177,13 +184,13 @@ gret_status gret_selective_scan(const void* u, long long ldu, const void* dt, lo
                                 float* h_final, int B, int N, int D, int n, gret_dtype io_dtype, void* workspace,
                                 size_t workspace_bytes, gret_stream_t stream) {
     return scan(ScanArgs{u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h0, o, h_final,
-                         Rows{nullptr, B, N, 0, 0}, D, n, io_dtype, workspace},
+                         uniform(B, N), D, n, io_dtype, workspace},
                 workspace_bytes, stream);
 }
 
 size_t gret_selective_scan_varlen_workspace_size(int num_seqs, int total_tokens, int max_seqlen, int D, int n,
                                                  gret_dtype io_dtype) {
-    return type_ok(io_dtype) ? scan_workspace(num_seqs, max_seqlen, total_tokens, D, n, true) : 0;
+    return scan_workspace(packed(nullptr, num_seqs, max_seqlen, total_tokens), D, n, true, io_dtype);
 }
 
 gret_status gret_selective_scan_varlen(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
@@ -194,7 +201,7 @@ gret_status gret_selective_scan_varlen(const void* u, long long ldu, const void*
                                        size_t workspace_bytes, gret_stream_t stream) {
     if (!cu_seqlens) return GRET_ERR_INVALID_ARG;
     return scan(ScanArgs{u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h0, o, h_final,
-                         Rows{cu_seqlens, num_seqs, max_seqlen, total_tokens, 0}, D, n, io_dtype, workspace},
+                         packed(cu_seqlens, num_seqs, max_seqlen, total_tokens), D, n, io_dtype, workspace},
                 workspace_bytes, stream);
 }
 
@@ -204,7 +211,7 @@ gret_status gret_selective_step(const void* u, long long ldu, const void* dt, lo
                                 void* o, int num_seqs, int D, int n, gret_dtype io_dtype, gret_stream_t stream) {
     if (!all_set(h_in, h_out)) return GRET_ERR_INVALID_ARG;
     const ScanArgs a = {u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h_in, o, h_out,
-                        Rows{nullptr, num_seqs, 1, 0, 0}, D, n, io_dtype, nullptr};
+                        uniform(num_seqs, 1), D, n, io_dtype, nullptr};
     if (gret_status e = scan_check(a)) return e;
     if (h_in != h_out && overlap(h_in, h_out, (size_t)num_seqs * D * n * sizeof(float))) return GRET_ERR_INVALID_ARG;
     return done(launch_selective_step(a, cu_stream(stream)));
@@ -231,7 +238,7 @@ gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long
 }
 
 size_t gret_short_conv_backward_workspace_size(int B, int N, int D, int K, gret_dtype io_dtype) {
-    if (rows_ok(Rows{nullptr, B, N, 0, 0}) || D <= 0 || D % kVec != 0 || K < 2 || K > 4 || !type_ok(io_dtype)) return 0;
+    if (rows_ok(uniform(B, N)) || D <= 0 || D % kVec != 0 || K < 2 || K > 4 || !type_ok(io_dtype)) return 0;
     return short_conv_backward_ws_bytes(B, N, D, K);
 }
 
@@ -243,7 +250,7 @@ gret_status gret_short_conv_backward(const void* x, long long ldx, const float* 
     if (act != GRET_ACT_NONE && act != GRET_ACT_SWISH) return GRET_ERR_INVALID_ARG;
     if (!all_set(dy, dx) || !all_aligned(dy, dtail, dx, dw, dbias, dtail0)) return GRET_ERR_INVALID_ARG;
     ConvBackwardArgs g = {};
-    g.f = ConvArgs{x, ldx, w, bias, tail0, dx, nullptr, Rows{nullptr, B, N, 0, 0}, D, K, act == GRET_ACT_SWISH, io_dtype};
+    g.f = ConvArgs{x, ldx, w, bias, tail0, dx, nullptr, uniform(B, N), D, K, act == GRET_ACT_SWISH, io_dtype};
     if (gret_status e = conv_check(g.f)) return e;
     if (!workspace_ok(workspace, workspace_bytes, short_conv_backward_ws_bytes(B, N, D, K))) return GRET_ERR_INVALID_ARG;
     g.dy = dy; g.dtail = dtail; g.dx = dx; g.dtail0 = dtail0; g.dw = dw; g.dbias = dbias; g.workspace = workspace;
@@ -251,7 +258,7 @@ gret_status gret_short_conv_backward(const void* x, long long ldx, const float* 
 }
 
 size_t gret_selective_scan_backward_workspace_size(int B, int N, int D, int n, gret_dtype io_dtype) {
-    if (rows_ok(Rows{nullptr, B, N, 0, 0}) || D <= 0 || D % kVec != 0 || !selective_states_supported(n) ||
+    if (rows_ok(uniform(B, N)) || D <= 0 || D % kVec != 0 || !selective_states_supported(n) ||
         !type_ok(io_dtype))
         return 0;
     return selective_backward_ws_bytes(B, N, D, n, io_dtype);
@@ -268,7 +275,7 @@ gret_status gret_selective_scan_backward(const void* u, long long ldu, const voi
     if (!all_aligned(dout, dh_final, du, ddt, dA, dBm, dCm, dskip, dz, ddt_bias, dh0)) return GRET_ERR_INVALID_ARG;
     ScanBackwardArgs g = {};
     g.f = ScanArgs{u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h0, du, nullptr,
-                   Rows{nullptr, B, N, 0, 0}, D, n, io_dtype, nullptr};
+                   uniform(B, N), D, n, io_dtype, nullptr};
     if (gret_status e = scan_check(g.f)) return e;
     if (!workspace_ok(workspace, workspace_bytes, selective_backward_ws_bytes(B, N, D, n, io_dtype)))
         return GRET_ERR_INVALID_ARG;

@@ -502,7 +502,7 @@ struct Parts {
 };
 Parts parts_of(int B, int N, int D, int n) {
     const Cut c = cut_of(n);
-    const size_t slots = (size_t)B * ((N + c.seg - 1) / c.seg), blocks = (D + c.channels - 1) / c.channels;
+    const size_t slots = (size_t)B * segments_of(N, c.seg), blocks = (D + c.channels - 1) / c.channels;
     Parts p;
     p.g = align256(slots * D * n * 4);
     p.steps = 2 * p.g;

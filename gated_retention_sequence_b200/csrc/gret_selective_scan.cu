@@ -343,7 +343,7 @@ __device__ __forceinline__ Slot find_ranked(const Rows& r, int rank) {
     }
     f.b = b;
     f.s = s;
-    f.segs = (len + r.seg - 1) / r.seg;
+    f.segs = segments_of(len, r.seg);
     f.seq_len = len;
     f.row0 = row0;
     f.first = s * r.seg;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs a, fl
         packed_range(a.rows.cu, b, a.rows.total, row0, len);
         len = min(len, a.rows.N);
     }
-    const int cuts = (len + a.rows.seg - 1) / a.rows.seg - 1;
+    const int cuts = segments_of(len, a.rows.seg) - 1;
     if (cuts <= 1) return;
     const long long slot = slot_start(a.rows, b), stride = (long long)a.D * NS;
     float* first = local + slot * stride + (size_t)d * NS + q;
@@ -532,7 +532,7 @@ bool selective_states_supported(int n) { return n == 8 || n == 16 || n == 32 || 
 size_t selective_scan_ws_bytes(int B, int N, int total, int D, int n, bool packed, int num_sms) {
     const int seg = segment(B, N, total, D, n, packed, num_sms);
     if (seg >= N) return 0;
-    const long long slots = packed ? (long long)total / seg + B : (long long)B * ((N + seg - 1) / seg);
+    const long long slots = packed ? (long long)total / seg + B : (long long)B * segments_of(N, seg);
     return align256((size_t)slots * D * (n + 1) * sizeof(float));
 }
 

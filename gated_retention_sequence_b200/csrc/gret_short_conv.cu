@@ -392,7 +392,7 @@ cudaError_t launch_short_conv_step(const ConvArgs& a, cudaStream_t s) {
 
 size_t short_conv_backward_ws_bytes(int B, int N, int D, int K) {
     const int seg = slot_tokens(kBackSeg, (long long)B * N, D);
-    const long long slots = (long long)B * ((N + seg - 1) / seg);
+    const long long slots = (long long)B * segments_of(N, seg);
     return align256((size_t)((slots + kBackSlots - 1) / kBackSlots) * (K + 1) * D * sizeof(float));
 }
 

@@ -358,7 +358,8 @@ size_t gret_prefill_projected_workspace_size(int B, int H, int N, int dk, int dv
  * wider projection are taken as they are; a uniform batch [B][N] has its rows
  * at b * N + n.  Outputs, states and parameters are contiguous.  Parameters,
  * states and sums are fp32.  Pointers must be 16-byte aligned; D is a multiple
- * of 8, at most 65536; all rows together number less than 2^31.  An output must
+ * of 8, at most 65536; all rows together, and one more for each packed sequence,
+ * number less than 2^31 - 2^20.  An output must
  * not overlap an input except where it is said (the forward calls refuse it).
  * A call may be captured into a CUDA graph once one like it has run outside a
  * capture.
@@ -382,8 +383,8 @@ gret_status gret_short_conv(const void* x, long long ldx, const float* w, const 
                             gret_stream_t stream);
 
 /* The same for a packed batch: x, y [total_tokens][D]; cu_seqlens, num_seqs,
- * max_seqlen and rows outside the sequences as in gret_prefill_varlen; tail0
- * and tail [num_seqs][K-1][D] (an empty sequence's tail is its tail0). */
+ * max_seqlen (any bound from above will do) and rows outside the sequences as in
+ * gret_prefill_varlen; tail0 and tail [num_seqs][K-1][D] (an empty sequence's tail is its tail0). */
 gret_status gret_short_conv_varlen(const void* x, long long ldx, const float* w, const float* bias, const void* tail0,
                                    const int* cu_seqlens, int num_seqs, int total_tokens, int max_seqlen, void* y,
                                    void* tail, int D, int K, gret_dtype io_dtype, gret_activation act,

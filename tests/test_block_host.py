@@ -228,3 +228,46 @@ def test_workspace_must_be_contiguous():
     for bad in (torch.zeros(1, dtype=torch.uint8).expand(1024), torch.zeros(2048, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError, match="contiguous"):
             _workspace(bad.as_subclass(Cuda), 1024, dense.device)
+
+
+MOST = 2 ** 31 - 2 ** 20                         # rows that no call takes
+
+
+def test_counts_next_to_31_bits():
+    """Row counts next to the limit neither wrap nor pass it."""
+    assert gret.gret_short_conv(**dict(CONV, B=1, N=MOST)) == UNSUPPORTED
+    assert gret.gret_selective_scan(**dict(SCAN, B=1, N=2 ** 31 - 1)) == UNSUPPORTED
+    back = {k: v for k, v in CONV.items() if k not in ("y", "tail")}
+    assert gret.gret_short_conv_backward(**dict(back, B=1, N=MOST, dy=P, dtail=None, dx=Q, dw=P, dbias=None, dtail0=None,
+                                                workspace=P, workspace_bytes=1 << 50)) == UNSUPPORTED
+    # the longest sequence that is taken: some 512 segments of 2^22 rows and a state of 17 words each
+    size = gret.gret_selective_scan_workspace_size(1, MOST - 1, 128, 16, BF)
+    assert 0 < size < 1024 * 128 * 17 * 4
+    assert 0 < gret.gret_selective_scan_varlen_workspace_size(1, MOST - 2, 2 ** 31 - 1, 128, 16, BF) < 1024 * 128 * 17 * 4
+    assert gret.gret_selective_scan_workspace_size(1, MOST, 128, 16, BF) == 0
+    assert gret.gret_selective_scan_varlen_workspace_size(2, MOST - 2, 5, 128, 16, BF) == 0
+
+
+def test_longest_sequence_is_a_bound_from_above():
+    """A bound past all rows says no more than the rows do."""
+    for T in (300, 5000):
+        want = gret.gret_selective_scan_varlen_workspace_size(4, T, T, 64, 16, BF)
+        for bound in (T + 1, 1 << 20, 2 ** 31 - 1):
+            assert gret.gret_selective_scan_varlen_workspace_size(4, T, bound, 64, 16, BF) == want
+
+
+def test_python_sizes_past_31_bits():
+    """Sizes that do not fit the library's counts are refused, not cut."""
+    class Cuda(torch.Tensor):
+        is_cuda = True
+
+    def cuda(*s, dtype=torch.bfloat16):
+        return torch.empty(s, dtype=dtype, device="meta").as_subclass(Cuda)
+
+    N = 2 ** 32 + 5
+    x, few, w, A = cuda(1, N, 8), cuda(1, N, 16), cuda(8, 4, dtype=torch.float32), cuda(8, 16, dtype=torch.float32)
+    for call in (lambda: gret.short_conv(x, w), lambda: gret.short_conv_backward(x, w, None, x),
+                 lambda: gret.selective_scan(x, x, A, few, few), lambda: gret.residual_norm(x, w_next=w[:, 0])):
+        with pytest.raises(gret.GretError) as e:
+            call()
+        assert e.value.status == UNSUPPORTED

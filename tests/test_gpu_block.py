@@ -673,3 +673,23 @@ def test_gradients_in_two_graphs_and_beside_one_another():
     torch.cuda.synchronize()
     for x, y in zip(again, outs[0]):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("bound", [2 ** 31 - 1, 2 ** 32 + 3])
+def test_packed_with_a_bound_past_all_rows(bound):
+    """The longest sequence may be given as any bound from above."""
+    lens, D, n = [300, 0, 5, 91], 24, 16
+    T = sum(lens) + 3
+    p, c, cu = scan_inputs("f32", T, D, n, len(lens)), conv_inputs("f32", T, D, 4, len(lens)), offsets(lens)
+    o, y = torch.full((T, D), 7.0, device="cuda"), torch.full((T, D), 7.0, device="cuda")
+    _, h = gret.selective_scan_varlen(**p, cu_seqlens=cu, max_seqlen=bound, o=o)
+    gret.short_conv_varlen(c["x"], c["w"], c["bias"], cu, bound, tail0=c["tail0"], y=y)
+    at = 0
+    for b, m in enumerate(lens):
+        if m:
+            ro, rh = bo.selective_scan(**scan_rows(p, at, at + m, b))
+            bo.check(o[at:at + m], ro, "f32", f"o of sequence {b}")
+            bo.check(h[b], rh, "f32", f"h of sequence {b}")
+            bo.check(y[at:at + m], bo.short_conv(c["x"][at:at + m], c["w"], c["bias"], c["tail0"][b])[0], "f32")
+        at += m
+    assert (o[at:] == 7).all() and (y[at:] == 7).all()
