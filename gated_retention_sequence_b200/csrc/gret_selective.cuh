@@ -47,6 +47,13 @@ __device__ __forceinline__ void store_states(float* to, const float2 (*v)[SPL / 
 // one thread for all of a state's segments.
 constexpr int kFoldU = 8, kFoldSerial = 16, kFoldThreads = 128;
 template <int Y> constexpr int kFoldX = kFoldThreads / Y;
+// Blocks of a sequence's fold.  A sequence has up to 65536 of them (65536
+// channels x 64 states), one more than a grid's second dimension takes, so that
+// a launch counts them all in its first.
+template <int Y>
+__host__ __device__ __forceinline__ int fold_blocks(int D, int n) {
+    return (D * (n / 4) + kFoldX<Y> - 1) / kFoldX<Y>;
+}
 template <int Y>
 struct FoldShared {
     float4 decay[Y][kFoldX<Y>], local[Y][kFoldX<Y>];

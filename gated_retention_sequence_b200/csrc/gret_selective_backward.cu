@@ -206,7 +206,8 @@ template <int NS, int Y>
 __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanBackwardArgs g, const Work w, int segs) {
     __shared__ FoldShared<Y> shared;
     const ScanArgs& a = g.f;
-    const int i = blockIdx.y * kFoldX<Y> + threadIdx.x, b = blockIdx.x;
+    const int blocks = fold_blocks<Y>(a.D, NS), b = blockIdx.x / blocks;
+    const int i = (blockIdx.x - b * blocks) * kFoldX<Y> + threadIdx.x;
     const bool on = i < a.D * (NS / 4);
     const int d = on ? i / (NS / 4) : 0, q = on ? i % (NS / 4) * 4 : 0;
     const long long stride = (long long)a.D * NS, first = (long long)b * segs, last = first + segs - 1;
@@ -514,8 +515,7 @@ Parts parts_of(int B, int N, int D, int n) {
 
 template <int NS, int Y>
 void launch_fold(const ScanBackwardArgs& g, const Work& w, int segs, cudaStream_t s) {
-    const dim3 grid(g.f.rows.B, (g.f.D * (NS / 4) + kFoldX<Y> - 1) / kFoldX<Y>);
-    fold_kernel<NS, Y><<<grid, dim3(kFoldX<Y>, Y), 0, s>>>(g, w, segs);
+    fold_kernel<NS, Y><<<g.f.rows.B * fold_blocks<Y>(g.f.D, NS), dim3(kFoldX<Y>, Y), 0, s>>>(g, w, segs);
 }
 
 template <typename T, int NS>

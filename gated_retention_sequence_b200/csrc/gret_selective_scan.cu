@@ -386,7 +386,8 @@ template <int NS>
 __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs a, float* local, const float* steps) {
     constexpr int Y = 8;
     __shared__ FoldShared<Y> shared;
-    const int i = blockIdx.y * kFoldX<Y> + threadIdx.x, b = blockIdx.x;
+    const int blocks = fold_blocks<Y>(a.D, NS), b = blockIdx.x / blocks;
+    const int i = (blockIdx.x - b * blocks) * kFoldX<Y> + threadIdx.x;
     const bool on = i < a.D * (NS / 4);
     const int d = on ? i / (NS / 4) : 0, q = on ? i % (NS / 4) * 4 : 0;
     int len = a.rows.N;
@@ -510,8 +511,7 @@ cudaError_t scan(const ScanArgs& a, cudaStream_t s) {
     if (a.rows.seg < a.rows.N) {
         const bool fold = (long long)kFoldSerial * a.rows.seg < a.rows.N;
         if (fold)
-            fold_kernel<NS><<<dim3(a.rows.B, (a.D * (NS / 4) + kFoldX<8> - 1) / kFoldX<8>), dim3(kFoldX<8>, 8), 0, s>>>(
-                a, local, steps);
+            fold_kernel<NS><<<a.rows.B * fold_blocks<8>(a.D, NS), dim3(kFoldX<8>, 8), 0, s>>>(a, local, steps);
         selective_scan_kernel<T, NS, false><<<grid, kWarps * 32, 0, s>>>(a, local, steps, blocks, fold);
     }
     return cudaGetLastError();

@@ -693,3 +693,18 @@ def test_packed_with_a_bound_past_all_rows(bound):
             bo.check(y[at:at + m], bo.short_conv(c["x"][at:at + m], c["w"], c["bias"], c["tail0"][b])[0], "f32")
         at += m
     assert (o[at:] == 7).all() and (y[at:] == 7).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_scan_backward_of_the_most_channels(io):
+    """65536 channels x 64 states with more segments than a thread folds.  Only a few channels have a gradient: the
+    others add nothing to dB and dC, so that the few make up all of both."""
+    N, D, n = 300, 65536, 64
+    keep = [0, 1, 31, 4096, 33333, 65528, 65535]
+    p = scan_inputs(io, N, D, n, 1)
+    do, dh = torch.zeros((1, N, D), dtype=TYPES[io], device="cuda"), torch.zeros(1, D, n, device="cuda")
+    do[..., keep], dh[:, keep] = draw(10, (1, N, len(keep)), io), draw(11, (1, len(keep), n))
+    g = scan_backward_call(p, do, 1, N, dh_final=dh)
+    few = {k: v if k in ("B", "C") else v[:, keep] if k in ROWS + ("h0",) else v[keep] for k, v in p.items()}
+    g = {k: v if k in ("dB", "dC") else v[..., keep, :] if k in ("dA", "dh0") else v[..., keep] for k, v in g.items()}
+    check_scan_backward(io, few, do[..., keep], dh[:, keep], g, 1, N)
