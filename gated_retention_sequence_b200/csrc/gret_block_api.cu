@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "gret_block.cuh"
 
 using namespace gret;
@@ -30,16 +32,32 @@ bool stride_ok(long long ld, int width, gret_dtype t) {
     return ld >= width && ld <= (1LL << 40) && ld * (long long)size_of(t) % 16 == 0;
 }
 
-bool overlap(const void* p, size_t p_bytes, const void* q, size_t q_bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return p && q && a < b + q_bytes && b < a + p_bytes;
+// What a pointer names: `bytes` from p on (nothing where p is null).
+struct Region {
+    const void* p;
+    size_t bytes;
+};
+bool overlap(const Region& x, const Region& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return x.p && y.p && a < b + y.bytes && b < a + x.bytes;
 }
-bool overlap(const void* p, const void* q, size_t bytes) { return overlap(p, bytes, q, bytes); }
+// No output meets an input or another output.
+bool apart(std::initializer_list<Region> outputs, std::initializer_list<Region> inputs) {
+    for (const Region* o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Region& i : inputs)
+            if (overlap(*o, i)) return false;
+        for (const Region* p = outputs.begin(); p != o; ++p)
+            if (overlap(*o, *p)) return false;
+    }
+    return true;
+}
 
 // Bytes from a tensor's first row to the end of its last.
 size_t span(long long rows, long long ld, int width, gret_dtype t) {
     return ((size_t)(rows - 1) * ld + width) * size_of(t);
 }
+size_t floats(long long a, long long b = 1, long long c = 1) { return (size_t)a * b * c * sizeof(float); }
+Region offsets(const Rows& r) { return {r.cu, ((size_t)r.B + 1) * sizeof(int)}; }
 long long rows_of(const Rows& r) { return r.cu ? (long long)r.total : (long long)r.B * r.N; }
 
 constexpr long long kMaxRows = (1LL << 31) - (1 << 20);     // a walk may count a few rows past the end in 31 bits
@@ -72,9 +90,17 @@ gret_status conv_check(const ConvArgs& a) {
     if (!all_aligned(a.x, a.w, a.bias, a.tail0, a.y, a.tail)) return GRET_ERR_INVALID_ARG;
     if (a.D % kVec != 0 || a.D > kMaxChannels || a.K < 2 || a.K > 4) return GRET_ERR_UNSUPPORTED;
     if (!stride_ok(a.ldx, a.D, a.io)) return GRET_ERR_INVALID_ARG;
-    const long long rows = rows_of(a.rows);
-    if (overlap(a.x, span(rows, a.ldx, a.D, a.io), a.y, span(rows, a.D, a.D, a.io))) return GRET_ERR_INVALID_ARG;
     return GRET_OK;
+}
+
+// What a convolution's arguments name, and whether its outputs are apart from what it reads.
+Region conv_rows(const ConvArgs& a, const void* p, long long ld) { return {p, span(rows_of(a.rows), ld, a.D, a.io)}; }
+Region conv_tail(const ConvArgs& a, const void* p) {
+    return {p, (size_t)a.rows.B * (a.K - 1) * a.D * size_of(a.io)};
+}
+bool conv_apart(const ConvArgs& a, const void* tail0) {
+    return apart({conv_rows(a, a.y, a.D), conv_tail(a, a.tail)},
+                 {conv_rows(a, a.x, a.ldx), conv_tail(a, tail0), {a.w, floats(a.D, a.K)}, {a.bias, floats(a.D)}, offsets(a.rows)});
 }
 
 gret_status conv(const void* x, long long ldx, const float* w, const float* bias, const void* tail0, void* y,
@@ -82,8 +108,7 @@ gret_status conv(const void* x, long long ldx, const float* w, const float* bias
     if (act != GRET_ACT_NONE && act != GRET_ACT_SWISH) return GRET_ERR_INVALID_ARG;
     const ConvArgs a = {x, ldx, w, bias, tail0, y, tail, rows, D, K, act == GRET_ACT_SWISH, io};
     if (gret_status e = conv_check(a)) return e;
-    const size_t tail_bytes = (size_t)rows.B * (K - 1) * D * size_of(io);
-    if (overlap(tail0, tail, tail_bytes)) return GRET_ERR_INVALID_ARG;
+    if (!conv_apart(a, tail0)) return GRET_ERR_INVALID_ARG;
     return done(launch_short_conv(a, cu_stream(stream)));
 }
 
@@ -99,12 +124,19 @@ gret_status scan_check(const ScanArgs& a) {
         return GRET_ERR_INVALID_ARG;
     const long long rows = rows_of(a.rows);
     if ((long long)a.rows.B * a.D * a.n > (1LL << 38) || rows * a.D > (1LL << 40)) return GRET_ERR_UNSUPPORTED;
-    const size_t out = span(rows, a.D, a.D, a.io);
-    if (overlap(a.u, span(rows, a.ldu, a.D, a.io), a.o, out) || overlap(a.dt, span(rows, a.lddt, a.D, a.io), a.o, out) ||
-        overlap(a.z, span(rows, a.ldz, a.D, a.io), a.o, out) || overlap(a.Bm, span(rows, a.ldb, a.n, a.io), a.o, out) ||
-        overlap(a.Cm, span(rows, a.ldc, a.n, a.io), a.o, out))
-        return GRET_ERR_INVALID_ARG;
     return GRET_OK;
+}
+
+// What a scan's arguments name, and whether its outputs are apart from what it reads.
+Region scan_rows(const ScanArgs& a, const void* p, long long ld, int width) {
+    return {p, span(rows_of(a.rows), ld, width, a.io)};
+}
+Region scan_state(const ScanArgs& a, const void* p) { return {p, floats(a.rows.B, a.D, a.n)}; }
+bool scan_apart(const ScanArgs& a, const float* h0, size_t workspace_bytes) {
+    return apart({scan_rows(a, a.o, a.D, a.D), scan_state(a, a.h), {workspace_bytes ? a.workspace : nullptr, workspace_bytes}},
+                 {scan_rows(a, a.u, a.ldu, a.D), scan_rows(a, a.dt, a.lddt, a.D), scan_rows(a, a.z, a.ldz, a.D),
+                  scan_rows(a, a.Bm, a.ldb, a.n), scan_rows(a, a.Cm, a.ldc, a.n), {a.A, floats(a.D, a.n)},
+                  {a.skip, floats(a.D)}, {a.dt_bias, floats(a.D)}, scan_state(a, h0), offsets(a.rows)});
 }
 
 bool workspace_ok(const void* ws, size_t have, size_t need) {
@@ -113,11 +145,10 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 
 gret_status scan(ScanArgs a, size_t workspace_bytes, gret_stream_t stream) {
     if (gret_status e = scan_check(a)) return e;
-    if (overlap(a.h0, a.h, (size_t)a.rows.B * a.D * a.n * sizeof(float))) return GRET_ERR_INVALID_ARG;
     int sms = 148;
     const bool device = device_info(nullptr, &sms);
     const size_t need = selective_scan_ws_bytes(a.rows.B, a.rows.N, a.rows.total, a.D, a.n, a.rows.cu != nullptr, sms);
-    if (!workspace_ok(a.workspace, workspace_bytes, need)) return GRET_ERR_INVALID_ARG;
+    if (!workspace_ok(a.workspace, workspace_bytes, need) || !scan_apart(a, a.h0, need)) return GRET_ERR_INVALID_ARG;
     if (!device) return GRET_ERR_CUDA;
     return done(launch_selective_scan(a, sms, cu_stream(stream)));
 }
@@ -169,8 +200,7 @@ gret_status gret_short_conv_step(const void* x, long long ldx, const float* w, c
     const ConvArgs a = {x, ldx, w, bias, tail_in, y, tail_out, uniform(num_seqs, 1), D, K,
                         act == GRET_ACT_SWISH, io_dtype};
     if (gret_status e = conv_check(a)) return e;
-    if (tail_in != tail_out && overlap(tail_in, tail_out, (size_t)num_seqs * (K - 1) * D * size_of(io_dtype)))
-        return GRET_ERR_INVALID_ARG;
+    if (!conv_apart(a, tail_in == tail_out ? nullptr : tail_in)) return GRET_ERR_INVALID_ARG;
     return done(launch_short_conv_step(a, cu_stream(stream)));
 }
 
@@ -213,7 +243,7 @@ gret_status gret_selective_step(const void* u, long long ldu, const void* dt, lo
     const ScanArgs a = {u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h_in, o, h_out,
                         uniform(num_seqs, 1), D, n, io_dtype, nullptr};
     if (gret_status e = scan_check(a)) return e;
-    if (h_in != h_out && overlap(h_in, h_out, (size_t)num_seqs * D * n * sizeof(float))) return GRET_ERR_INVALID_ARG;
+    if (!scan_apart(a, h_in == h_out ? nullptr : h_in, 0)) return GRET_ERR_INVALID_ARG;
     return done(launch_selective_step(a, cu_stream(stream)));
 }
 
@@ -224,13 +254,11 @@ gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long
     const NormArgs a = {x, y, gate, ldx, ldy, ldg, scale, w_post, w_next, r, n, T, D, eps, stream_dtype, io_dtype};
     if (gret_status e = norm_check(a)) return e;
     if ((y && !r) || (w_next && !n)) return GRET_ERR_INVALID_ARG;
-    // r may be x itself; nothing else may meet
-    const size_t xs = span(T, ldx, D, stream_dtype), ys = span(T, ldy, D, io_dtype), gs = span(T, ldg, D, io_dtype);
-    const size_t rs = span(T, D, D, stream_dtype), ns = span(T, D, D, io_dtype);
-    if (!y) r = nullptr;
-    if (!w_next) n = nullptr;
-    if ((overlap(x, xs, r, rs) && !(r == x && ldx == D)) || overlap(y, ys, r, rs) || overlap(gate, gs, r, rs) ||
-        overlap(x, xs, n, ns) || overlap(y, ys, n, ns) || overlap(gate, gs, n, ns) || overlap(r, rs, n, ns))
+    // r may be x itself
+    const bool in_place = y && r == x && ldx == D;
+    if (!apart({{y ? r : nullptr, span(T, D, D, stream_dtype)}, {w_next ? n : nullptr, span(T, D, D, io_dtype)}},
+               {{in_place ? nullptr : x, span(T, ldx, D, stream_dtype)}, {y, span(T, ldy, D, io_dtype)},
+                {gate, span(T, ldg, D, io_dtype)}, {scale, floats(D)}, {w_post, floats(D)}, {w_next, floats(D)}}))
         return GRET_ERR_INVALID_ARG;
     int sms = 0;
     if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
@@ -252,7 +280,12 @@ gret_status gret_short_conv_backward(const void* x, long long ldx, const float* 
     ConvBackwardArgs g = {};
     g.f = ConvArgs{x, ldx, w, bias, tail0, dx, nullptr, uniform(B, N), D, K, act == GRET_ACT_SWISH, io_dtype};
     if (gret_status e = conv_check(g.f)) return e;
-    if (!workspace_ok(workspace, workspace_bytes, short_conv_backward_ws_bytes(B, N, D, K))) return GRET_ERR_INVALID_ARG;
+    const size_t need = short_conv_backward_ws_bytes(B, N, D, K);
+    if (!workspace_ok(workspace, workspace_bytes, need)) return GRET_ERR_INVALID_ARG;
+    if (!apart({conv_rows(g.f, dx, D), {dw, floats(D, K)}, {dbias, floats(D)}, conv_tail(g.f, dtail0), {workspace, need}},
+               {conv_rows(g.f, x, ldx), {w, floats(D, K)}, {bias, floats(D)}, conv_tail(g.f, tail0),
+                conv_rows(g.f, dy, D), conv_tail(g.f, dtail)}))
+        return GRET_ERR_INVALID_ARG;
     g.dy = dy; g.dtail = dtail; g.dx = dx; g.dtail0 = dtail0; g.dw = dw; g.dbias = dbias; g.workspace = workspace;
     return done(launch_short_conv_backward(g, cu_stream(stream)));
 }
@@ -277,7 +310,15 @@ gret_status gret_selective_scan_backward(const void* u, long long ldu, const voi
     g.f = ScanArgs{u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h0, du, nullptr,
                    uniform(B, N), D, n, io_dtype, nullptr};
     if (gret_status e = scan_check(g.f)) return e;
-    if (!workspace_ok(workspace, workspace_bytes, selective_backward_ws_bytes(B, N, D, n, io_dtype)))
+    const size_t need = selective_backward_ws_bytes(B, N, D, n, io_dtype);
+    if (!workspace_ok(workspace, workspace_bytes, need)) return GRET_ERR_INVALID_ARG;
+    const ScanArgs& f = g.f;
+    if (!apart({scan_rows(f, du, D, D), scan_rows(f, ddt, D, D), scan_rows(f, z ? dz : nullptr, D, D),
+                scan_rows(f, dBm, n, n), scan_rows(f, dCm, n, n), {dA, floats(D, n)}, {dskip, floats(D)},
+                {ddt_bias, floats(D)}, scan_state(f, dh0), {workspace, need}},
+               {scan_rows(f, u, ldu, D), scan_rows(f, dt, lddt, D), scan_rows(f, z, ldz, D), scan_rows(f, Bm, ldb, n),
+                scan_rows(f, Cm, ldc, n), {A, floats(D, n)}, {skip, floats(D)}, {dt_bias, floats(D)}, scan_state(f, h0),
+                scan_rows(f, dout, D, D), scan_state(f, dh_final)}))
         return GRET_ERR_INVALID_ARG;
     int sms = 0;
     if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
@@ -307,7 +348,14 @@ gret_status gret_residual_norm_backward(const void* x, long long ldx, const void
     if (!all_aligned(dr, dn, dx, dy, dgate, dscale, dw_post, dw_next)) return GRET_ERR_INVALID_ARG;
     int sms = 148;
     const bool device = device_info(&g.status, &sms);
-    if (!workspace_ok(workspace, workspace_bytes, residual_norm_backward_ws_bytes(T, D, sms))) return GRET_ERR_INVALID_ARG;
+    const size_t need = residual_norm_backward_ws_bytes(T, D, sms), stream_row = span(T, D, D, stream_dtype),
+                 block_row = span(T, D, D, io_dtype);
+    if (!workspace_ok(workspace, workspace_bytes, need)) return GRET_ERR_INVALID_ARG;
+    if (!apart({{dx, stream_row}, {y ? dy : nullptr, block_row}, {gate ? dgate : nullptr, block_row}, {dscale, floats(D)},
+                {dw_post, floats(D)}, {dw_next, floats(D)}, {workspace, need}},
+               {{x, span(T, ldx, D, stream_dtype)}, {y, span(T, ldy, D, io_dtype)}, {gate, span(T, ldg, D, io_dtype)},
+                {scale, floats(D)}, {w_post, floats(D)}, {w_next, floats(D)}, {dr, stream_row}, {dn, block_row}}))
+        return GRET_ERR_INVALID_ARG;
     if (!device) return GRET_ERR_CUDA;
     g.dr = dr; g.dn = dn; g.dx = dx; g.dy = dy; g.dgate = dgate;
     g.dscale = dscale; g.dw_post = dw_post; g.dw_next = dw_next; g.workspace = workspace;

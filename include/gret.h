@@ -359,8 +359,9 @@ size_t gret_prefill_projected_workspace_size(int B, int H, int N, int dk, int dv
  * at b * N + n.  Outputs, states and parameters are contiguous.  Parameters,
  * states and sums are fp32.  Pointers must be 16-byte aligned; D is a multiple
  * of 8, at most 65536; all rows together, and one more for each packed sequence,
- * number less than 2^31 - 2^20.  An output must
- * not overlap an input except where it is said (the forward calls refuse it).
+ * number less than 2^31 - 2^20.  No output (the workspace among them) may overlap
+ * an input or another output except where it is said; a call that would is
+ * refused, a tensor counting from its first row to the end of its last.
  * A call may be captured into a CUDA graph once one like it has run outside a
  * capture.
  * ------------------------------------------------------------------------ */

@@ -271,3 +271,80 @@ def test_python_sizes_past_31_bits():
         with pytest.raises(gret.GretError) as e:
             call()
         assert e.value.status == UNSUPPORTED
+
+
+# Every pointer of every call: its bytes, and whether the call writes there.  Pointers may be moved onto one another.
+def _regions():
+    B, N, D, K, n, T = 2, 40, 64, 4, 16, 80
+    row, tail, state, par, ab = T * D * 2, B * (K - 1) * D * 2, B * D * n * 4, D * 4, T * n * 2
+    conv_in = dict(x=row, w=D * K * 4, bias=par, tail0=tail)
+    scan_in = dict(u=row, dt=row, A=D * n * 4, Bm=ab, Cm=ab, skip=par, z=row, dt_bias=par, h0=state)
+    norm_in = dict(x=row, y=row, gate=row, scale=par, w_post=par, w_next=par)
+    lds = dict(ldu=D, lddt=D, ldb=n, ldc=n, ldz=D)
+    conv = dict(ldx=D, D=D, K=K, io_dtype=BF, act=1, stream=None)
+    scan = dict(lds, D=D, n=n, io_dtype=BF, stream=None)
+    norm = dict(ldx=D, ldy=D, ldg=D, T=T, D=D, eps=1e-5, stream_dtype=BF, io_dtype=BF, stream=None)
+    cu = dict(cu_seqlens=(B + 1) * 4)
+    packed = dict(num_seqs=B, total_tokens=T, max_seqlen=N)
+    step_row, step_ab = B * D * 2, B * n * 2
+    size = gret.gret_selective_scan_workspace_size
+    # few channels and many tokens, so that the sequence is cut and needs a workspace
+    cut = dict(lds, ldu=8, lddt=8, ldz=8, B=1, N=4000, D=8, n=n, io_dtype=BF, stream=None)
+    cut_row, cut_ab, cut_ws = 4000 * 8 * 2, 4000 * n * 2, size(1, 4000, 8, n, BF)
+    cut_in = dict(u=cut_row, dt=cut_row, A=8 * n * 4, Bm=cut_ab, Cm=cut_ab, skip=32, z=cut_row, dt_bias=32, h0=8 * n * 4)
+    conv_ws = gret.gret_short_conv_backward_workspace_size(B, N, D, K, BF)
+    scan_ws = gret.gret_selective_scan_backward_workspace_size(B, N, D, n, BF)
+    norm_ws = gret.gret_residual_norm_backward_workspace_size(T, D)
+    assert cut_ws and conv_ws and scan_ws and norm_ws
+    return {
+        "conv": (gret.gret_short_conv, conv_in, dict(y=row, tail=tail), dict(conv, B=B, N=N)),
+        "conv_varlen": (gret.gret_short_conv_varlen, dict(conv_in, **cu), dict(y=row, tail=tail), dict(conv, **packed)),
+        "conv_step": (gret.gret_short_conv_step, dict(x=step_row, w=D * K * 4, bias=par, tail_in=tail),
+                      dict(y=step_row, tail_out=tail), dict(conv, num_seqs=B)),
+        "conv_backward": (gret.gret_short_conv_backward, dict(conv_in, dy=row, dtail=tail),
+                          dict(dx=row, dw=D * K * 4, dbias=par, dtail0=tail, workspace=conv_ws),
+                          dict(conv, B=B, N=N, workspace_bytes=conv_ws)),
+        "scan": (gret.gret_selective_scan, cut_in, dict(o=cut_row, h_final=8 * n * 4, workspace=cut_ws),
+                 dict(cut, workspace_bytes=cut_ws)),
+        "scan_varlen": (gret.gret_selective_scan_varlen, dict(scan_in, **cu), dict(o=row, h_final=state),
+                        dict(scan, **packed, workspace=1 << 40, workspace_bytes=1 << 30)),
+        "step": (gret.gret_selective_step,
+                 dict(u=step_row, dt=step_row, A=D * n * 4, Bm=step_ab, Cm=step_ab, skip=par, z=step_row, dt_bias=par,
+                      h_in=state), dict(o=step_row, h_out=state), dict(scan, num_seqs=B)),
+        "scan_backward": (gret.gret_selective_scan_backward, dict(scan_in, dout=row, dh_final=state),
+                          dict(du=row, ddt=row, dA=D * n * 4, dBm=ab, dCm=ab, dskip=par, dz=row, ddt_bias=par, dh0=state,
+                               workspace=scan_ws), dict(scan, B=B, N=N, workspace_bytes=scan_ws)),
+        "norm": (gret.gret_residual_norm, norm_in, dict(r=row, n=row), norm),
+        "norm_backward": (gret.gret_residual_norm_backward, dict(norm_in, dr=row, dn=row),
+                          dict(dx=row, dy=row, dgate=row, dscale=par, dw_post=par, dw_next=par, workspace=norm_ws),
+                          dict(norm, workspace_bytes=norm_ws)),
+    }
+
+
+IN_PLACE = {("norm", "r", "x"), ("conv_step", "tail_out", "tail_in"), ("step", "h_out", "h_in")}
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers name no memory: only where nothing can be launched")
+@pytest.mark.parametrize("name", ["conv", "conv_varlen", "conv_step", "conv_backward", "scan", "scan_varlen", "step",
+                                  "scan_backward", "norm", "norm_backward"])
+def test_outputs_apart_from_inputs_and_one_another(name):
+    """An output that meets an input or another output by 16 bytes is refused, one that ends where it begins is not."""
+    call, inputs, outputs, rest = _regions()[name]
+    sizes = dict(inputs, **outputs)
+    at = {k: (i + 1) << 28 for i, k in enumerate(sizes)}
+    ok = gret.Status.ERR_CUDA                    # past all checks: there is no device to launch on
+    assert call(**at, **rest) == ok
+    for out in outputs:
+        for other in sizes:
+            if other == out:
+                continue
+            step = 256 if out == "workspace" else 16
+            behind, before = at[other] + sizes[other], at[other] - sizes[out]
+            near = behind - 1 & -step            # the last place that still meets it
+            assert call(**dict(at, **{out: near}), **rest) == INVALID, (out, other)
+            assert call(**dict(at, **{out: -(-behind // step) * step}), **rest) == ok, (out, other)
+            assert call(**dict(at, **{out: before & -step}), **rest) == ok, (out, other)
+            if sizes[out] >= step:
+                assert call(**dict(at, **{out: (before & -step) + step}), **rest) == INVALID, (out, other)
+            same = dict(at, **{out: at[other]})
+            assert call(**same, **rest) == (ok if (name, out, other) in IN_PLACE else INVALID), (out, other)
