@@ -2,12 +2,27 @@
 // channels and states.
 #pragma once
 
+#include <float.h>
+
 #include "gret_block.cuh"
 
 namespace gret {
 
 constexpr int kScanWarps = 4;       // warps of a block: neighbouring channels, the same tokens
 constexpr int kPair = 2;            // channels of a lane
+
+// A in powers of two a unit step.  A = -inf, which keeps nothing of the tokens
+// before, and an A whose product with log2 e passes fp32 are the lowest finite
+// number: a step of zero, as the tokens that fill a group have, then leaves the
+// state as it is instead of giving 0 x inf.  NaN stays NaN.
+__device__ __forceinline__ float log2_rate(float A) {
+    const float x = A * kLog2e;
+    return x < -FLT_MAX ? -FLT_MAX : x;
+}
+__device__ __forceinline__ float2 log2_rate(float2 A) { return make_float2(log2_rate(A.x), log2_rate(A.y)); }
+__device__ __forceinline__ float4 log2_rate(float4 A) {
+    return make_float4(log2_rate(A.x), log2_rate(A.y), log2_rate(A.z), log2_rate(A.w));
+}
 
 // The values of a lane's two channels x SPL states, as pairs of states, from
 // or to rows of n per channel; a channel from `end` on reads as zero.
@@ -65,7 +80,7 @@ template <bool kAfter, int Y>
 __device__ __forceinline__ float4 fold_segments(FoldShared<Y>& shared, bool on, float* v, long long stride, const float* sums,
                                                 long long step, int count, float4 A, float4 x) {
     const int tx = threadIdx.x, ty = threadIdx.y;
-    A = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
+    A = log2_rate(A);
     for (int base = 0; base < count; base += Y * kFoldU) {
         const int first = base + ty * kFoldU, mine = on ? min(kFoldU, count - first) : 0;
         float4 l[kFoldU];

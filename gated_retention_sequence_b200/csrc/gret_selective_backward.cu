@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, 4) ends_kernel(const ScanBack
     for (int c = 0; c < kPair; ++c)
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            A[c][i] = mul2(A[c][i], both(kLog2e));
+            A[c][i] = log2_rate(A[c][i]);
             h[c][i] = back[c][i] = both(0.f);
             P[c][i] = both(1.f);
         }
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, NS == 64 ? 2 : 3) walk_kernel
         for (int c = 0; c < kPair; ++c)
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                A[c][i] = mul2(A[c][i], both(kLog2e));
+                A[c][i] = log2_rate(A[c][i]);
                 dA[c][i] = both(0.f);
             }
         // the state before every group

@@ -102,7 +102,7 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, int block
 #pragma unroll
     for (int c = 0; c < kPair; ++c)
 #pragma unroll
-        for (int i = 0; i < H; ++i) A[c][i] = mul2(A[c][i], both(kLog2e));
+        for (int i = 0; i < H; ++i) A[c][i] = log2_rate(A[c][i]);
     if (kFinal) {
 #pragma unroll 2
         for (int k = 1; k <= apart; ++k) {
@@ -470,8 +470,7 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Scan
         raw[k] = to_f32(static_cast<const T*>(a.dt)[b * a.lddt + d]);
         z[k] = a.z ? to_f32(static_cast<const T*>(a.z)[b * a.ldz + d]) : 0.f;
     }
-    float4 A = *reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q);
-    A = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
+    const float4 A = log2_rate(*reinterpret_cast<const float4*>(a.A + (size_t)d * NS + q));
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
 #pragma unroll
     for (int k = 0; k < kStepSeqs; k += 2) {

@@ -405,7 +405,9 @@ gret_status gret_short_conv_step(const void* x, long long ldx, const float* w, c
  *   u, dt, z  [B][N][D] io dtype with row strides ldu, lddt, ldz; z may be NULL
  *             (no gate)
  *   Bm, Cm    [B][N][n] io dtype with row strides ldb, ldc, shared by all channels
- *   A         fp32 [D][n]; negative in a model that decays
+ *   A         fp32 [D][n]; negative in a model that decays, and -inf where nothing
+ *             is kept.  Where A is positive the growth over any run of tokens must
+ *             stay within fp32, as a long sequence is joined from segments.
  *   skip, dt_bias  fp32 [D] or NULL (zero)
  *   h0        fp32 [B][D][n], the state before the first token, or NULL (zero)
  *   o         [B][N][D];  h_final fp32 [B][D][n] or NULL, must not overlap h0

@@ -708,3 +708,52 @@ def test_scan_backward_of_the_most_channels(io):
     few = {k: v if k in ("B", "C") else v[:, keep] if k in ROWS + ("h0",) else v[keep] for k, v in p.items()}
     g = {k: v if k in ("dB", "dC") else v[..., keep, :] if k in ("dA", "dh0") else v[..., keep] for k, v in g.items()}
     check_scan_backward(io, few, do[..., keep], dh[:, keep], g, 1, N)
+
+
+# A that keeps nothing of the tokens before: any step of more than 1e-3 decays to zero in 32 bits and in 64, so the
+# oracle takes a finite number in their place.
+NOTHING = (float("-inf"), -3.4e38, -3e38, -1e30)
+
+
+def keep_nothing(p):
+    p["dt_bias"].zero_()
+    for i, a in enumerate(NOTHING):
+        p["A"][2 * i] = a                        # a channel of them
+        p["A"][2 * i + 1, 1::3] = a              # and a channel with some
+    return dict(p, A=p["A"].clamp(min=-1e6))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("B,N", [(2, 1), (1, 17), (2, 63), (2, 1203)])
+def test_scan_that_keeps_nothing(io, n, B, N):
+    D = 24
+    p = scan_inputs(io, B * N, D, n, B)
+    ref = keep_nothing(p)
+    o, h = scan_call(p, B, N)
+    cu = torch.arange(0, B * N + 1, N, dtype=torch.int32, device="cuda")
+    o2, h2 = gret.selective_scan_varlen(**p, cu_seqlens=cu, max_seqlen=N)
+    for b in range(B):
+        ro, rh = bo.selective_scan(**scan_rows(ref, b * N, (b + 1) * N, b))
+        bo.check(o[b], ro, io, f"o of sequence {b}")
+        bo.check(h[b], rh, "f32", f"h of sequence {b}")
+        bo.check(o2[b * N:(b + 1) * N], ro, io, f"o of packed sequence {b}")
+        bo.check(h2[b], rh, "f32", f"h of packed sequence {b}")
+    if N == 1:
+        h0 = p.pop("h0")
+        o, h = gret.selective_step(**p, h=h0.clone())
+        for b in range(B):
+            ro, rh = bo.selective_scan(**scan_rows(ref, b, b + 1, b))
+            bo.check(o[b:b + 1], ro, io)
+            bo.check(h[b], rh, "f32")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("B,N", [(2, 1), (2, 17), (2, 601)])
+def test_scan_backward_that_keeps_nothing(io, n, B, N):
+    D = 24
+    p = scan_inputs(io, B * N, D, n, B)
+    ref = keep_nothing(p)
+    do, dh = draw(10, (B, N, D), io), draw(11, (B, D, n))
+    check_scan_backward(io, ref, do, dh, scan_backward_call(p, do, B, N, dh_final=dh), B, N)
