@@ -55,7 +55,10 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return warp_sum((threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f);
 }
 
-// Eight sums behind one barrier; `red`: 128 words (at most 16 warps).  Each
+// Eight sums behind one barrier, which also orders the block's shared memory
+// before and after it, in a block of one warp too (a shuffle alone does not: the
+// row that a copy is about to replace has been read by all); `red`: 128 words (at
+// most 16 warps).  Each
 // round halves the values a lane keeps, so that a lane ends with one of the
 // eight over its warp, and after the barrier with one over four warps.
 __device__ __forceinline__ void block_sums(float* v, float* red) {
@@ -84,6 +87,8 @@ __device__ __forceinline__ void block_sums(float* v, float* red) {
         sum = (left > 0 ? q.x : 0.f) + (left > 1 ? q.y : 0.f) + (left > 2 ? q.z : 0.f) + (left > 3 ? q.w : 0.f);
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    } else {
+        __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, sum, 4 * i);

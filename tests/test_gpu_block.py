@@ -757,3 +757,24 @@ def test_scan_backward_that_keeps_nothing(io, n, B, N):
     ref = keep_nothing(p)
     do, dh = draw(10, (B, N, D), io), draw(11, (B, D, n))
     check_scan_backward(io, ref, do, dh, scan_backward_call(p, do, B, N, dh_final=dh), B, N)
+
+
+def check_norm(io, stream, T, D):
+    p = norm_inputs(io, stream, T, D)
+    r, n = gret.residual_norm(**p)
+    rr, rn = bo.residual_norm(**p)
+    bo.check(r, rr, stream, "r")
+    bo.check(n, rn, io, "n")
+    dr, dn = draw(8, (T, D), stream), draw(9, (T, D), io)
+    g = gret.residual_norm_backward(**p, dr=dr, dn=dn)
+    for k, v in bo.residual_norm(**p, dr=dr, dn=dn).items():
+        bo.check(g[k], v, stream if k == "dx" else io if k in ("dy", "dgate") else "f32", k)
+    again = gret.residual_norm_backward(**p, dr=dr, dn=dn)
+    assert all(torch.equal(g[k], again[k]) for k in g)
+
+
+@pytest.mark.parametrize("io,stream", KINDS)
+@pytest.mark.parametrize("D", [8, 72, 256])
+def test_norm_blocks_of_one_warp_with_many_rows(io, stream, D):
+    # 16 blocks an SM, each of one warp, whose rows in shared memory are replaced while it walks seven or eight rows
+    check_norm(io, stream, 16 * torch.cuda.get_device_properties(0).multi_processor_count * 7 + 5, D)
