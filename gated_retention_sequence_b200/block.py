@@ -500,13 +500,17 @@ def residual_norm(x, y=None, gate=None, scale=None, w_post=None, w_next=None, ep
     r = x + scale * rms(y) * w_post * swish(gate);  n = rms(r) * w_next, with rms(v) = v / sqrt(mean(v^2) + eps).
     x [...,D] bf16 or fp32 (the residual stream); y, gate [...,D] in x's dtype, or bf16 beside an fp32 x; scale, w_post,
     w_next [D] fp32.  Each of gate, scale, w_post and w_next may be None; without y the call is the norm alone.
-    Returns (r in x's dtype, n in y's dtype or None); ``r=x`` updates the stream in place.  Without y, n has x's dtype
-    unless a buffer for it is given (bf16 beside an fp32 stream)."""
+    Returns (r in x's dtype, n in y's dtype or None); ``r=x`` updates the stream in place.  Without y, r is x itself and n
+    has x's dtype unless a buffer for it is given (bf16 beside an fp32 stream)."""
     torch = _g._torch()
     dev, sd, io, T, D, ld = _norm_inputs(x, y, gate, scale, w_post, w_next, n)
     io_torch = torch.float32 if io == Dtype.F32 else torch.bfloat16
     _opt(r, "r", x.dtype, x.shape, dev)
     _opt(n, "n", io_torch, x.shape, dev)
+    if n is not None and w_next is None:
+        raise ValueError("n goes with w_next")
+    if r is not None and y is None and r.data_ptr() != x.data_ptr():
+        raise ValueError("r goes with y")
     with _on(dev, stream) as st:
         if y is None:
             r = x

@@ -348,3 +348,14 @@ def test_outputs_apart_from_inputs_and_one_another(name):
                 assert call(**dict(at, **{out: (before & -step) + step}), **rest) == INVALID, (out, other)
             same = dict(at, **{out: at[other]})
             assert call(**same, **rest) == (ok if (name, out, other) in IN_PLACE else INVALID), (out, other)
+
+
+def test_norm_buffers_that_nothing_would_write_are_refused():
+    class Cuda(torch.Tensor):
+        is_cuda = True
+
+    x, other, w = (torch.zeros(s).as_subclass(Cuda) for s in ((3, 64), (3, 64), (64,)))
+    with pytest.raises(ValueError, match="n goes with w_next"):
+        gret.residual_norm(x, y=other, n=torch.zeros(3, 64).as_subclass(Cuda))
+    with pytest.raises(ValueError, match="r goes with y"):
+        gret.residual_norm(x, w_next=w, r=other)
