@@ -204,6 +204,8 @@ def _on(dev, stream):
         if torch.cuda.current_device() == dev.index:
             return _Here(torch._C._cuda_getCurrentRawStream(dev.index))
         stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, expected {dev}")
     return _elsewhere(dev, stream)
 
 

@@ -359,3 +359,13 @@ def test_norm_buffers_that_nothing_would_write_are_refused():
         gret.residual_norm(x, y=other, n=torch.zeros(3, 64).as_subclass(Cuda))
     with pytest.raises(ValueError, match="r goes with y"):
         gret.residual_norm(x, w_next=w, r=other)
+
+
+def test_stream_of_another_device_is_refused():
+    """A launch would go to the stream's device, with pointers of the tensors'."""
+    from types import SimpleNamespace
+
+    from gated_retention_sequence_b200.block import _on
+
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        _on(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0))
