@@ -83,12 +83,16 @@ gret_status done(cudaError_t e) { return e == cudaSuccess ? GRET_OK : GRET_ERR_C
 cudaStream_t cu_stream(gret_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // ------------------------------------------------------------ short convolution
+gret_status conv_sizes(const Rows& r, int D, int K) {
+    if (D <= 0 || K <= 0) return GRET_ERR_INVALID_ARG;
+    if (gret_status e = rows_ok(r)) return e;
+    return D % kVec != 0 || D > kMaxChannels || K < 2 || K > 4 ? GRET_ERR_UNSUPPORTED : GRET_OK;
+}
+
 gret_status conv_check(const ConvArgs& a) {
     if (!all_set(a.x, a.w, a.y) || !type_ok(a.io)) return GRET_ERR_INVALID_ARG;
-    if (a.D <= 0 || a.K <= 0) return GRET_ERR_INVALID_ARG;
-    if (gret_status e = rows_ok(a.rows)) return e;
     if (!all_aligned(a.x, a.w, a.bias, a.tail0, a.y, a.tail)) return GRET_ERR_INVALID_ARG;
-    if (a.D % kVec != 0 || a.D > kMaxChannels || a.K < 2 || a.K > 4) return GRET_ERR_UNSUPPORTED;
+    if (gret_status e = conv_sizes(a.rows, a.D, a.K)) return e;
     if (!stride_ok(a.ldx, a.D, a.io)) return GRET_ERR_INVALID_ARG;
     return GRET_OK;
 }
@@ -113,17 +117,21 @@ gret_status conv(const void* x, long long ldx, const float* w, const float* bias
 }
 
 // --------------------------------------------------------------- selective scan
+gret_status scan_sizes(const Rows& r, bool packed, int D, int n) {
+    if (D <= 0 || n <= 0) return GRET_ERR_INVALID_ARG;
+    if (gret_status e = rows_ok(r, packed)) return e;
+    if (D % kVec != 0 || D > kMaxChannels || !selective_states_supported(n)) return GRET_ERR_UNSUPPORTED;
+    const long long rows = packed ? (long long)r.total : (long long)r.B * r.N;
+    return (long long)r.B * D * n > (1LL << 38) || rows * D > (1LL << 40) ? GRET_ERR_UNSUPPORTED : GRET_OK;
+}
+
 gret_status scan_check(const ScanArgs& a) {
     if (!all_set(a.u, a.dt, a.A, a.Bm, a.Cm, a.o) || !type_ok(a.io)) return GRET_ERR_INVALID_ARG;
-    if (a.D <= 0 || a.n <= 0) return GRET_ERR_INVALID_ARG;
-    if (gret_status e = rows_ok(a.rows)) return e;
     if (!all_aligned(a.u, a.dt, a.A, a.Bm, a.Cm, a.skip, a.z, a.dt_bias, a.h0, a.o, a.h)) return GRET_ERR_INVALID_ARG;
-    if (a.D % kVec != 0 || a.D > kMaxChannels || !selective_states_supported(a.n)) return GRET_ERR_UNSUPPORTED;
+    if (gret_status e = scan_sizes(a.rows, a.rows.cu != nullptr, a.D, a.n)) return e;
     if (!stride_ok(a.ldu, a.D, a.io) || !stride_ok(a.lddt, a.D, a.io) || !stride_ok(a.ldb, a.n, a.io) ||
         !stride_ok(a.ldc, a.n, a.io) || (a.z && !stride_ok(a.ldz, a.D, a.io)))
         return GRET_ERR_INVALID_ARG;
-    const long long rows = rows_of(a.rows);
-    if ((long long)a.rows.B * a.D * a.n > (1LL << 38) || rows * a.D > (1LL << 40)) return GRET_ERR_UNSUPPORTED;
     return GRET_OK;
 }
 
@@ -154,7 +162,7 @@ gret_status scan(ScanArgs a, size_t workspace_bytes, gret_stream_t stream) {
 }
 
 size_t scan_workspace(const Rows& r, int D, int n, bool packed, gret_dtype io) {
-    if (!type_ok(io) || rows_ok(r, packed) || D <= 0 || D % kVec != 0 || !selective_states_supported(n)) return 0;
+    if (!type_ok(io) || scan_sizes(r, packed, D, n)) return 0;
     int sms = 148;
     device_info(nullptr, &sms);
     return selective_scan_ws_bytes(r.B, r.N, r.total, D, n, packed, sms);
@@ -266,7 +274,7 @@ gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long
 }
 
 size_t gret_short_conv_backward_workspace_size(int B, int N, int D, int K, gret_dtype io_dtype) {
-    if (rows_ok(uniform(B, N)) || D <= 0 || D % kVec != 0 || K < 2 || K > 4 || !type_ok(io_dtype)) return 0;
+    if (conv_sizes(uniform(B, N), D, K) || !type_ok(io_dtype)) return 0;
     return short_conv_backward_ws_bytes(B, N, D, K);
 }
 
@@ -291,9 +299,7 @@ gret_status gret_short_conv_backward(const void* x, long long ldx, const float* 
 }
 
 size_t gret_selective_scan_backward_workspace_size(int B, int N, int D, int n, gret_dtype io_dtype) {
-    if (rows_ok(uniform(B, N)) || D <= 0 || D % kVec != 0 || !selective_states_supported(n) ||
-        !type_ok(io_dtype))
-        return 0;
+    if (scan_sizes(uniform(B, N), false, D, n) || !type_ok(io_dtype)) return 0;
     return selective_backward_ws_bytes(B, N, D, n, io_dtype);
 }
 
@@ -328,7 +334,7 @@ gret_status gret_selective_scan_backward(const void* u, long long ldu, const voi
 }
 
 size_t gret_residual_norm_backward_workspace_size(long long T, int D) {
-    if (T <= 0 || D <= 0 || D % kVec != 0 || D > kNormMaxChannels) return 0;
+    if (T <= 0 || T > 0x7fffffffLL || D <= 0 || D % kVec != 0 || D > kNormMaxChannels) return 0;
     int sms = 148;
     device_info(nullptr, &sms);
     return residual_norm_backward_ws_bytes(T, D, sms);

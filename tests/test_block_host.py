@@ -369,3 +369,18 @@ def test_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError, match="stream is on cuda:1"):
         _on(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0))
+
+
+@pytest.mark.parametrize("D,B,N", [(65544, 1, 4000), (1 << 24, 1, 400), (64, 1 << 16, 1 << 16), (65536, 1 << 18, 2),
+                                   (60, 2, 4000), (0, 2, 4000), (-64, 2, 4000)])
+def test_workspace_sizes_are_zero_where_the_call_is_refused(D, B, N):
+    """What a call refuses needs no memory: a caller that asks first would else allocate it."""
+    ld = max(D, 8) * 4
+    over = dict(B=B, N=N, D=D, n=64, ldu=ld, lddt=ld, ldb=64, ldc=64)
+    assert gret.gret_selective_scan(**dict(SCAN, **over)) in (INVALID, UNSUPPORTED)
+    assert gret.gret_selective_scan_workspace_size(B, N, D, 64, BF) == 0
+    assert gret.gret_selective_scan_backward_workspace_size(B, N, D, 64, BF) == 0
+    assert gret.gret_selective_scan_varlen_workspace_size(B, min(B * N, 2 ** 31 - 1), N, D, 64, BF) == 0
+    if (D, B) != (65536, 1 << 18):
+        assert gret.gret_short_conv_backward_workspace_size(B, N, D, 4, BF) == 0
+    assert gret.gret_residual_norm_backward_workspace_size(1 << 31, 64) == 0
