@@ -778,3 +778,151 @@ def check_norm(io, stream, T, D):
 def test_norm_blocks_of_one_warp_with_many_rows(io, stream, D):
     # 16 blocks an SM, each of one warp, whose rows in shared memory are replaced while it walks seven or eight rows
     check_norm(io, stream, 16 * torch.cuda.get_device_properties(0).multi_processor_count * 7 + 5, D)
+
+
+# ------------------------------------------------- cut sequences of every segment length and join
+PERIOD = 24                                      # channels that a wide tensor repeats: no warp's or block's share of them
+WARP = {8: 32, 16: 16, 32: 16, 64: 8}            # the scan's channels a warp
+
+
+def wide(t, D, dim=-1):
+    """24 channels, along `dim`, repeated up to D."""
+    return t.repeat([D // PERIOD if i == dim % t.dim() else 1 for i in range(t.dim())])
+
+
+def repeated(p, D):
+    """The scan's inputs of 24 channels, repeated up to D."""
+    at = {"A": 0, "h0": 1}
+    return {k: v if k in ("B", "C") or v is None else wide(v, D, at.get(k, -1)) for k, v in p.items()}
+
+
+def check_repeated(got, want, io, dim, what):
+    """The 24 channels' result, and the same bits in every repetition along `dim`."""
+    parts = got.split(PERIOD, dim)
+    bo.check(parts[0], want, io, what)
+    for i, part in enumerate(parts):
+        assert torch.equal(part, parts[0]), f"{what}, repetition {i}"
+
+
+TYPE_IDS = {"bf16": gret.Dtype.BF16, "f32": gret.Dtype.F32}
+# sequences, tokens of each, warps of channels -> tokens of a segment and segments of a sequence (on 148 SMs)
+CUTS = [(5, 500, 16, 32, 16), (2, 1500, 16, 32, 47), (6, 500, 21, 64, 8), (3, 1021, 21, 64, 16), (3, 1040, 21, 64, 17),
+        (2, 1700, 21, 64, 27), (4, 1200, 64, 80, 15), (2, 2500, 64, 80, 32)]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("B,N,warps,seg,segs", CUTS)
+def test_scan_cut_into_segments_of_many_tiles(io, n, B, N, warps, seg, segs):
+    """Segments of two, four and five tiles; up to 16 of them joined by the second launch, more by a fold."""
+    D = WARP[n] * warps // PERIOD * PERIOD
+    need = gret.gret_selective_scan_workspace_size(B, N, D, n, TYPE_IDS[io])
+    assert need // (D * (n + 1) * 4) == B * segs and -(-N // seg) == segs and -(-N // (seg + 16)) < segs
+    p = scan_inputs(io, B * N, PERIOD, n, B)
+    o, h = scan_call(repeated(p, D), B, N)
+    for b in range(B):
+        ro, rh = bo.selective_scan(**scan_rows(p, b * N, (b + 1) * N, b))
+        check_repeated(o[b], ro, io, 1, f"o of sequence {b}")
+        check_repeated(h[b], rh, "f32", 0, f"h of sequence {b}")
+
+
+# sequences in all, the long ones among them, warps of channels -> tokens of a segment; the longest has up to 16 segments
+# or more, and the batch up to 64 sequences (the rests by length), up to 256 (in the batch's order) or more (unranked)
+PACKED_CUTS = [(12, (1500, 100, 900), 40, 64), (12, (1000, 700), 40, 64), (40, (2000, 1100), 6, 16),
+               (70, (2000, 1100), 6, 16), (70, (2600, 64, 1100), 40, 64), (70, (950, 800), 40, 64),
+               (300, (2000, 1500), 6, 32), (300, (2500, 1700, 900), 30, 80), (300, (1000, 900), 30, 64)]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("S,longest,warps,seg", PACKED_CUTS)
+def test_scan_packed_and_cut_in_every_order(io, n, S, longest, warps, seg):
+    lens = list(longest) + [(37 * i) % 40 for i in range(S - len(longest))]
+    lens = [lens[i * 11 % S] for i in range(S)]                 # the long ones among the others
+    D, T = WARP[n] * warps // PERIOD * PERIOD, sum(lens) + 3
+    assert sorted(lens)[-len(longest):] == sorted(longest)
+    need = gret.gret_selective_scan_varlen_workspace_size(S, T, max(lens), D, n, TYPE_IDS[io])
+    slots = need // (D * (n + 1) * 4) - S
+    assert slots == T // seg and slots != T // (seg + 16) and (seg == 16 or slots != T // (seg - 16))
+    p = scan_inputs(io, T, PERIOD, n, S)
+    o = torch.full((T, D), 7.0, dtype=TYPES[io], device="cuda")
+    _, h = gret.selective_scan_varlen(**repeated(p, D), cu_seqlens=offsets(lens), max_seqlen=max(lens), o=o)
+    at = 0
+    for b, m in enumerate(lens):
+        if m:
+            ro, rh = bo.selective_scan(**scan_rows(p, at, at + m, b))
+            check_repeated(o[at:at + m], ro, io, 1, f"o of sequence {b}")
+            check_repeated(h[b], rh, "f32", 0, f"h of sequence {b}")
+        else:
+            assert torch.equal(h[b], wide(p["h0"][b], D, 0))
+        at += m
+    assert (o[at:] == 7).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+def test_scan_backward_of_several_sequences_of_many_segments(io, n):
+    # 22 segments or more each: folded in eight parts
+    B, N, D = 3, 700, 40
+    p = scan_inputs(io, B * N, D, n, B)
+    do, dh = draw(10, (B, N, D), io), draw(11, (B, D, n))
+    check_scan_backward(io, p, do, dh, scan_backward_call(p, do, B, N, dh_final=dh), B, N)
+
+
+# --------------------------------------------------- the convolution's long segments
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [2, 4])
+def test_conv_segments_of_64_tokens(io, K):
+    """Enough rows and channels that a thread walks 64 tokens, whose copies go around their buffers."""
+    B, N, D, lens = 2, 4737, 171 * PERIOD, [5000, 0, 1, 3, 4001, 63, 65, 300, 38]
+    T = B * N
+    assert T // 64 * (D // 4) >= 148 * 1024 and sum(lens) == T - 3
+    small = conv_inputs(io, T, PERIOD, K, len(lens))
+    p = {k: wide(v, D, 0 if k == "w" else -1) for k, v in small.items()}
+    y, tail = gret.short_conv(p["x"].view(B, N, D), p["w"], p["bias"], tail0=p["tail0"][:B])
+    for b in range(B):
+        ry, rt = bo.short_conv(small["x"][b * N:(b + 1) * N], small["w"], small["bias"], small["tail0"][b])
+        check_repeated(y[b], ry, io, 1, f"y of sequence {b}")
+        check_repeated(tail[b], rt, io, 1, f"tail of sequence {b}")
+    y = torch.full((T, D), 7.0, dtype=TYPES[io], device="cuda")
+    _, tail = gret.short_conv_varlen(p["x"], p["w"], p["bias"], offsets(lens), max(lens), tail0=p["tail0"], y=y)
+    at = 0
+    for b, m in enumerate(lens):
+        ry, rt = bo.short_conv(small["x"][at:at + m], small["w"], small["bias"], small["tail0"][b])
+        check_repeated(y[at:at + m], ry, io, 1, f"y of packed sequence {b}")
+        check_repeated(tail[b], rt, io, 1, f"tail of packed sequence {b}")
+        at += m
+    assert (y[at:] == 7).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [3, 4])
+def test_conv_backward_segments_of_128_tokens(io, K):
+    B, N, D = 2, 4737, 342 * PERIOD
+    slots = -(-N // 128) * B
+    assert gret.gret_short_conv_backward_workspace_size(B, N, D, K, TYPE_IDS[io]) // ((K + 1) * D * 4) == -(-slots // 4)
+    small = conv_inputs(io, B * N, PERIOD, K, B)
+    p = {k: wide(v, D, 0 if k == "w" else -1) for k, v in small.items()}
+    dy, dtail = draw(5, (B, N, PERIOD), io), draw(6, (B, K - 1, PERIOD), io)
+    g = gret.short_conv_backward(p["x"].view(B, N, D), p["w"], p["bias"], wide(dy, D), tail0=p["tail0"],
+                                 dtail=wide(dtail, D))
+    total = None
+    for b in range(B):
+        want = bo.short_conv(small["x"][b * N:(b + 1) * N], small["w"], small["bias"], small["tail0"][b], dy=dy[b],
+                             dtail=dtail[b])
+        check_repeated(g["dx"][b], want["dx"], io, 1, f"dx of sequence {b}")
+        check_repeated(g["dtail0"][b], want["dtail0"], io, 1, f"dtail0 of sequence {b}")
+        total = {k: want[k] if total is None else total[k] + want[k] for k in ("dw", "dbias")}
+    for k, v in total.items():
+        check_repeated(g[k], v, "f32", 0, k)
+
+
+# ------------------------------------------------------- the norm's blocks with many rows
+# Rows that go at least twice around a block's rows in shared memory, on 148 SMs: 2672 rows of 2048 channels (forward six
+# or seven rows a block, one vector a thread; gradients nine or ten), 1337 rows of up to 4096 (gradients nine or ten, one
+# vector a thread), 745 rows of more (five or six, two vectors); all parts and vectors that fill the rows at 2048, 4096
+# and 8192 channels
+@pytest.mark.parametrize("io,stream", KINDS)
+@pytest.mark.parametrize("T,D", [(2672, 2048), (1337, 2056), (1337, 4096), (745, 4104), (745, 8192)])
+def test_norm_blocks_with_many_rows(io, stream, T, D):
+    check_norm(io, stream, T, D)
