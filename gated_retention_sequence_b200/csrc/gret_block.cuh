@@ -206,9 +206,10 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoi
 
 // softplus of two numbers, max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].
 // log1p(e) = e P(e) with P of degree 9, the minimax fit of log1p(e) / e on
-// [0, 1] in relative error by Remez exchange (0.1 units; 2.5 units with P in
-// fp32, measured over the interval), so that small steps keep their relative
-// precision; one special function each instead of two.
+// [0, 1] in relative error by Remez exchange, so that small steps keep their
+// relative precision; one special function each instead of two.  In units of
+// 2^-24 over the interval: P of these fp32 coefficients is off by 0.56, and e P(e)
+// formed in fp32 by 2.6.
 __device__ __forceinline__ float2 softplus2(float2 x) {
     const float2 e = make_float2(exp2_approx(-kLog2e * fabsf(x.x)), exp2_approx(-kLog2e * fabsf(x.y)));
     float2 p = both(-0.0032440251670777798f);

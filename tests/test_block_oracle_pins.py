@@ -123,3 +123,26 @@ def test_bounds_hold_in_fp32():
         d = np.log1p(np.exp(p["dt"][t] + p["dt_bias"])).astype(np.float32)
         s = np.exp(d[:, None] * p["A"]) * s + (d * p["u"][t])[:, None] * p["B"][t]
     assert (np.abs(s - h.v) <= h.e).all()
+
+
+def test_softplus_polynomial_keeps_its_stated_error():
+    """The polynomial that the kernels take for log1p(e) / e, read from their source, against log1p in 64 bits."""
+    import os
+    import re
+
+    path = os.path.join(os.path.dirname(__file__), "..", "gated_retention_sequence_b200", "csrc", "gret_block.cuh")
+    with open(path) as f:
+        body = f.read().split("float2 softplus2(float2 x) {")[1].split("\n}")[0]
+    coefficients = [np.float32(c) for c in re.findall(r"both\((-?[0-9.]+)f\)", body)]
+    assert len(coefficients) == 10
+    e = np.unique(np.concatenate([np.linspace(0, 1, 500001)[1:], np.logspace(-30, 0, 100001)]).astype(np.float32))
+    x, want = e.astype(np.float64), np.log1p(e.astype(np.float64))
+    exact, single = np.zeros_like(x), np.zeros_like(e)
+    for c in coefficients:
+        exact = exact * x + np.float64(c)
+        # a fused multiply-add: the product of two fp32 is exact in 64 bits, the sum is rounded to 32
+        single = (single.astype(np.float64) * x + np.float64(c)).astype(np.float32)
+    single = (single.astype(np.float64) * x).astype(np.float32).astype(np.float64)
+    unit = 2.0 ** -24
+    assert np.abs(exact * x / want - 1).max() <= 0.56 * unit
+    assert np.abs(single / want - 1).max() <= 2.6 * unit
