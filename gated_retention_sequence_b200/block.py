@@ -248,7 +248,6 @@ def short_conv(x, w, bias=None, tail0=None, activation: Optional[str] = "swish",
 
     x [B,N,D] bf16 or fp32; w [D,K] fp32, K of 2 to 4 (the last tap takes the token itself); bias [D] fp32 or None;
     tail0 [B,K-1,D], the last inputs of the piece before, or None.  Returns (y [B,N,D], tail [B,K-1,D] or None)."""
-    torch = _g._torch()
     B, N, D = x.shape
     dev, io = x.device, _first(x)
     ldx = _rows(x, "x", x.dtype, x.shape, dev)
@@ -299,7 +298,6 @@ def short_conv_step(x, w, bias, tail, activation: Optional[str] = "swish", y=Non
     """One token per sequence (gret_short_conv_step): x [S,D], tail [S,K-1,D].
 
     The new tail goes to ``tail_out``, or over ``tail`` where that is None.  Returns (y [S,D], the new tail)."""
-    torch = _g._torch()
     S, D = x.shape
     dev, io = x.device, _first(x)
     ldx = _rows(x, "x", x.dtype, x.shape, dev)

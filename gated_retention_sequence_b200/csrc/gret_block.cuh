@@ -290,7 +290,7 @@ struct ConvArgs {
     int swish;
     gret_dtype io;
 };
-cudaError_t launch_short_conv(ConvArgs a, cudaStream_t s);
+cudaError_t launch_short_conv(ConvArgs a, int num_sms, cudaStream_t s);
 cudaError_t launch_short_conv_step(const ConvArgs& a, cudaStream_t s);   // tail0 -> tail, B rows
 
 struct ConvBackwardArgs {
@@ -300,8 +300,8 @@ struct ConvBackwardArgs {
     float *dw, *dbias;
     void* workspace;
 };
-size_t short_conv_backward_ws_bytes(int B, int N, int D, int K);
-cudaError_t launch_short_conv_backward(ConvBackwardArgs a, cudaStream_t s);
+size_t short_conv_backward_ws_bytes(int B, int N, int D, int K, int num_sms);
+cudaError_t launch_short_conv_backward(ConvBackwardArgs a, int num_sms, cudaStream_t s);
 
 struct ScanArgs {
     const void *u, *dt, *Bm, *Cm, *z;
@@ -327,8 +327,8 @@ struct ScanBackwardArgs {
     float *dA, *dskip, *ddt_bias, *dh0;
     void* workspace;
 };
-size_t selective_backward_ws_bytes(int B, int N, int D, int n, gret_dtype io);
-cudaError_t launch_selective_backward(ScanBackwardArgs a, int num_sms, cudaStream_t s);
+size_t selective_backward_ws_bytes(int B, int N, int D, int n);
+cudaError_t launch_selective_backward(const ScanBackwardArgs& a, cudaStream_t s);
 
 struct NormArgs {
     const void *x, *y, *gate;

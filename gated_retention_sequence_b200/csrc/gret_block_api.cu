@@ -113,7 +113,9 @@ gret_status conv(const void* x, long long ldx, const float* w, const float* bias
     const ConvArgs a = {x, ldx, w, bias, tail0, y, tail, rows, D, K, act == GRET_ACT_SWISH, io};
     if (gret_status e = conv_check(a)) return e;
     if (!conv_apart(a, tail0)) return GRET_ERR_INVALID_ARG;
-    return done(launch_short_conv(a, cu_stream(stream)));
+    int sms = 0;
+    if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
+    return done(launch_short_conv(a, sms, cu_stream(stream)));
 }
 
 // --------------------------------------------------------------- selective scan
@@ -275,7 +277,9 @@ gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long
 
 size_t gret_short_conv_backward_workspace_size(int B, int N, int D, int K, gret_dtype io_dtype) {
     if (conv_sizes(uniform(B, N), D, K) || !type_ok(io_dtype)) return 0;
-    return short_conv_backward_ws_bytes(B, N, D, K);
+    int sms = 148;
+    device_info(nullptr, &sms);
+    return short_conv_backward_ws_bytes(B, N, D, K, sms);
 }
 
 gret_status gret_short_conv_backward(const void* x, long long ldx, const float* w, const float* bias,
@@ -288,19 +292,22 @@ gret_status gret_short_conv_backward(const void* x, long long ldx, const float* 
     ConvBackwardArgs g = {};
     g.f = ConvArgs{x, ldx, w, bias, tail0, dx, nullptr, uniform(B, N), D, K, act == GRET_ACT_SWISH, io_dtype};
     if (gret_status e = conv_check(g.f)) return e;
-    const size_t need = short_conv_backward_ws_bytes(B, N, D, K);
+    int sms = 148;
+    const bool device = device_info(nullptr, &sms);
+    const size_t need = short_conv_backward_ws_bytes(B, N, D, K, sms);
     if (!workspace_ok(workspace, workspace_bytes, need)) return GRET_ERR_INVALID_ARG;
     if (!apart({conv_rows(g.f, dx, D), {dw, floats(D, K)}, {dbias, floats(D)}, conv_tail(g.f, dtail0), {workspace, need}},
                {conv_rows(g.f, x, ldx), {w, floats(D, K)}, {bias, floats(D)}, conv_tail(g.f, tail0),
                 conv_rows(g.f, dy, D), conv_tail(g.f, dtail)}))
         return GRET_ERR_INVALID_ARG;
+    if (!device) return GRET_ERR_CUDA;
     g.dy = dy; g.dtail = dtail; g.dx = dx; g.dtail0 = dtail0; g.dw = dw; g.dbias = dbias; g.workspace = workspace;
-    return done(launch_short_conv_backward(g, cu_stream(stream)));
+    return done(launch_short_conv_backward(g, sms, cu_stream(stream)));
 }
 
 size_t gret_selective_scan_backward_workspace_size(int B, int N, int D, int n, gret_dtype io_dtype) {
     if (scan_sizes(uniform(B, N), false, D, n) || !type_ok(io_dtype)) return 0;
-    return selective_backward_ws_bytes(B, N, D, n, io_dtype);
+    return selective_backward_ws_bytes(B, N, D, n);
 }
 
 gret_status gret_selective_scan_backward(const void* u, long long ldu, const void* dt, long long lddt, const float* A,
@@ -316,7 +323,7 @@ gret_status gret_selective_scan_backward(const void* u, long long ldu, const voi
     g.f = ScanArgs{u, dt, Bm, Cm, z, ldu, lddt, ldb, ldc, ldz, A, skip, dt_bias, h0, du, nullptr,
                    uniform(B, N), D, n, io_dtype, nullptr};
     if (gret_status e = scan_check(g.f)) return e;
-    const size_t need = selective_backward_ws_bytes(B, N, D, n, io_dtype);
+    const size_t need = selective_backward_ws_bytes(B, N, D, n);
     if (!workspace_ok(workspace, workspace_bytes, need)) return GRET_ERR_INVALID_ARG;
     const ScanArgs& f = g.f;
     if (!apart({scan_rows(f, du, D, D), scan_rows(f, ddt, D, D), scan_rows(f, z ? dz : nullptr, D, D),
@@ -326,11 +333,9 @@ gret_status gret_selective_scan_backward(const void* u, long long ldu, const voi
                 scan_rows(f, Cm, ldc, n), {A, floats(D, n)}, {skip, floats(D)}, {dt_bias, floats(D)}, scan_state(f, h0),
                 scan_rows(f, dout, D, D), scan_state(f, dh_final)}))
         return GRET_ERR_INVALID_ARG;
-    int sms = 0;
-    if (!device_info(nullptr, &sms)) return GRET_ERR_CUDA;
     g.dout = dout; g.dh_final = dh_final; g.du = du; g.ddt = ddt; g.dBm = dBm; g.dCm = dCm; g.dz = dz;
     g.dA = dA; g.dskip = dskip; g.ddt_bias = ddt_bias; g.dh0 = dh0; g.workspace = workspace;
-    return done(launch_selective_backward(g, sms, cu_stream(stream)));
+    return done(launch_selective_backward(g, cu_stream(stream)));
 }
 
 size_t gret_residual_norm_backward_workspace_size(long long T, int D) {

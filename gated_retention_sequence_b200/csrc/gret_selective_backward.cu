@@ -553,9 +553,9 @@ cudaError_t backward(ScanBackwardArgs g, cudaStream_t s) {
 
 }  // namespace
 
-size_t selective_backward_ws_bytes(int B, int N, int D, int n, gret_dtype) { return parts_of(B, N, D, n).all; }
+size_t selective_backward_ws_bytes(int B, int N, int D, int n) { return parts_of(B, N, D, n).all; }
 
-cudaError_t launch_selective_backward(ScanBackwardArgs g, int, cudaStream_t s) {
+cudaError_t launch_selective_backward(const ScanBackwardArgs& g, cudaStream_t s) {
     const bool bf = g.f.io == GRET_BF16;
     switch (g.f.n) {
         case 8: return bf ? backward<__nv_bfloat16, 8>(g, s) : backward<float, 8>(g, s);

@@ -56,9 +56,9 @@ __device__ __forceinline__ void store4(float* p, const float2* v) {
 
 // Tokens of a slot: `most`, or fewer where that leaves the GPU without threads
 // (some 1024 per SM), down to 16.
-int slot_tokens(int most, long long tokens, int D) {
+int slot_tokens(int most, long long tokens, int D, int num_sms) {
     int seg = most;
-    while (seg > 16 && tokens / seg * (D / kC) < 148 * 1024) seg /= 2;
+    while (seg > 16 && tokens / seg * (D / kC) < num_sms * 1024LL) seg /= 2;
     return seg;
 }
 
@@ -335,8 +335,7 @@ __global__ void __launch_bounds__(kBackGroups* kBackSlots, 4) short_conv_backwar
 static_assert(kBackGroups * kC == kBackGroups * kBackSlots, "a thread of the block for each of its channels");
 
 template <typename T, int K>
-cudaError_t conv_backward(ConvBackwardArgs g, cudaStream_t s) {
-    g.f.rows.seg = slot_tokens(kBackSeg, (long long)g.f.rows.B * g.f.rows.N, g.f.D);
+cudaError_t conv_backward(const ConvBackwardArgs& g, cudaStream_t s) {
     const long long slots = slots_of(g.f.rows);
     const int D = g.f.D;
     const dim3 grid((unsigned)((slots + kBackSlots - 1) / kBackSlots), (D + kBackGroups * kC - 1) / (kBackGroups * kC));
@@ -371,8 +370,8 @@ cudaError_t conv_step(const ConvArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_short_conv(ConvArgs a, cudaStream_t s) {
-    a.rows.seg = slot_tokens(kSeg, a.rows.cu ? a.rows.total : (long long)a.rows.B * a.rows.N, a.D);
+cudaError_t launch_short_conv(ConvArgs a, int num_sms, cudaStream_t s) {
+    a.rows.seg = slot_tokens(kSeg, a.rows.cu ? a.rows.total : (long long)a.rows.B * a.rows.N, a.D, num_sms);
     if (a.io == GRET_BF16) {
         if (a.K == 2) return conv<__nv_bfloat16, 2>(a, s);
         return a.K == 3 ? conv<__nv_bfloat16, 3>(a, s) : conv<__nv_bfloat16, 4>(a, s);
@@ -390,14 +389,15 @@ cudaError_t launch_short_conv_step(const ConvArgs& a, cudaStream_t s) {
     return a.K == 3 ? conv_step<float, 3>(a, s) : conv_step<float, 4>(a, s);
 }
 
-size_t short_conv_backward_ws_bytes(int B, int N, int D, int K) {
-    const int seg = slot_tokens(kBackSeg, (long long)B * N, D);
+size_t short_conv_backward_ws_bytes(int B, int N, int D, int K, int num_sms) {
+    const int seg = slot_tokens(kBackSeg, (long long)B * N, D, num_sms);
     const long long slots = (long long)B * segments_of(N, seg);
     return align256((size_t)((slots + kBackSlots - 1) / kBackSlots) * (K + 1) * D * sizeof(float));
 }
 
-cudaError_t launch_short_conv_backward(ConvBackwardArgs g, cudaStream_t s) {
+cudaError_t launch_short_conv_backward(ConvBackwardArgs g, int num_sms, cudaStream_t s) {
     const int K = g.f.K;
+    g.f.rows.seg = slot_tokens(kBackSeg, (long long)g.f.rows.B * g.f.rows.N, g.f.D, num_sms);
     if (g.f.io == GRET_BF16) {
         if (K == 2) return conv_backward<__nv_bfloat16, 2>(g, s);
         return K == 3 ? conv_backward<__nv_bfloat16, 3>(g, s) : conv_backward<__nv_bfloat16, 4>(g, s);
