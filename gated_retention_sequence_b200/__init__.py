@@ -1,8 +1,10 @@
 """Gated-retention (gRet) mixer on NVIDIA B200: Python face of libgret.
 
 The mixer ("YOCO 深度技术分析", section 2.2; chunkwise form, section 5.3.2)
-runs entirely in the CUDA library ``libgret.so`` built from ``csrc/``; this
-package only marshals arguments (see ``gret.py``).
+runs entirely in the CUDA library ``libgret.so`` built from ``csrc/``, and so do
+the operators of the selective state space block next to it (short convolution,
+selective scan, residual norm); this package only marshals arguments (see
+``gret.py`` and ``block.py``).
 """
 from .gret import (  # noqa: F401
     Dtype, Epilogue, GretError, LIB_PATH, Path, SIGNATURES, Status, check_device_status, decode_step,

@@ -23,11 +23,16 @@
 // A sequence of one segment is walked alone, from h0 and dh_final.
 //
 // Three exponentials per state and token, all of them parallel over the tokens.
-// 4 x 4096 tokens x 2048 channels x 16 states, bf16: 962 us, of them ends 200,
-// fold 55, walk 670, join 36.  The walk issues 217 instructions
-// per token and 16 channels (59 % of the issue slots, 67 % of the shared memory's
-// cycles); more blocks an SM, at 128 registers and 28 tokens a segment, took
-// 1063 us, and blocks of two, three or eight warps 1015 to 1155.
+// 4 x 4096 tokens x 2048 channels x 16 states, bf16: 958 us, of them ends 200,
+// fold 55, walk 670, join 36.  The walk issues 217 instructions per token and 16
+// channels; no unit is full (60 % of the issue slots, 67 % of the shared memory's
+// cycles), as 12 warps an SM hide too little; more blocks an SM, at 128 registers
+// and 28 tokens a segment, took 1063 us, and blocks of two, three or eight warps
+// 1015 to 1155.  With 8, 32, 64 states it takes 650, 1866, 4556 us (in fp32 828,
+// 2034, 4806; 1062 with 16): at 64 states a segment is 16 tokens, whose states,
+// gradients and shares alone are 2.2 GB written and read, and 8 warps fit an SM.
+// The workspace, for 4 x 4096 tokens x 4096 channels and 8, 16, 32, 64 states, is
+// 0.26, 0.56, 1.4 and 4.4 GB.
 #include "gret_selective.cuh"
 
 namespace gret {

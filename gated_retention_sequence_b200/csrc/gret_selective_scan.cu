@@ -8,8 +8,8 @@
 // B and C are shared by all channels of a token.  One exponential per token,
 // channel and state is all but unavoidable, as A is any matrix, and bounds the
 // time: at 16 a clock and SM they take 239 us for 16384 tokens x 4096 channels x
-// 16 states, whose bytes take 87.  38 packed sequences of that size take 398 us,
-// with the special function unit three quarters busy; evaluating a quarter of
+// 16 states, whose bytes take 87.  38 packed sequences of that size take 398 us
+// (564 in fp32), with the special function unit 72 % busy; evaluating a quarter of
 // the powers by a polynomial instead made it slower (379 -> 408 us at 64 x 256 x
 // 4096), as the instructions then bound it.  The shared memory's data path comes
 // next, hence two channels a lane that share their B and C, and those in their
@@ -276,9 +276,13 @@ __device__ __forceinline__ void walk(const ScanArgs& a, const Slot& f, int block
 // first, so that the launch does not end on long ones.  All 32 lanes call it
 // together and go over the offsets 32 at a time.  More than kSorted sequences
 // leave their rests in the order of the batch, and more than kRanked take
-// find_slot's order, as the search itself would cost too much.  38 whole
-// sequences of 16384 tokens x 4096 channels: 398 us (412 before B and C were
-// staged in their own type, and 543 in the batch's order then).
+// find_slot's order, as the search itself would cost too much.  In us, at 16384
+// tokens x 4096 channels x 16 states: 64 sequences with the rests by length 414, in
+// the batch's order 660; 128 sequences 613 and 508 (the search grows with the square
+// of their number).  Whole segments first against find_slot's order: 65 sequences
+// 515 and 555, 128 sequences 508 and 499, 256 sequences 511 and 461, 512 sequences
+// 748 and 532; at 512 channels, where the batch is cut, 256 sequences take 121 and
+// 109.  The two cross between 65 and 128 sequences, below the border.
 constexpr int kRanked = 256, kSorted = 64;
 __device__ __forceinline__ Slot find_ranked(const Rows& r, int rank) {
     if (!r.cu || r.B > kRanked) return find_slot(r, rank);
@@ -447,7 +451,7 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 // One token per sequence: the states are read and written once, 16 bytes at a
 // time, n / 4 lanes to a channel, and the memory bandwidth bounds the time.  A
 // thread takes its states of kStepSeqs sequences, whose loads are all in flight
-// together and which share A: 25 us, 5.6 TB/s, at 256 sequences x 4096 channels x
+// together and which share A: 27 us, 5.2 TB/s, at 256 sequences x 4096 channels x
 // 16 states (one sequence a thread 39 us).  h may be h0.
 constexpr int kStepSeqs = 4;
 template <typename T, int NS>

@@ -204,8 +204,10 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const ConvArg
 //   dw[k]   = sum_t ds[t] x[t-K+1+k],  dbias = sum_t ds[t]
 // and dtail adds to the last K-1 rows.  A thread walks one slot and K-1 tokens
 // past its end; the slots of a block add up their dw and dbias in shared memory.
-// Issue slots bound it: 109 us at 16384 x 4096, bf16 (150 us with a condition
-// per row for the slot's ends).
+// 109 us at 16384 x 4096, bf16 (150 us with a condition per row for the slot's
+// ends).  No unit is full (59 % of the issue slots, 33 % of the special functions,
+// 0.58 of the copy rate): at 128 registers 16 warps an SM hide too little of each
+// row's chain from copy to sum.  fp32, with twice the bytes, takes 157 us.
 constexpr int kBackGroups = 32, kBackSlots = 4, kBackSeg = 128, kBackBatch = 4, kBackAhead = 1;
 
 template <typename T, int K>

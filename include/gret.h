@@ -465,7 +465,9 @@ gret_status gret_residual_norm(const void* x, long long ldx, const void* y, long
  * fp32, summed over all rows in a fixed order, so that a call gives the same
  * bits every time.  Workspaces are 256-byte aligned, of the size that the
  * function next to the call gives (0 for refused arguments); calls that share
- * one must not overlap.  Uniform batches only.
+ * one must not overlap.  The scan's is large: states and sums for each 32 tokens
+ * (16 with n 64), 0.56 GB for 16384 tokens, 4096 channels and n 16, 4.4 GB with
+ * n 64.  Uniform batches only.
  *
  * gret_short_conv_backward -- of <y, dy> + <tail, dtail>: dx, and where wanted
  * (not NULL) dw [D][K], dbias [D], dtail0 [B][K-1][D].  dy [B][N][D]; dtail
