@@ -926,3 +926,97 @@ def test_conv_backward_segments_of_128_tokens(io, K):
 @pytest.mark.parametrize("T,D", [(2672, 2048), (1337, 2056), (1337, 4096), (745, 4104), (745, 8192)])
 def test_norm_blocks_with_many_rows(io, stream, T, D):
     check_norm(io, stream, T, D)
+
+
+# ------------------------------------------------------------------ large batches
+def sample(p, rows, seqs, keep):
+    """Some rows, sequences and channels of a scan's inputs."""
+    q = {k: v[rows] if k in ROWS else v for k, v in p.items()}
+    q["h0"] = None if q["h0"] is None else q["h0"][seqs]
+    at = {"A": 0, "h0": 0}
+    return {k: v if k in ("B", "C") or v is None else v[..., keep, :] if k in at else v[..., keep] for k, v in q.items()}
+
+
+def random_scan(io, rows, D, n, seqs):
+    """Inputs drawn on the GPU, for sizes that the host would take long for."""
+    gen = torch.Generator("cuda").manual_seed(5)
+    normal = lambda *s, to="f32": torch.randn(s, generator=gen, device="cuda", dtype=TYPES[to])  # noqa: E731
+    return dict(u=normal(rows, D, to=io), dt=normal(rows, D, to=io), A=-torch.exp(normal(D, n)), B=normal(rows, n, to=io),
+                C=normal(rows, n, to=io), skip=normal(D), z=normal(rows, D, to=io), dt_bias=normal(D) - 3,
+                h0=normal(seqs, D, n)), normal
+
+
+def check_large(io, B, N, D, n, keep, seqs):
+    """All calls at a size of many rows, at some sequences and channels."""
+    p, normal = random_scan(io, B * N, D, n, B)
+    do = normal(B, N, D, to=io)
+    o, h = scan_call(p, B, N)
+    g = scan_backward_call(p, do, B, N)
+    w, bias = normal(D, 4), normal(D)
+    y, tail = gret.short_conv(p["u"].view(B, N, D), w, bias)
+    c = gret.short_conv_backward(p["u"].view(B, N, D), w, bias, do)
+    norm = dict(x=p["u"], y=p["dt"], gate=p["z"], scale=normal(D), w_post=normal(D), w_next=normal(D))
+    r, v = gret.residual_norm(**norm)
+    m = gret.residual_norm_backward(**norm, dr=do.view(B * N, D), dn=do.view(B * N, D))
+    for b in seqs:
+        rows = slice(b * N, (b + 1) * N)
+        q, up = sample(p, rows, b, keep), do[b][:, keep]
+        ro, rh = bo.selective_scan(**q)
+        bo.check(o[b][:, keep], ro, io, f"o of sequence {b}")
+        bo.check(h[b][keep], rh, "f32", f"h of sequence {b}")
+        want = bo.selective_scan(**q, do=up)
+        for k in ("du", "ddt", "dz"):
+            bo.check(g[k][b][:, keep], want[k], io, f"{k} of sequence {b}")
+        bo.check(g["dh0"][b][keep], want["dh0"], "f32", f"dh0 of sequence {b}")
+        ry, rt = bo.short_conv(q["u"], w[keep], bias[keep])
+        bo.check(y[b][:, keep], ry, io, f"y of sequence {b}")
+        bo.check(tail[b][:, keep], rt, io, f"tail of sequence {b}")
+        bo.check(c["dx"][b][:, keep], bo.short_conv(q["u"], w[keep], bias[keep], dy=up)["dx"], io, f"dx of sequence {b}")
+        whole = {k: t[rows] if t.dim() == 2 else t for k, t in norm.items()}
+        rr, rn = bo.residual_norm(**whole)
+        bo.check(r[rows], rr, io, f"r of sequence {b}")
+        bo.check(v[rows], rn, io, f"n of sequence {b}")
+        want = bo.residual_norm(**whole, dr=do[b], dn=do[b])
+        for k in ("dx", "dy", "dgate"):
+            bo.check(m[k][rows], want[k], io, f"norm's {k} of sequence {b}")
+
+
+def test_outputs_past_31_bits():
+    """Dense tensors of more than 2^31 entries, each side of that and at the end."""
+    B, N, D = 5300, 100, 4096
+    cross = 2 ** 31 // (N * D)
+    assert B * N * D > 2 ** 31
+    check_large("bf16", B, N, D, 16, [0, 31, 2047, 4095], [0, cross, B - 1])
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 2, 40])
+def test_more_sequences_than_a_grids_second_dimension(io, N):
+    B = 70001
+    check_large(io, B, N, 16, 8, list(range(16)), [0, 1, 65535, 65536, B - 1])
+    p, normal = random_scan(io, B, 16, 8, B)
+    h0, p["h0"] = p["h0"], None
+    lens = torch.arange(B, device="cuda") % 3
+    lens[-1] += B - lens.sum()                   # the last sequence takes the rows that are left
+    cu = torch.cat([lens.new_zeros(1), lens.cumsum(0)]).to(torch.int32)
+    longest, x = int(lens.max()), p["u"]
+    o, h = gret.selective_scan_varlen(**dict(p, h0=h0), cu_seqlens=cu, max_seqlen=longest)
+    w, tail = normal(16, 4), normal(B, 3, 16, to=io)
+    y, t = gret.short_conv_varlen(x, w, None, cu, longest, tail0=tail)
+    q = {k: v for k, v in p.items() if k != "h0"}
+    o1, h1 = gret.selective_step(**q, h=h0, h_out=torch.empty_like(h0))
+    y1, t1 = gret.short_conv_step(x, w, None, tail, tail_out=torch.empty_like(tail))
+    for b in (0, 1, 2, 65534, 65535, 65536, B - 2):
+        at, end = int(cu[b]), int(cu[b + 1])
+        ro, rh = bo.selective_scan(**scan_rows(dict(p, h0=h0), at, end, b)) if end > at else (None, bo.f64(h0[b]))
+        if end > at:
+            bo.check(o[at:end], ro, io, f"o of packed sequence {b}")
+            bo.check(y[at:end], bo.short_conv(x[at:end], w, None, tail[b])[0], io, f"y of packed sequence {b}")
+        bo.check(h[b], rh, "f32", f"h of packed sequence {b}")
+        ro, rh = bo.selective_scan(**scan_rows(dict(p, h0=h0), b, b + 1, b))
+        bo.check(o1[b:b + 1], ro, io)
+        bo.check(h1[b], rh, "f32")
+        ry, rt = bo.short_conv(x[b:b + 1], w, None, tail[b])
+        bo.check(y1[b:b + 1], ry, io)
+        assert (t1[b].double().cpu().numpy() == rt.v).all()
