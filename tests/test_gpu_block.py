@@ -1020,3 +1020,82 @@ def test_more_sequences_than_a_grids_second_dimension(io, N):
         ry, rt = bo.short_conv(x[b:b + 1], w, None, tail[b])
         bo.check(y1[b:b + 1], ry, io)
         assert (t1[b].double().cpu().numpy() == rt.v).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("N,at", [(61, 22), (1203, 700)])
+def test_a_value_that_is_no_number_stays_in_its_channel_and_behind_its_token(io, n, N, at):
+    """Whole and cut sequences: what comes before the token, and every other channel, keeps its bits."""
+    B, D, bad = 2, 40, 13
+    p = scan_inputs(io, B * N, D, n, B)
+    others = [d for d in range(D) if d != bad]
+    do = draw(10, (B, N, D), io)
+    o, h = scan_call(p, B, N)
+    g = scan_backward_call(p, do, B, N)
+    c = conv_inputs(io, B * N, D, 4, B)
+    x = c["x"].view(B, N, D)
+    y, tail = gret.short_conv(x, c["w"], c["bias"], tail0=c["tail0"])
+    dx = gret.short_conv_backward(x, c["w"], c["bias"], do, tail0=c["tail0"])
+    for k in ("u", "dt", "z", "do"):
+        for value in (float("nan"), float("inf")):
+            up = do.clone()
+            q = dict(p, **{k: p[k].clone()}) if k != "do" else p
+            (up if k == "do" else q[k].view(B, N, D))[1, at, bad] = value
+            o2, h2 = scan_call(q, B, N)
+            g2 = scan_backward_call(q, up, B, N)
+            assert torch.equal(o2[0], o[0]) and torch.equal(o2[1, :at], o[1, :at]) and torch.equal(h2[0], h[0]), (k, value)
+            assert torch.equal(o2[..., others], o[..., others]) and torch.equal(h2[:, others], h[:, others]), (k, value)
+            for w in ("du", "ddt", "dz"):
+                assert torch.equal(g2[w][0], g[w][0]) and torch.equal(g2[w][..., others], g[w][..., others]), (k, w, value)
+            for w in ("dA", "dskip", "ddt_bias"):
+                assert torch.equal(g2[w][others], g[w][others]), (k, w, value)
+            # a gradient goes back no further than to the tokens it comes from
+            assert k != "do" or all(torch.equal(g2[w][1, at + 1:], g[w][1, at + 1:]) for w in ("du", "ddt", "dz")), value
+    for value in (float("nan"), float("inf")):
+        x2 = x.clone()
+        x2[1, at, bad] = value
+        y2, t2 = gret.short_conv(x2, c["w"], c["bias"], tail0=c["tail0"])
+        assert torch.equal(y2[0], y[0]) and torch.equal(y2[1, :at], y[1, :at]) and torch.equal(y2[1, at + 4:], y[1, at + 4:])
+        assert torch.equal(y2[..., others], y[..., others]) and torch.equal(t2, tail)
+        dx2 = gret.short_conv_backward(x2, c["w"], c["bias"], do, tail0=c["tail0"])
+        assert torch.equal(dx2["dx"][..., others], dx["dx"][..., others]) and torch.equal(dx2["dx"][0], dx["dx"][0])
+        assert torch.equal(dx2["dx"][1, :at - 3], dx["dx"][1, :at - 3])
+        assert torch.equal(dx2["dx"][1, at + 4:], dx["dx"][1, at + 4:])
+        assert torch.equal(dx2["dw"][others], dx["dw"][others]) and torch.equal(dx2["dbias"][others], dx["dbias"][others])
+
+
+@pytest.mark.parametrize("io,stream", KINDS)
+def test_a_row_that_is_no_number_stays_in_its_row(io, stream):
+    T, D, bad = 3000, 264, 1444
+    p = norm_inputs(io, stream, T, D)
+    dr, dn = draw(8, (T, D), stream), draw(9, (T, D), io)
+    r, n = gret.residual_norm(**p)
+    g = gret.residual_norm_backward(**p, dr=dr, dn=dn)
+    rest = [t for t in range(T) if t != bad]
+    for k in ("x", "y", "gate"):
+        for value in (float("nan"), float("inf")):
+            q = dict(p, **{k: p[k].clone()})
+            q[k][bad, 77] = value
+            r2, n2 = gret.residual_norm(**q)
+            g2 = gret.residual_norm_backward(**q, dr=dr, dn=dn)
+            gret.check_device_status()
+            for a, b in [(r, r2), (n, n2)] + [(g[w], g2[w]) for w in ("dx", "dy", "dgate")]:
+                assert torch.equal(a[rest], b[rest]), (k, value)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+def test_scan_of_states_that_grow(io, n):
+    """A positive A, by less over the whole sequence than fp32 holds: cut sequences and their gradients."""
+    B, N, D = 2, 1203, 24
+    p = scan_inputs(io, B * N, D, n, B)
+    p["A"] = p["A"].abs().clamp(max=2.0) * 0.02
+    o, h = scan_call(p, B, N)
+    do, dh = draw(10, (B, N, D), io), draw(11, (B, D, n))
+    g = scan_backward_call(p, do, B, N, dh_final=dh)
+    for b in range(B):
+        ro, rh = bo.selective_scan(**scan_rows(p, b * N, (b + 1) * N, b))
+        bo.check(o[b], ro, io, f"o of sequence {b}")
+        bo.check(h[b], rh, "f32", f"h of sequence {b}")
+    check_scan_backward(io, p, do, dh, g, B, N)
